@@ -32,7 +32,8 @@
  *     PN_WINDOW_ADVANCING, one window of W steps that slides past its
  *     converged prefix (below).
  *
- * Memory conventions (all functions):
+ * Memory conventions (the solver and scan entries; the sequence-layer
+ * operators state theirs where they are declared):
  *   - float pointers named params, x, s0, out, A, b are DEVICE pointers to
  *     C-contiguous float32 arrays owned by the caller; the library never
  *     frees them.
@@ -293,6 +294,144 @@ int pn_affine_scan(const float* A, const float* b, const float* s0, int64_t B, i
 /* Workspace bytes for pn_affine_scan. */
 size_t pn_affine_scan_workspace_bytes(int64_t B, int64_t T, int64_t D, int32_t dense,
                                       const pn_opts* opts);
+
+/* ------------------------------------------------------------------------
+ * Sequence-layer operators: the linear recurrence with a matrix state
+ * (linear attention with a decay per head), and what prepares its queries
+ * and keys (rotation by position, norm per head).
+ *
+ * Conventions of this part:
+ *   - every field of the argument blocks is 8 bytes wide (a double, an
+ *     int64_t or a pointer); pointers are DEVICE pointers unless named host;
+ *   - token tensors are [B, T, heads, channels] in one storage type (PN_F32,
+ *     PN_BF16, PN_F16), channels adjacent, the other strides free and given
+ *     in elements (0 broadcasts an input); outputs are C-contiguous;
+ *   - states are C-contiguous float32 [B, H, dk, dv]; all arithmetic, sums
+ *     and states are at least float32, one rounding at the end;
+ *   - calls ENQUEUE their kernels on `stream` (hipStream_t, NULL = the null
+ *     stream) and return without waiting, so they can be captured into a
+ *     graph; nothing is allocated: a workspace is given by the caller,
+ *     256-byte aligned (PN_EWORKSPACE otherwise), and is free for reuse by
+ *     later work of the same stream;
+ *   - sizes, strides, pointers and overlaps are checked on the host before
+ *     any launch (PN_EINVAL, PN_EUNSUPPORTED); a size of 0 is an empty
+ *     problem (PN_OK; what has elements left is still written, as a state);
+ *   - indices held in device memory (positions, lengths, slots) are bounded
+ *     in the kernels as each entry states: no value of theirs reads or
+ *     writes outside the arrays given. */
+enum { PN_F32 = 0, PN_BF16 = 1, PN_F16 = 2 };
+
+/* A token tensor [B, T, heads, channels]: strides in elements. */
+typedef struct pn_tokens {
+    void* p;
+    int64_t sb, st, sh;
+} pn_tokens;
+
+/* table[p][i] = magnitude * (cos, sin)(p * freq[i]), computed in float64 and
+ * rounded once: float32 [n_pos, n_freq, 2].  freq is a HOST array of n_freq
+ * (1 .. 128) float64 angles per position. */
+int pn_rotary_table(const double* freq_host, int64_t n_freq, int64_t n_pos, double magnitude,
+                    float* table, void* stream);
+
+/* Arguments of pn_rotary, pn_qk_norm_rotary and its backward.
+ * Rotation: of the first R (even, 0 <= R <= D) of D (1 .. 256) channels,
+ * channel pairs (i, i + R/2), or (2i, 2i + 1) if interleaved, turn by the
+ * angle of table row p: (a, b) -> (a c - b s, b c + a s); the other channels
+ * pass.  p = positions[b * pos_sb + t * pos_st] (int32, or int64 if pos64),
+ * or offset + t if positions is NULL; a p outside [0, n_pos) gives NaN in the
+ * rotated channels. */
+typedef struct pn_rotary_args {
+    int64_t dtype, B, T, D, R, interleaved;
+    int64_t inverse;            /* pn_rotary: 1 turns back (the gradient)       */
+    int64_t hq, hk;             /* heads of q and k; hk = 0: no k                */
+    pn_tokens q, k;             /* inputs                                       */
+    void *q_out, *k_out;        /* contiguous [B, T, hq | hk, D]                 */
+    const float* table;         /* [n_pos, R/2, 2]                              */
+    int64_t n_pos;
+    const void* positions;
+    int64_t pos64, pos_sb, pos_st, offset;
+    double eps;                 /* norm entries: x / sqrt(mean x^2 + eps)        */
+    const float *qw, *kw;       /* norm weights, float32 [D] or [heads, D]; NULL = 1 */
+    int64_t qw_sh, kw_sh;       /* 0: one [D] for all heads, D: one per head      */
+    pn_tokens dq, dk;           /* backward: gradients of q_out and k_out         */
+    float *dqw, *dkw;           /* backward: gradients of the weights, shaped as
+                                   they are (written where qw / kw is given)     */
+    void* workspace;
+    int64_t workspace_bytes;
+    void* stream;
+} pn_rotary_args;
+
+/* Rotation alone, of q and (hk > 0) k.  q_out may be q itself (in place, if
+ * q is contiguous), likewise k_out; other overlaps are PN_EINVAL. */
+int pn_rotary(const pn_rotary_args* a);
+/* Norm of each head's channels, times its weight, then the rotation, in one
+ * pass.  In place as above. */
+int pn_qk_norm_rotary(const pn_rotary_args* a);
+/* Gradients: dq, dk come in (of the outputs), q_out and k_out receive the
+ * gradients of q and k, dqw and dkw those of the weights (sums in a fixed
+ * order: the same bits on every run).  No output may overlap an input. */
+int pn_qk_norm_rotary_backward(const pn_rotary_args* a);
+/* Workspace bytes of pn_qk_norm_rotary_backward (the other two need none);
+ * 0 with the error set for invalid arguments.  Pointers are not looked at. */
+size_t pn_qk_norm_rotary_workspace_bytes(const pn_rotary_args* a);
+
+/* Linear attention with a decay per head.  For each sequence and head,
+ *     S_t = lam S_{t-1} + k_t^T v_t,   o_t = scale * q_t S_t,
+ * lam = exp(log_decay[h]) (log_decay <= 0 in use; -inf, a state that holds
+ * the current token only, and growth are allowed), S_0 = initial_state or 0.
+ * q has H heads; k and v have HK heads, H a multiple of HK: head h uses key
+ * and value head h / (H / HK).  1 <= dk, dv <= 256.
+ * lengths (int32 [B], NULL = T each; values are clamped to [0, T]): tokens at
+ * and after lengths[b] are padding: never read, their rows of the outputs 0,
+ * and final_state is the state after lengths[b] tokens.  A NaN or infinity
+ * in a token reaches the outputs from that token on, and may reach those of
+ * the up to 63 tokens before it. */
+typedef struct pn_linattn_args {
+    int64_t dtype, B, T, H, HK, dk, dv;
+    double scale;
+    const float* log_decay;     /* [H]                                          */
+    const int32_t* lengths;     /* [B] or NULL                                  */
+    pn_tokens q, k, v;
+    const float* initial_state; /* [B, H, dk, dv] or NULL (zeros)                */
+    void* o;                    /* forward: [B, T, H, dv]                        */
+    float* final_state;         /* forward: [B, H, dk, dv] or NULL               */
+    pn_tokens do_;              /* backward: gradient of o                       */
+    const float* d_final_state; /* backward: gradient of final_state, or NULL    */
+    void *dq, *dk_, *dv_;       /* backward: [B, T, H, dk], [B, T, HK, dk | dv]   */
+    float* d_initial_state;     /* backward: [B, H, dk, dv] or NULL              */
+    void* workspace;
+    int64_t workspace_bytes;
+    void* stream;
+} pn_linattn_args;
+
+/* All T tokens of every sequence (prompts, training). */
+int pn_linear_attention(const pn_linattn_args* a);
+/* Gradients of q, k, v (summed over the heads that share them) and of the
+ * initial state; the decay is a constant of the layer. */
+int pn_linear_attention_backward(const pn_linattn_args* a);
+/* Workspace bytes of the two; 0 with the error set for invalid arguments.
+ * Pointers are not looked at, except for NULL. */
+size_t pn_linear_attention_workspace_bytes(const pn_linattn_args* a, int32_t backward);
+
+/* One token for each of B sequences (serving): the state is updated in place
+ * and o_t returned.  q, k, v: [B, heads, channels] (st is not used).  state
+ * is a pool [n_slots, H, dk, dv]; sequence b owns slot slots[b] (int32), or
+ * slot b if slots is NULL (then n_slots >= B).  A slot outside [0, n_slots)
+ * marks an idle row: o is 0 there and no state is touched.  Two rows of one
+ * call must not name the same slot. */
+typedef struct pn_linattn_step_args {
+    int64_t dtype, B, H, HK, dk, dv;
+    double scale;
+    const float* log_decay;     /* [H]                                          */
+    pn_tokens q, k, v;
+    float* state;
+    const int32_t* slots;       /* [B] or NULL                                  */
+    int64_t n_slots;
+    void* o;                    /* [B, H, dv]                                   */
+    void* stream;
+} pn_linattn_step_args;
+
+int pn_linear_attention_step(const pn_linattn_step_args* a);
 
 /* Message of the last error on this thread ("" if none).  The pointer stays
  * valid until the next library call on the same thread. */

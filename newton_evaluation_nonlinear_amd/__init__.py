@@ -7,6 +7,9 @@ there is no fallback of any kind.
 
     out, iters, status = pn.eval(cell, params, x, s0, mode=pn.QUASI_NEWTON, tol=1e-5)
 
+The sequence-layer operators (rotary positions, norm + rotation, linear
+attention with a decay per head) are in ``sequence.py``.
+
 The method, the stop rule and all layouts are documented in include/pn.h.
 """
 
@@ -14,6 +17,10 @@ import ctypes
 import os
 
 import torch
+
+from . import sequence
+from .sequence import (linear_attention, linear_attention_backward, linear_attention_step, qk_norm_rotary,
+                       qk_norm_rotary_backward, rotary, rotary_frequencies, rotary_table)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpn.so")
@@ -27,7 +34,7 @@ WINDOW_CONSECUTIVE, WINDOW_ADVANCING = 0, 1
 
 EXPORTED = ("pn_opts_init", "pn_eval", "pn_eval_ex", "pn_eval_f16", "pn_eval_noalloc",
             "pn_workspace_bytes", "pn_affine_scan", "pn_affine_scan_workspace_bytes", "pn_last_error",
-            "pn_version")
+            "pn_version") + sequence.EXPORTED
 
 
 class PnError(RuntimeError):
@@ -99,6 +106,7 @@ def lib():
         L.pn_last_error.restype = ctypes.c_char_p
         L.pn_version.argtypes = []
         L.pn_version.restype = ctypes.c_char_p
+        sequence.declare(L)
         _lib = L
     return _lib
 

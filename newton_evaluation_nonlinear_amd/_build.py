@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libpn.so")
 CEILING_LIB = os.path.join(HERE, "libpn_ceiling.so")
 CEILING_SOURCES = ["pn_ceiling.hip"]
 
-SOURCES = ["pn_api.cpp", "pn_diag.hip", "pn_cell.hip", "pn_dense.hip", "pn_scan.hip", "pn_static.hip", "pn_small.hip"]
+SOURCES = ["pn_api.cpp", "pn_diag.hip", "pn_cell.hip", "pn_dense.hip", "pn_scan.hip", "pn_static.hip", "pn_small.hip",
+           "pn_seq_api.cpp", "pn_rotary.hip", "pn_linattn.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -45,6 +45,15 @@ int fail(int code, const char* fmt, ...) {
     return code;
 }
 
+}  // namespace
+
+namespace pn {
+int set_error(int code, const char* msg) { return fail(code, "%s", msg); }
+void clear_error() { g_err.clear(); }
+}  // namespace pn
+
+namespace {
+
 #define PN_HIP(call)                                                                    \
     do {                                                                                \
         hipError_t e_ = (call);                                                         \
