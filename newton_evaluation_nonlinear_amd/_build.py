@@ -22,7 +22,8 @@ CEILING_LIB = os.path.join(HERE, "libpn_ceiling.so")
 CEILING_SOURCES = ["pn_ceiling.hip"]
 
 SOURCES = ["pn_api.cpp", "pn_diag.hip", "pn_cell.hip", "pn_dense.hip", "pn_scan.hip", "pn_static.hip", "pn_small.hip",
-           "pn_seq_api.cpp", "pn_rotary.hip", "pn_linattn.hip"]
+           "pn_seq_api.cpp", "pn_rotary.hip", "pn_linattn.hip", "pn_linattn_bf16.hip",
+           "pn_linattn_f16.hip", "pn_linattn_f32.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -1,4 +1,6 @@
-// Linear attention with a decay per head.
+// Linear attention with a decay per head: segments of the time axis, the scan
+// over them, and the form for single tokens (the chunk kernels are in
+// pn_linattn_chunk.hpp).
 //
 // The operator, for one sequence and head, over tokens i (LaOp):
 //     S_i = lam S_{i-1} + ws K_i^T V_i,   O_i = inter * Q_i S_i.
@@ -7,87 +9,64 @@
 // so the gradients are the same operator: dq with (Q, K, V) = (do, v, k), and,
 // over reversed time, dv with (k, q, do) and dk with (v, do, q).
 
-#include "pn_seq.hpp"
-#include "pn_seq_device.hpp"
+#include "pn_linattn_chunk.hpp"
 
 namespace pn {
 namespace {
 
 constexpr int kCols = 64;
 
-__device__ __forceinline__ int seq_len(const int32_t* lengths, int b, int T) {
-    if (!lengths) return T;
-    const int n = lengths[b];
-    return n < 0 ? 0 : (n > T ? T : n);
+// The state before each segment from the states the segments leave alone:
+//     S_{n+1} = lam^{tokens of n} S_n + U_n,
+// in place, element by element; slot n holds U_n, then S_{n+1}.
+__global__ __launch_bounds__(256) void la_carry(LaChunkArgs g) {
+    const LaOp& op = g.a.op[blockIdx.y];
+    const int n = op.DK * op.DV;
+    const int64_t total = static_cast<int64_t>(g.a.B) * g.a.H * n;
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (e >= total) return;
+    const int64_t bh = e / n;
+    const int at = static_cast<int>(e - bh * n), row = at / op.DV, col = at - row * op.DV;
+    const int h = static_cast<int>(bh % g.a.H), b = static_cast<int>(bh / g.a.H);
+    const int64_t len = seq_len(g.a.lengths, b, static_cast<int>(g.a.T));
+    const double gl = g.a.log_decay[h];
+    const float whole = static_cast<float>(exp(gl * static_cast<double>(g.seg)));
+    float s = op.s_in ? op.s_in[bh * n + row * op.s_k + col * op.s_v] : 0.0f;
+    float* u = g.carry[blockIdx.y] + e;
+    for (int i = 0; i + 1 < g.n_seg; ++i) {
+        const int64_t left = len - i * g.seg;
+        const float d = left >= g.seg ? whole : (left <= 0 ? 1.0f : static_cast<float>(exp(gl * static_cast<double>(left))));
+        s = d * s + u[i * total];
+        u[i * total] = s;
+    }
 }
 
-// The recurrence as written: a workgroup owns one head's state for 64 columns,
-// each of its 4 waves a quarter of the rows in registers, and walks the tokens.
-template <typename T, int ROWS>
-__global__ __launch_bounds__(256) void la_recurrent(LaArgs a, int which) {
-    const LaOp op = a.op[which];
-    __shared__ float sq[256], sk[256], part[4][kCols];
-    const int tid = threadIdx.x, col = tid % kCols, wv = tid / kCols;
-    const int h = blockIdx.x % a.H, b = blockIdx.x / a.H;
-    const int vv = blockIdx.y * kCols + col;
-    const int N = static_cast<int>(a.T), len = seq_len(a.lengths, b, N);
-    const bool live = vv < op.DV;
-    const float lam = expf(a.log_decay[h]);
-    float S[ROWS];
-    const int64_t sbase = (static_cast<int64_t>(b) * a.H + h) * op.DK * op.DV;
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int r = wv * ROWS + i;
-        S[i] = op.s_in && live && r < op.DK ? op.s_in[sbase + r * op.s_k + vv * op.s_v] : 0.0f;
-    }
-    const T* qp = static_cast<const T*>(op.q.p) + b * op.q.sb + (h / op.q.div) * op.q.sh;
-    const T* kp = static_cast<const T*>(op.k.p) + b * op.k.sb + (h / op.k.div) * op.k.sh;
-    const T* vp = static_cast<const T*>(op.v.p) + b * op.v.sb + (h / op.v.div) * op.v.sh;
-    for (int i = 0; i < N; ++i) {
-        const int64_t t = op.reverse && i < len ? len - 1 - i : i;
-        float o = 0.0f;
-        if (i < len) {
-            __syncthreads();
-            sq[tid] = tid < op.DK ? to_f32(qp[t * op.q.st + tid]) : 0.0f;
-            sk[tid] = tid < op.DK ? to_f32(kp[t * op.k.st + tid]) : 0.0f;
-            const float v = live ? op.ws * to_f32(vp[t * op.v.st + vv]) : 0.0f;
-            __syncthreads();
-            const float before = op.reverse ? 1.0f : lam, after = op.reverse ? lam : 1.0f;
-            float s = 0.0f;
-#pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                const float n = before * S[j] + sk[wv * ROWS + j] * v;
-                s += sq[wv * ROWS + j] * n;
-                S[j] = after * n;
-            }
-            part[wv][col] = s;
-            __syncthreads();
-            o = op.inter * (part[0][col] + part[1][col] + part[2][col] + part[3][col]);
-        }
-        if (wv == 0 && live) {
-            const int64_t at = ((b * a.T + t) * a.H + h) * op.DV + vv;
-            if (op.o_f32) static_cast<float*>(op.o)[at] = o;
-            else static_cast<T*>(op.o)[at] = from_f32<T>(o);
-        }
-    }
-    if (op.s_out && live)
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const int r = wv * ROWS + i;
-            if (r < op.DK) op.s_out[sbase + static_cast<int64_t>(r) * op.DV + vv] = S[i];
-        }
+// Segments of the time axis: one where sequences, heads and columns fill the
+// device, else as many as fill it, of whole chunks.
+constexpr int64_t kFillGroups = 512;
+
+int chunk_tokens(int dtype) { return dtype == PN_BF16 ? Parts<bf16>::C : Parts<float>::C; }
+
+void segments(const LaArgs& a, int64_t* seg, int* n_seg) {
+    int dv = 0;
+    for (int w = 0; w < a.n_ops; ++w) dv = a.op[w].DV > dv ? a.op[w].DV : dv;
+    const int64_t C = chunk_tokens(a.dtype), chunks = (a.T + C - 1) / C, cols = 32 * la_waves(a);
+    const int64_t groups = static_cast<int64_t>(a.B) * a.H * ((dv + cols - 1) / cols) * a.n_ops;
+    int64_t n = (kFillGroups + groups - 1) / groups;
+    if (n > chunks) n = chunks;
+    if (n < 1) n = 1;
+    const int64_t per = chunks > 0 ? (chunks + n - 1) / n : 1;
+    *seg = per * C;
+    *n_seg = chunks > 0 ? static_cast<int>((chunks + per - 1) / per) : 1;
 }
 
-template <typename T>
-hipError_t launch_recurrent(const LaArgs& a, hipStream_t st) {
-    for (int w = 0; w < a.n_ops; ++w) {
-        const dim3 grid(a.B * a.H, (a.op[w].DV + kCols - 1) / kCols);
-        if (a.op[w].DK <= 128) la_recurrent<T, 32><<<grid, 256, 0, st>>>(a, w);
-        else la_recurrent<T, 64><<<grid, 256, 0, st>>>(a, w);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+// An operand that can be read (or the output written) 16 bytes at a time.
+bool wide(const void* p, int64_t sb, int64_t st, int64_t sh, int D, int elem) {
+    return D % 8 == 0 && ((reinterpret_cast<intptr_t>(p) | sb * elem | st * elem | sh * elem) & 15) == 0;
+}
+bool wide(const LaOperand& x, int D, const LaArgs& a) {
+    const int elem = a.dtype == PN_F32 ? 4 : 2;
+    return wide(x.p, a.B > 1 ? x.sb : 0, a.T > 1 ? x.st : 0, a.H / x.div > 1 ? x.sh : 0, D, elem);
 }
 
 template <typename T>
@@ -140,12 +119,46 @@ __global__ __launch_bounds__(256) void la_step(pn_linattn_step_args a) {
 
 }  // namespace
 
-hipError_t launch_linattn(const LaArgs& a, hipStream_t st) {
-    switch (a.dtype) {
-        case PN_F32: return launch_recurrent<float>(a, st);
-        case PN_BF16: return launch_recurrent<bf16>(a, st);
-        default: return launch_recurrent<f16>(a, st);
+size_t linattn_workspace(const LaArgs& a) {
+    int64_t seg;
+    int n_seg;
+    segments(a, &seg, &n_seg);
+    size_t n = 0;
+    for (int w = 0; w < a.n_ops; ++w)
+        n += sizeof(float) * static_cast<size_t>(n_seg - 1) * a.B * a.H * a.op[w].DK * a.op[w].DV;
+    return n;
+}
+
+hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st) {
+    LaChunkArgs g{};
+    g.a = a;
+    segments(a, &g.seg, &g.n_seg);
+    float* ws = static_cast<float*>(workspace);
+    int64_t most = 0;
+    for (int w = 0; w < a.n_ops; ++w) {
+        const LaOp& op = a.op[w];
+        g.vec[w] = (wide(op.q, op.DK, a) ? 1 : 0) | (wide(op.k, op.DK, a) ? 2 : 0) | (wide(op.v, op.DV, a) ? 4 : 0) |
+                   (wide(op.o, 0, 0, 0, op.DV, 4) ? 8 : 0);
+        const int64_t n = static_cast<int64_t>(a.B) * a.H * op.DK * op.DV;
+        g.carry[w] = ws;
+        ws += (g.n_seg - 1) * n;
+        most = n > most ? n : most;
     }
+    auto run = [&](bool out) {
+        switch (a.dtype) {
+            case PN_F32: return launch_chunks<float>(g, out, st);
+            case PN_BF16: return launch_chunks<bf16>(g, out, st);
+            default: return launch_chunks<f16>(g, out, st);
+        }
+    };
+    if (g.n_seg > 1) {
+        hipError_t e = run(false);
+        if (e != hipSuccess) return e;
+        la_carry<<<dim3(static_cast<uint32_t>((most + 255) / 256), a.n_ops), 256, 0, st>>>(g);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return run(true);
 }
 
 hipError_t launch_group_sum(const float* in, void* out, int dtype, int64_t rows, int G, int D, hipStream_t st) {

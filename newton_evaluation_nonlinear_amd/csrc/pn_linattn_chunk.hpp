@@ -1,0 +1,466 @@
+// The chunked form of the operator in pn_seq.hpp (LaOp), on the matrix cores.
+//
+// A chunk of C tokens with state S before it, for i, j inside the chunk:
+//     O_i = f lam^{i+1} Q_i S + p sum_{j <= i} lam^{i-j} (Q_i . K_j) V_j
+//     S  <- lam^C S + ws sum_j lam^{C-1-j} K_j^T V_j
+// (time reversed: lam^{i} and lam^{C-j}, since lam then follows a token).
+//
+// A wave owns 32 columns (value channels) of a state and walks the chunks of
+// its part of the sequence with that state, DK x 32 float32, in its
+// accumulators.  Nothing of it goes through LDS: an accumulator tile's lanes
+// are columns and its registers rows, which is how the next product wants
+// its operand, once the rows are dealt to the registers as perm() does and
+// the float32 values are cut into bfloat16 parts.  The same holds for the
+// scores, which are formed transposed (K Q^T) and feed the product with V.
+// So a chunk's products are, per wave,
+//     scores^T = K Q^T,   O^T = S^T Q^T (scaled) + V^T scores^T,   S += K^T (w V).
+// The waves of a workgroup (32 NW columns) share Q, K and K^T in LDS; V^T is
+// read by the wave that owns its columns.
+//
+// Precision.  A float32 operand is a sum of bfloat16 parts of 8 bits each, a
+// product of two the sum of the parts' products of order below `LIM`; a
+// storage type has NP parts (bfloat16 1, binary16 2, float32 3, all exact).
+// Outputs in 16 bits take LIM 2 (2^-16 per operand); the state, and float32
+// outputs, LIM 3 (2^-24).
+#pragma once
+
+#include <type_traits>
+
+#include "pn_seq.hpp"
+#include "pn_seq_device.hpp"
+
+namespace pn {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <typename T>
+struct Parts;
+template <>
+struct Parts<bf16> { static constexpr int NP = 1, LIM = 2, C = 64; };
+template <>
+struct Parts<f16> { static constexpr int NP = 2, LIM = 2, C = 32; };
+template <>
+struct Parts<float> { static constexpr int NP = 3, LIM = 3, C = 32; };
+
+// One launch of chunk workgroups (pn_linattn.hip).
+struct LaChunkArgs {
+    LaArgs a;
+    int64_t seg;           // tokens of a segment (a multiple of C)
+    int32_t n_seg;
+    int32_t vec[3];        // operands of op[w] readable 16 bytes at a time (bits q 1, k 2, v 4), output writable (8)
+    float* carry[3];       // [n_seg - 1][B * H][DK][DV] states: of each segment alone, then before the next segment
+};
+
+__device__ __forceinline__ int seq_len(const int32_t* lengths, int b, int T) {
+    if (!lengths) return T;
+    const int n = lengths[b];
+    return n < 0 ? 0 : (n > T ? T : n);
+}
+
+// Row (or column) of a 32-wide tile that lane index m stands for: register r
+// of half h of an accumulator tile then holds row 16 (r / 8) + 8 h + r % 8.
+__device__ __forceinline__ int perm(int m) { return 16 * (m >> 4) + 8 * ((m >> 2) & 1) + 4 * ((m >> 3) & 1) + (m & 3); }
+
+// Element offset of 16-byte block b of a row of NB blocks: the blocks of 16
+// neighbouring rows that are read together fall into different banks, and so
+// do those of every eighth row, which the transposing store writes together.
+template <int NB>
+__device__ __forceinline__ int block_at(int row, int b) {
+    constexpr int per = NB >= 16 ? 1 : 16 / NB, mask = (NB >= 16 ? 16 : NB) - 1;
+    return (row * NB + (b ^ (((row / per) ^ (row / 16)) & mask))) * 8;
+}
+
+// 8 float32 values as N bfloat16 parts.
+template <int N>
+__device__ __forceinline__ void split(const float* x, bf16x8* part) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bf16x2 p = __builtin_convertvector((f32x2){r[2 * i], r[2 * i + 1]}, bf16x2);
+            w[i] = __builtin_bit_cast(uint32_t, p);
+            if (n + 1 < N) {
+                r[2 * i] -= __uint_as_float(w[i] << 16);
+                r[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+        part[n] = __builtin_bit_cast(bf16x8, w);
+    }
+}
+
+// 8 values of a storage type as its NP parts.
+template <typename T>
+__device__ __forceinline__ void parts_of(const Pack<T, 8>& x, bf16x8* part) {
+    if constexpr (sizeof(T) == 2 && Parts<T>::NP == 1) {
+        part[0] = __builtin_bit_cast(bf16x8, x);
+    } else {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = to_f32(x.v[i]);
+        split<Parts<T>::NP>(f, part);
+    }
+}
+
+template <int NP>
+__device__ __forceinline__ void sum_parts(const bf16x8* part, float* x) {
+#pragma unroll
+    for (int n = NP - 1; n >= 0; --n) {
+        const u32x4 w = __builtin_bit_cast(u32x4, part[n]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xffff0000u);
+            x[2 * i] = n == NP - 1 ? a : x[2 * i] + a;
+            x[2 * i + 1] = n == NP - 1 ? b : x[2 * i + 1] + b;
+        }
+    }
+}
+
+// c += the products of the parts of a (NA) and b (NB) of order below LIM.
+template <int NA, int NB, int LIM>
+__device__ __forceinline__ f32x16 product(const bf16x8* a, const bf16x8* b, f32x16 c) {
+#pragma unroll
+    for (int o = (NA + NB - 2 < LIM - 1 ? NA + NB - 2 : LIM - 1); o >= 0; --o)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (o - i >= 0 && o - i < NB) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[o - i], c, 0, 0, 0);
+    return c;
+}
+
+// Rows of one operand on their way from memory to LDS: units of 4 tokens x 8
+// channels, UNITS per thread.
+template <typename T, int C, int W, int NT>
+struct Stage {
+    static constexpr int NU = (C / 4) * (W / 8);                 // units of a chunk
+    static constexpr int UNITS = (NU + NT - 1) / NT;
+    Pack<T, 8> x[UNITS][4];
+
+    // Tokens i0 .. of the operand's order (t = i, or last - i reversed); zero
+    // from token `n` on and from channel D on.
+    __device__ __forceinline__ void load(const T* base, int64_t st, bool vec, int c0, int D, int i0, int n, int last,
+                                         bool reverse) {
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int unit = threadIdx.x + u * NT;
+            const int ch = c0 + (unit % (W / 8)) * 8, tk = i0 + (unit / (W / 8)) * 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = tk + j;
+                Pack<T, 8> v{};
+                if ((NU % NT == 0 || unit < NU) && i < n && ch < D) {
+                    const T* p = base + (reverse ? last - i : i) * st + ch;
+                    if (vec) {
+                        v = *reinterpret_cast<const Pack<T, 8>*>(p);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (ch + e < D) v.v[e] = p[e];
+                    }
+                }
+                x[u][j] = v;
+            }
+        }
+    }
+    // To LDS as rows[part][token][channel] and / or cols[part][channel][token].
+    template <bool ROWS, bool COLS>
+    __device__ __forceinline__ void store(bf16* rows, bf16* cols) const {
+        constexpr int NP = Parts<T>::NP;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int unit = threadIdx.x + u * NT;
+            if (NU % NT != 0 && unit >= NU) continue;
+            const int cb = unit % (W / 8), tk = (unit / (W / 8)) * 4;
+            bf16x8 p[4][NP];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                parts_of<T>(x[u][j], p[j]);
+                if (ROWS)
+#pragma unroll
+                    for (int n = 0; n < NP; ++n)
+                        *reinterpret_cast<bf16x8*>(rows + n * C * W + block_at<W / 8>(tk + j, cb)) = p[j][n];
+            }
+            if (COLS)
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    u32x4 w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = __builtin_bit_cast(u32x4, p[j][n]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // channel e of the 4 tokens: the low or high halves of word e / 2
+                        const uint32_t sel = e % 2 ? 0x07060302u : 0x05040100u;
+                        const u32x2 v = {__builtin_amdgcn_perm(w[1][e / 2], w[0][e / 2], sel),
+                                         __builtin_amdgcn_perm(w[3][e / 2], w[2][e / 2], sel)};
+                        *reinterpret_cast<u32x2*>(cols + n * C * W + block_at<C / 8>(cb * 8 + e, tk / 8) + tk % 8) = v;
+                    }
+                }
+        }
+    }
+};
+
+// 8 values of an output tile (registers 8 t ..) to channels ch .. of a row.
+template <typename T>
+__device__ __forceinline__ void put(T* row, int ch, int D, bool vec, const f32x16& o, int t) {
+    Pack<T, 8> v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v.v[e] = from_f32<T>(o[8 * t + e]);
+    if (vec) {
+        if (ch < D) *reinterpret_cast<Pack<T, 8>*>(row + ch) = v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (ch + e < D) row[ch + e] = v.v[e];
+    }
+}
+
+template <typename T, int DKP, int NW, bool OUT>
+struct LaShared {
+    static constexpr int NP = Parts<T>::NP, C = Parts<T>::C;
+    bf16 q[OUT ? NP * C * DKP : 8];
+    bf16 k[OUT ? NP * C * DKP : 8];
+    bf16 kt[NP * DKP * C];
+    bf16 vt[NP * NW * 32 * C];
+    float pw[C + 4];         // lam^0 .. lam^C
+    float w[C];              // weights of V in the state
+};
+
+// OUT: outputs of a segment, from the state before it.  Otherwise the state
+// that a segment leaves alone (from zero), for the scan over segments.
+template <typename T, int DKP, int NW, bool OUT>
+__global__ __launch_bounds__(64 * NW) void la_chunk(LaChunkArgs g) {
+    constexpr int NP = Parts<T>::NP, LIM = Parts<T>::LIM, C = Parts<T>::C, NT = 64 * NW;
+    constexpr int KT = DKP / 32, IT = C / 32;
+    __shared__ LaShared<T, DKP, NW, OUT> sh;
+    const LaArgs& a = g.a;
+    const int op_i = blockIdx.z;
+    const LaOp& op = a.op[op_i];
+    const int c0 = blockIdx.y * 32 * NW;
+    if (c0 >= op.DV) return;
+    const int segs = OUT ? g.n_seg : g.n_seg - 1;
+    const int bh = blockIdx.x / segs, sg = blockIdx.x - bh * segs;
+    const int h = bh % a.H, b = bh / a.H;
+    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, half = lane / 32, l32 = lane % 32, pl = perm(l32);
+    const int N = static_cast<int>(a.T), len = seq_len(a.lengths, b, N), vec = g.vec[op_i];
+    const bool reverse = op.reverse;
+    const int DK = op.DK, DV = op.DV;
+    const int i_begin = static_cast<int>(sg * g.seg);
+    const int i_end = static_cast<int>(min(static_cast<int64_t>(N), (sg + 1) * g.seg));
+    const int n_end = min(i_end, len);                   // tokens that count
+    const double gl = a.log_decay[h];
+
+    if (tid <= C) sh.pw[tid] = tid == 0 ? 1.0f : static_cast<float>(exp(gl * tid));
+    __syncthreads();
+    if (tid < C) sh.w[tid] = op.ws * sh.pw[C - 1 - tid + (reverse ? 1 : 0)];
+
+    // this lane's decays between tokens of a tile pair, times the scale
+    float mdiag[OUT ? 16 : 1], moff[OUT && IT > 1 ? 16 : 1];
+    const float pscale = op.inter * op.ws;
+    if (OUT) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int d = l32 - (16 * (r / 8) + 8 * half + r % 8);
+            mdiag[r] = d >= 0 ? pscale * sh.pw[d < 0 ? 0 : d] : 0.0f;
+            if (IT > 1) moff[r] = pscale * sh.pw[32 + d];
+        }
+    }
+
+    const int64_t state_at = static_cast<int64_t>(bh) * DK * DV;
+    const int col = c0 + 32 * wave + pl;                 // this lane's column of the state
+    f32x16 S[KT];
+    {
+        const float* from = OUT ? (sg > 0 ? g.carry[op_i] + static_cast<int64_t>(sg - 1) * a.B * a.H * DK * DV : op.s_in) : nullptr;
+        const int sk = sg > 0 ? DV : op.s_k, sv = sg > 0 ? 1 : op.s_v;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = 32 * t + 16 * (r / 8) + 8 * half + r % 8;
+                S[t][r] = from && row < DK && col < DV ? from[state_at + row * sk + col * sv] : 0.0f;
+            }
+    }
+
+    const T* kb = static_cast<const T*>(op.k.p) + b * op.k.sb + (h / op.k.div) * op.k.sh;
+    const T* vb = static_cast<const T*>(op.v.p) + b * op.v.sb + (h / op.v.div) * op.v.sh;
+    const T* qb = static_cast<const T*>(op.q.p) + b * op.q.sb + (h / op.q.div) * op.q.sh;
+    Stage<T, C, DKP, NT> kst, qst;
+    Stage<T, C, 32 * NW, NT> vst;
+    if (i_begin < n_end) {
+        kst.load(kb, op.k.st, vec & 2, 0, DK, i_begin, n_end, len - 1, reverse);
+        vst.load(vb, op.v.st, vec & 4, c0, DV, i_begin, n_end, len - 1, reverse);
+        if (OUT) qst.load(qb, op.q.st, vec & 1, 0, DK, i_begin, n_end, len - 1, reverse);
+    }
+    for (int i0 = i_begin; i0 < n_end; i0 += C) {
+        const int L = min(C, n_end - i0);
+        __syncthreads();                                  // the chunk before is read
+        kst.template store<OUT, true>(sh.k, sh.kt);
+        vst.template store<false, true>(nullptr, sh.vt);
+        if (OUT) qst.template store<true, false>(sh.q, nullptr);
+        if (L < C && tid < C) sh.w[tid] = tid < L ? op.ws * sh.pw[L - 1 - tid + (reverse ? 1 : 0)] : 0.0f;
+        __syncthreads();
+        if (i0 + C < n_end) {
+            kst.load(kb, op.k.st, vec & 2, 0, DK, i0 + C, n_end, len - 1, reverse);
+            vst.load(vb, op.v.st, vec & 4, c0, DV, i0 + C, n_end, len - 1, reverse);
+            if (OUT) qst.load(qb, op.q.st, vec & 1, 0, DK, i0 + C, n_end, len - 1, reverse);
+        }
+        bf16x8 vf[C / 16][NP];
+#pragma unroll
+        for (int t = 0; t < C / 16; ++t)
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+                vf[t][n] = *reinterpret_cast<const bf16x8*>(
+                    sh.vt + n * C * 32 * NW + block_at<C / 8>(32 * wave + pl, 2 * t + half));
+        if (OUT) {
+            f32x16 P[IT][IT], O[IT];                       // P[i][j], j <= i
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                O[i] = (f32x16)(0.0f);
+#pragma unroll
+                for (int j = 0; j <= i; ++j) P[i][j] = (f32x16)(0.0f);
+            }
+#pragma unroll
+            for (int t = 0; t < DKP / 16; ++t) {
+                bf16x8 qf[IT][NP], kf[IT][NP], sf[LIM];
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) {
+                        qf[i][n] = *reinterpret_cast<const bf16x8*>(sh.q + n * C * DKP + block_at<DKP / 8>(32 * i + l32, 2 * t + half));
+                        kf[i][n] = *reinterpret_cast<const bf16x8*>(sh.k + n * C * DKP + block_at<DKP / 8>(32 * i + pl, 2 * t + half));
+                    }
+                float s8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s8[e] = S[t / 2][8 * (t % 2) + e];
+                split<LIM>(s8, sf);
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+#pragma unroll
+                    for (int j = 0; j <= i; ++j) P[i][j] = product<NP, NP, 3>(kf[j], qf[i], P[i][j]);
+                    O[i] = product<LIM, NP, LIM>(sf, qf[i], O[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const float f = op.inter * sh.pw[32 * i + l32 + (reverse ? 0 : 1)];
+                O[i] *= f;
+#pragma unroll
+                for (int j = 0; j <= i; ++j) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        float p8[8];
+                        bf16x8 pf[LIM];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) p8[e] = P[i][j][8 * t + e] * (i == j ? mdiag[8 * t + e] : moff[8 * t + e]);
+                        split<LIM>(p8, pf);
+                        O[i] = product<NP, LIM, LIM>(vf[2 * j + t], pf, O[i]);
+                    }
+                }
+                const int row = 32 * i + l32;
+                if (row < L) {
+                    const int64_t tok = reverse ? len - 1 - (i0 + row) : i0 + row;
+                    const int64_t at = ((b * a.T + tok) * a.H + h) * DV;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int ch = c0 + 32 * wave + 16 * t + 8 * half;
+                        if (op.o_f32) put(static_cast<float*>(op.o) + at, ch, DV, vec & 8, O[i], t);
+                        else put(static_cast<T*>(op.o) + at, ch, DV, vec & 8, O[i], t);
+                    }
+                }
+            }
+        }
+        const float decay = sh.pw[L];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) S[t] *= decay;
+#pragma unroll
+        for (int t = 0; t < C / 16; ++t) {
+            float v8[8];
+            bf16x8 wv[3];
+            sum_parts<NP>(vf[t], v8);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v8[e] *= sh.w[16 * t + 8 * half + e];
+            split<3>(v8, wv);
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                bf16x8 kf[NP];
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+                    kf[n] = *reinterpret_cast<const bf16x8*>(sh.kt + n * C * DKP + block_at<C / 8>(32 * kt + pl, 2 * t + half));
+                S[kt] = product<NP, 3, 3>(kf, wv, S[kt]);
+            }
+        }
+    }
+    if (OUT) {
+        // padding rows
+        for (int64_t e = static_cast<int64_t>(max(i_begin, n_end)) * 32 * NW + tid; e < static_cast<int64_t>(i_end) * 32 * NW; e += NT) {
+            const int64_t t = e / (32 * NW);
+            const int c = c0 + static_cast<int>(e % (32 * NW));
+            const int64_t at = ((b * a.T + t) * a.H + h) * DV + c;
+            if (c < DV) {
+                if (op.o_f32) static_cast<float*>(op.o)[at] = 0.0f;
+                else static_cast<T*>(op.o)[at] = from_f32<T>(0.0f);
+            }
+        }
+    }
+    float* to = OUT ? (sg == segs - 1 ? op.s_out : nullptr) : g.carry[op_i] + static_cast<int64_t>(sg) * a.B * a.H * DK * DV;
+    if (to && col < DV)
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = 32 * t + 16 * (r / 8) + 8 * half + r % 8;
+                if (row < DK) to[state_at + static_cast<int64_t>(row) * DV + col] = S[t][r];
+            }
+}
+
+// Columns per workgroup of a launch, and its padded rows.
+inline int la_waves(const LaArgs& a) {
+    int dk = 0, dv = 0;
+    for (int w = 0; w < a.n_ops; ++w) {
+        if (a.op[w].DK > dk) dk = a.op[w].DK;
+        if (a.op[w].DV > dv) dv = a.op[w].DV;
+    }
+    // float32 parts of 256 rows and 128 columns pass the 160 KB of LDS
+    return dv <= 64 || (dk > 128 && a.dtype == PN_F32) ? 2 : 4;
+}
+
+template <typename T>
+hipError_t launch_chunks(const LaChunkArgs& g, bool out, hipStream_t st) {
+    int dk = 0, dv = 0;
+    for (int w = 0; w < g.a.n_ops; ++w) {
+        if (g.a.op[w].DK > dk) dk = g.a.op[w].DK;
+        if (g.a.op[w].DV > dv) dv = g.a.op[w].DV;
+    }
+    const int nw = la_waves(g.a);
+    const int segs = out ? g.n_seg : g.n_seg - 1;
+    const dim3 grid(static_cast<uint32_t>(g.a.B * g.a.H * segs), (dv + 32 * nw - 1) / (32 * nw), g.a.n_ops);
+    auto go = [&](auto rows, auto waves) {
+        constexpr int DKP = decltype(rows)::value, NW = decltype(waves)::value;
+        if (out) la_chunk<T, DKP, NW, true><<<grid, 64 * NW, 0, st>>>(g);
+        else la_chunk<T, DKP, NW, false><<<grid, 64 * NW, 0, st>>>(g);
+        return hipGetLastError();
+    };
+    using std::integral_constant;
+    using W2 = integral_constant<int, 2>;
+    using W4 = integral_constant<int, 4>;
+    auto rows = [&](auto r) {
+        using R = decltype(r);
+        if constexpr (R::value == 256 && sizeof(T) == 4) return go(r, W2{});
+        else return nw == 2 ? go(r, W2{}) : go(r, W4{});
+    };
+    if (dk <= 32) return rows(integral_constant<int, 32>{});
+    if (dk <= 64) return rows(integral_constant<int, 64>{});
+    if (dk <= 128) return rows(integral_constant<int, 128>{});
+    return rows(integral_constant<int, 256>{});
+}
+extern template hipError_t launch_chunks<float>(const LaChunkArgs&, bool, hipStream_t);
+extern template hipError_t launch_chunks<bf16>(const LaChunkArgs&, bool, hipStream_t);
+extern template hipError_t launch_chunks<f16>(const LaChunkArgs&, bool, hipStream_t);
+
+}  // namespace pn

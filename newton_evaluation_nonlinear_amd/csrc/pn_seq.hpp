@@ -54,7 +54,8 @@ struct LaArgs {
     const float* log_decay;
     const int32_t* lengths;
 };
-hipError_t launch_linattn(const LaArgs& a, hipStream_t st);
+size_t linattn_workspace(const LaArgs& a);      // bytes; sizes of `a` only
+hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st);
 // out[b, t, x, d] = sum over g of in[b, t, x * G + g, d]
 hipError_t launch_group_sum(const float* in, void* out, int dtype, int64_t rows, int G, int D, hipStream_t st);
 hipError_t launch_linattn_step(const pn_linattn_step_args& a, hipStream_t st);

@@ -161,18 +161,95 @@ int check_linattn_sizes(int64_t dtype, int64_t B, int64_t T, int64_t H, int64_t 
     return PN_OK;
 }
 
-// Regions of the workspace, in order.
+LaOperand operand(const pn_tokens& x, int div) { return LaOperand{x.p, x.sb, x.st, x.sh, div}; }
+
+// The operators of a call and the regions of its workspace.
 struct LinattnPlan {
-    size_t dk_part = 0, dv_part = 0, total = 0;   // float32 dk and dv of each head, where heads share them
+    LaArgs la{};
+    size_t off_dk = 0, off_dv = 0, off_carry = 0, total = 0;   // float32 dk, dv of each head (where shared), carries
 };
 LinattnPlan plan_linattn(const pn_linattn_args& a, bool backward) {
     LinattnPlan p;
-    if (backward && a.H != a.HK) {
-        p.dk_part = 0;
-        p.total = align_up(sizeof(float) * static_cast<size_t>(a.B * a.T * a.H * a.dk));
-        p.dv_part = p.total;
-        p.total += align_up(sizeof(float) * static_cast<size_t>(a.B * a.T * a.H * a.dv));
+    LaArgs& g = p.la;
+    g.dtype = static_cast<int32_t>(a.dtype);
+    g.B = static_cast<int32_t>(a.B);
+    g.H = static_cast<int32_t>(a.H);
+    g.T = a.T;
+    g.log_decay = a.log_decay;
+    g.lengths = a.lengths;
+    const int share = static_cast<int>(a.H / a.HK);
+    const int32_t dk = static_cast<int32_t>(a.dk), dv = static_cast<int32_t>(a.dv);
+    const float scale = static_cast<float>(a.scale);
+    char* ws = static_cast<char*>(a.workspace);
+    if (!backward) {
+        LaOp& f = g.op[0];
+        f.q = operand(a.q, 1);
+        f.k = operand(a.k, share);
+        f.v = operand(a.v, share);
+        f.o = a.o;
+        f.DK = dk;
+        f.DV = dv;
+        f.inter = scale;
+        f.ws = 1.0f;
+        f.s_in = a.initial_state;
+        f.s_k = dv;
+        f.s_v = 1;
+        f.s_out = a.final_state;
+        g.n_ops = 1;
+    } else {
+        if (share > 1) {
+            p.total = align_up(sizeof(float) * static_cast<size_t>(a.B * a.T * a.H) * dk);
+            p.off_dv = p.total;
+            p.total += align_up(sizeof(float) * static_cast<size_t>(a.B * a.T * a.H) * dv);
+        }
+        // dq: the state S again, transposed
+        LaOp& q = g.op[0];
+        q.q = operand(a.do_, 1);
+        q.k = operand(a.v, share);
+        q.v = operand(a.k, share);
+        q.o = a.dq;
+        q.DK = dv;
+        q.DV = dk;
+        q.inter = scale;
+        q.ws = 1.0f;
+        q.s_in = a.initial_state;
+        q.s_k = 1;
+        q.s_v = dv;
+        // dv: the state's gradient R, backwards in time
+        LaOp& v = g.op[1];
+        v.q = operand(a.k, share);
+        v.k = operand(a.q, 1);
+        v.v = operand(a.do_, 1);
+        v.o = share > 1 ? static_cast<void*>(ws + p.off_dv) : a.dv_;
+        v.o_f32 = share > 1;
+        v.reverse = 1;
+        v.DK = dk;
+        v.DV = dv;
+        v.inter = 1.0f;
+        v.ws = scale;
+        v.s_in = a.d_final_state;
+        v.s_k = dv;
+        v.s_v = 1;
+        v.s_out = a.d_initial_state;
+        // dk: R again, transposed
+        LaOp& k = g.op[2];
+        k.q = operand(a.v, share);
+        k.k = operand(a.do_, 1);
+        k.v = operand(a.q, 1);
+        k.o = share > 1 ? static_cast<void*>(ws + p.off_dk) : a.dk_;
+        k.o_f32 = share > 1;
+        k.reverse = 1;
+        k.DK = dv;
+        k.DV = dk;
+        k.inter = 1.0f;
+        k.ws = scale;
+        k.s_in = a.d_final_state;
+        k.s_k = 1;
+        k.s_v = dv;
+        g.n_ops = 3;
     }
+    p.off_carry = p.total;
+    p.total += align_up(linattn_workspace(g));
     return p;
 }
 
@@ -227,19 +304,6 @@ int check_linattn(const pn_linattn_args* p, bool backward) {
             if (overlap(out[i], out[j])) return fail(PN_EINVAL, "two outputs overlap");
     }
     return PN_OK;
-}
-
-LaOperand operand(const pn_tokens& x, int div) { return LaOperand{x.p, x.sb, x.st, x.sh, div}; }
-
-LaArgs la_args(const pn_linattn_args& a) {
-    LaArgs g{};
-    g.dtype = static_cast<int32_t>(a.dtype);
-    g.B = static_cast<int32_t>(a.B);
-    g.H = static_cast<int32_t>(a.H);
-    g.T = a.T;
-    g.log_decay = a.log_decay;
-    g.lengths = a.lengths;
-    return g;
 }
 
 }  // namespace
@@ -321,85 +385,24 @@ size_t pn_linear_attention_workspace_bytes(const pn_linattn_args* a, int32_t bac
 int pn_linear_attention(const pn_linattn_args* a) {
     PN_TRY(check_linattn(a, false));
     if (a->B == 0 || a->H == 0) return PN_OK;
-    LaArgs g = la_args(*a);
-    const int share = static_cast<int>(a->H / a->HK);
-    LaOp& f = g.op[0];
-    f.q = operand(a->q, 1);
-    f.k = operand(a->k, share);
-    f.v = operand(a->v, share);
-    f.o = a->o;
-    f.DK = static_cast<int32_t>(a->dk);
-    f.DV = static_cast<int32_t>(a->dv);
-    f.inter = static_cast<float>(a->scale);
-    f.ws = 1.0f;
-    f.s_in = a->initial_state;
-    f.s_k = f.DV;
-    f.s_v = 1;
-    f.s_out = a->final_state;
-    g.n_ops = 1;
-    return launched(launch_linattn(g, static_cast<hipStream_t>(a->stream)));
+    const LinattnPlan p = plan_linattn(*a, false);
+    return launched(launch_linattn(p.la, static_cast<char*>(a->workspace) + p.off_carry, static_cast<hipStream_t>(a->stream)));
 }
 
 int pn_linear_attention_backward(const pn_linattn_args* a) {
     PN_TRY(check_linattn(a, true));
     if (a->B == 0 || a->H == 0) return PN_OK;
     hipStream_t st = static_cast<hipStream_t>(a->stream);
-    LaArgs g = la_args(*a);
-    const int share = static_cast<int>(a->H / a->HK);
-    const int32_t dk = static_cast<int32_t>(a->dk), dv = static_cast<int32_t>(a->dv);
-    const LinattnPlan plan = plan_linattn(*a, true);
+    const LinattnPlan p = plan_linattn(*a, true);
     char* ws = static_cast<char*>(a->workspace);
-    const float scale = static_cast<float>(a->scale);
-    // dq: the state S again, transposed
-    LaOp& q = g.op[0];
-    q.q = operand(a->do_, 1);
-    q.k = operand(a->v, share);
-    q.v = operand(a->k, share);
-    q.o = a->dq;
-    q.DK = dv;
-    q.DV = dk;
-    q.inter = scale;
-    q.ws = 1.0f;
-    q.s_in = a->initial_state;
-    q.s_k = 1;
-    q.s_v = dv;
-    // dv: the state's gradient R, backwards in time
-    LaOp& v = g.op[1];
-    v.q = operand(a->k, share);
-    v.k = operand(a->q, 1);
-    v.v = operand(a->do_, 1);
-    v.o = share > 1 ? static_cast<void*>(ws + plan.dv_part) : a->dv_;
-    v.o_f32 = share > 1;
-    v.reverse = 1;
-    v.DK = dk;
-    v.DV = dv;
-    v.inter = 1.0f;
-    v.ws = scale;
-    v.s_in = a->d_final_state;
-    v.s_k = dv;
-    v.s_v = 1;
-    v.s_out = a->d_initial_state;
-    // dk: R again, transposed
-    LaOp& k = g.op[2];
-    k.q = operand(a->v, share);
-    k.k = operand(a->do_, 1);
-    k.v = operand(a->q, 1);
-    k.o = share > 1 ? static_cast<void*>(ws + plan.dk_part) : a->dk_;
-    k.o_f32 = share > 1;
-    k.reverse = 1;
-    k.DK = dv;
-    k.DV = dk;
-    k.inter = 1.0f;
-    k.ws = scale;
-    k.s_in = a->d_final_state;
-    k.s_k = 1;
-    k.s_v = dv;
-    g.n_ops = 3;
-    PN_TRY(launched(launch_linattn(g, st)));
+    PN_TRY(launched(launch_linattn(p.la, ws + p.off_carry, st)));
+    const int share = static_cast<int>(a->H / a->HK);
     if (share > 1 && a->T > 0) {
         const int64_t rows = a->B * a->T * a->HK;
-        PN_TRY(launched(launch_group_sum(reinterpret_cast<float*>(ws + plan.dk_part), a->dk_, g.dtype, rows, share, dk, st)));
-        PN_TRY(launched(launch_group_sum(reinterpret_cast<float*>(ws + plan.dv_part), a->dv_, g.dtype, rows, share, dv, st)));
+        PN_TRY(launched(launch_group_sum(reinterpret_cast<float*>(ws + p.off_dk), a->dk_, p.la.dtype, rows, share,
+                                         static_cast<int>(a->dk), st)));
+        PN_TRY(launched(launch_group_sum(reinterpret_cast<float*>(ws + p.off_dv), a->dv_, p.la.dtype, rows, share,
+                                         static_cast<int>(a->dv), st)));
     }
     return PN_OK;
 }
