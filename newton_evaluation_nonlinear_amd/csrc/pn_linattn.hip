@@ -119,12 +119,16 @@ __global__ __launch_bounds__(256) void la_step(pn_linattn_step_args a) {
 
 }  // namespace
 
+// Operators whose states between segments are formed: the first ones that
+// read their own (dk reads dv's, transposed).
+static int carried(const LaArgs& a) { return a.n_ops == 3 ? 2 : a.n_ops; }
+
 size_t linattn_workspace(const LaArgs& a) {
     int64_t seg;
     int n_seg;
     segments(a, &seg, &n_seg);
     size_t n = 0;
-    for (int w = 0; w < a.n_ops; ++w)
+    for (int w = 0; w < carried(a); ++w)
         n += sizeof(float) * static_cast<size_t>(n_seg - 1) * a.B * a.H * a.op[w].DK * a.op[w].DV;
     return n;
 }
@@ -140,25 +144,35 @@ hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st) {
         g.vec[w] = (wide(op.q, op.DK, a) ? 1 : 0) | (wide(op.k, op.DK, a) ? 2 : 0) | (wide(op.v, op.DV, a) ? 4 : 0) |
                    (wide(op.o, 0, 0, 0, op.DV, 4) ? 8 : 0);
         const int64_t n = static_cast<int64_t>(a.B) * a.H * op.DK * op.DV;
-        g.carry[w] = ws;
-        ws += (g.n_seg - 1) * n;
+        if (op.carry_from == w) {
+            g.carry[w] = ws;
+            g.c_k[w] = op.DV;
+            g.c_v[w] = 1;
+            ws += (g.n_seg - 1) * n;
+        } else {
+            g.carry[w] = g.carry[op.carry_from];
+            g.c_k[w] = 1;
+            g.c_v[w] = op.DK;
+        }
         most = n > most ? n : most;
     }
-    auto run = [&](bool out) {
+    auto run = [&](const LaChunkArgs& c, bool out) {
         switch (a.dtype) {
-            case PN_F32: return launch_chunks<float>(g, out, st);
-            case PN_BF16: return launch_chunks<bf16>(g, out, st);
-            default: return launch_chunks<f16>(g, out, st);
+            case PN_F32: return launch_chunks<float>(c, out, st);
+            case PN_BF16: return launch_chunks<bf16>(c, out, st);
+            default: return launch_chunks<f16>(c, out, st);
         }
     };
     if (g.n_seg > 1) {
-        hipError_t e = run(false);
+        LaChunkArgs c = g;
+        c.a.n_ops = carried(a);
+        hipError_t e = run(c, false);
         if (e != hipSuccess) return e;
-        la_carry<<<dim3(static_cast<uint32_t>((most + 255) / 256), a.n_ops), 256, 0, st>>>(g);
+        la_carry<<<dim3(static_cast<uint32_t>((most + 255) / 256), c.a.n_ops), 256, 0, st>>>(c);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return run(true);
+    return run(g, true);
 }
 
 hipError_t launch_group_sum(const float* in, void* out, int dtype, int64_t rows, int G, int D, hipStream_t st) {

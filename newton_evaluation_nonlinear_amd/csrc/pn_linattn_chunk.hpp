@@ -53,8 +53,19 @@ struct LaChunkArgs {
     int64_t seg;           // tokens of a segment (a multiple of C)
     int32_t n_seg;
     int32_t vec[3];        // operands of op[w] readable 16 bytes at a time (bits q 1, k 2, v 4), output writable (8)
-    float* carry[3];       // [n_seg - 1][B * H][DK][DV] states: of each segment alone, then before the next segment
+    // [n_seg - 1][B * H] states, of each segment alone, then before the next
+    // segment; element (x, y) of one at x * c_k + y * c_v
+    float* carry[3];
+    int32_t c_k[3], c_v[3];
 };
+
+// The workgroup's place in the launch, so that neighbours (columns of a head,
+// operators and segments of it, heads that share keys and values) are on one
+// of the 8 dies, and in its L2: ids go to the dies in turn.
+__device__ __forceinline__ int neighbour_id(int id, int total) {
+    const int die = id & 7, q = total >> 3, r = total & 7;
+    return (die < r ? die * (q + 1) : r * (q + 1) + (die - r) * q) + (id >> 3);
+}
 
 __device__ __forceinline__ int seq_len(const int32_t* lengths, int b, int T) {
     if (!lengths) return T;
@@ -66,14 +77,12 @@ __device__ __forceinline__ int seq_len(const int32_t* lengths, int b, int T) {
 // of half h of an accumulator tile then holds row 16 (r / 8) + 8 h + r % 8.
 __device__ __forceinline__ int perm(int m) { return 16 * (m >> 4) + 8 * ((m >> 2) & 1) + 4 * ((m >> 3) & 1) + (m & 3); }
 
-// Element offset of 16-byte block b of a row of NB blocks: the blocks of 16
-// neighbouring rows that are read together fall into different banks, and so
-// do those of every eighth row, which the transposing store writes together.
-template <int NB>
-__device__ __forceinline__ int block_at(int row, int b) {
-    constexpr int per = NB >= 16 ? 1 : 16 / NB, mask = (NB >= 16 ? 16 : NB) - 1;
-    return (row * NB + (b ^ (((row / per) ^ (row / 16)) & mask))) * 8;
-}
+// Elements from one LDS row of W to the next: 16 bytes of padding put the
+// 16-byte reads of neighbouring rows into different banks, and keep every
+// read of a lane at a constant distance from its first.  (The float32 parts
+// of 256 rows leave no room for it.)
+template <typename T, int DKP>
+constexpr int pitch(int W) { return W + (sizeof(T) == 4 && DKP == 256 ? 0 : 8); }
 
 // 8 float32 values as N bfloat16 parts.
 template <int N>
@@ -136,56 +145,82 @@ __device__ __forceinline__ f32x16 product(const bf16x8* a, const bf16x8* b, f32x
 }
 
 // Rows of one operand on their way from memory to LDS: units of 4 tokens x 8
-// channels, UNITS per thread.
-template <typename T, int C, int W, int NT>
+// channels, UNITS per thread.  An operand that is stored transposed has
+// neighbouring lanes on neighbouring tokens, so that their stores join in an
+// LDS row; one that is not has them on neighbouring channels.  A chunk's tokens past the last one repeat it:
+// what they add is dropped (rows not stored) or weighted 0.
+template <typename T, int C, int W, int NT, bool COLS>
 struct Stage {
     static constexpr int NU = (C / 4) * (W / 8);                 // units of a chunk
     static constexpr int UNITS = (NU + NT - 1) / NT;
     Pack<T, 8> x[UNITS][4];
+    const T* p[UNITS];       // the unit's first token in the next chunk to load
+    int64_t step;            // elements from one token to the next
+    int valid;               // channels from the operand's first on
+    bool vec;
 
-    // Tokens i0 .. of the operand's order (t = i, or last - i reversed); zero
-    // from token `n` on and from channel D on.
-    __device__ __forceinline__ void load(const T* base, int64_t st, bool vec, int c0, int D, int i0, int n, int last,
-                                         bool reverse) {
+    __device__ __forceinline__ static int token(int u) {
+        const int i = threadIdx.x + u * NT;
+        return (COLS ? i % (C / 4) : i / (W / 8)) * 4;
+    }
+    __device__ __forceinline__ static int channel(int u) {
+        const int i = threadIdx.x + u * NT;
+        return (COLS ? i / (C / 4) : i % (W / 8)) * 8;
+    }
+
+    // `base`: channel 0 of the first token of the first chunk.
+    __device__ __forceinline__ void open(const T* base, int64_t step_, bool vec_, int c0, int D) {
+        step = step_;
+        vec = vec_;
+        valid = D - c0;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) p[u] = base + token(u) * step + c0 + channel(u);
+    }
+    // The next chunk, of which L tokens exist.
+    __device__ __forceinline__ void load(int L) {
+        const bool full = L >= C;
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
-            const int unit = threadIdx.x + u * NT;
-            const int ch = c0 + (unit % (W / 8)) * 8, tk = i0 + (unit / (W / 8)) * 4;
+            const int left = valid - channel(u), last = L - 1 - token(u);
+            const bool on = (NU % NT == 0 || static_cast<int>(threadIdx.x) + u * NT < NU) && left > 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = tk + j;
-                Pack<T, 8> v{};
-                if ((NU % NT == 0 || unit < NU) && i < n && ch < D) {
-                    const T* p = base + (reverse ? last - i : i) * st + ch;
-                    if (vec) {
-                        v = *reinterpret_cast<const Pack<T, 8>*>(p);
-                    } else {
+            for (int j = 0; j < 4; ++j) x[u][j] = Pack<T, 8>{};
+            if (on) {
+                if (vec && full) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[u][j] = *reinterpret_cast<const Pack<T, 8>*>(p[u] + j * step);
+                } else if (vec) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[u][j] = *reinterpret_cast<const Pack<T, 8>*>(p[u] + (j < last ? j : last) * step);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const T* row = p[u] + (j < last ? j : last) * step;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if (ch + e < D) v.v[e] = p[e];
+                            if (e < left) x[u][j].v[e] = row[e];
                     }
                 }
-                x[u][j] = v;
             }
+            p[u] += C * step;
         }
     }
     // To LDS as rows[part][token][channel] and / or cols[part][channel][token].
-    template <bool ROWS, bool COLS>
+    template <bool ROWS, int RP, int CP>
     __device__ __forceinline__ void store(bf16* rows, bf16* cols) const {
         constexpr int NP = Parts<T>::NP;
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
-            const int unit = threadIdx.x + u * NT;
-            if (NU % NT != 0 && unit >= NU) continue;
-            const int cb = unit % (W / 8), tk = (unit / (W / 8)) * 4;
+            if (NU % NT != 0 && static_cast<int>(threadIdx.x) + u * NT >= NU) continue;
+            const int ch = channel(u), tk = token(u);
             bf16x8 p[4][NP];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 parts_of<T>(x[u][j], p[j]);
                 if (ROWS)
 #pragma unroll
-                    for (int n = 0; n < NP; ++n)
-                        *reinterpret_cast<bf16x8*>(rows + n * C * W + block_at<W / 8>(tk + j, cb)) = p[j][n];
+                    for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8*>(rows + (n * C + tk + j) * RP + ch) = p[j][n];
             }
             if (COLS)
 #pragma unroll
@@ -199,7 +234,7 @@ struct Stage {
                         const uint32_t sel = e % 2 ? 0x07060302u : 0x05040100u;
                         const u32x2 v = {__builtin_amdgcn_perm(w[1][e / 2], w[0][e / 2], sel),
                                          __builtin_amdgcn_perm(w[3][e / 2], w[2][e / 2], sel)};
-                        *reinterpret_cast<u32x2*>(cols + n * C * W + block_at<C / 8>(cb * 8 + e, tk / 8) + tk % 8) = v;
+                        *reinterpret_cast<u32x2*>(cols + (n * W + ch + e) * CP + tk) = v;
                     }
                 }
         }
@@ -222,101 +257,145 @@ __device__ __forceinline__ void put(T* row, int ch, int D, bool vec, const f32x1
 }
 
 template <typename T, int DKP, int NW, bool OUT>
-struct LaShared {
+struct alignas(16) LaShared {
     static constexpr int NP = Parts<T>::NP, C = Parts<T>::C;
-    bf16 q[OUT ? NP * C * DKP : 8];
-    bf16 k[OUT ? NP * C * DKP : 8];
-    bf16 kt[NP * DKP * C];
-    bf16 vt[NP * NW * 32 * C];
-    float pw[C + 4];         // lam^0 .. lam^C
-    float w[C];              // weights of V in the state
+    static constexpr int RP = pitch<T, DKP>(DKP), CP = pitch<T, DKP>(C);
+    alignas(16) bf16 q[OUT ? NP * C * RP : 8];      // [part][token][channel]
+    alignas(16) bf16 k[OUT ? NP * C * RP : 8];
+    alignas(16) bf16 kt[NP * DKP * CP];             // [part][channel][token]
+    alignas(16) bf16 vt[NP * NW * 32 * CP];
+    alignas(16) float w[C];         // weights of V in the state
+    alignas(16) float back[32];     // lam^{32 - j}
+    float pw[C + 4];                // lam^0 .. lam^C
 };
+
+__device__ __forceinline__ bf16x8 fragment(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
+
+// S += K^T (w V), w V in N parts.
+template <typename T, int DKP, int CP, int N>
+__device__ __forceinline__ void add_tokens(f32x16* S, const bf16* kt, const float* w, const bf16x8 (*vf)[Parts<T>::NP]) {
+    constexpr int NP = Parts<T>::NP, C = Parts<T>::C;
+#pragma unroll
+    for (int t = 0; t < C / 16; ++t) {
+        float v8[8];
+        bf16x8 wv[N];
+        sum_parts<NP>(vf[t], v8);
+        const Pack<float, 4> w0 = *reinterpret_cast<const Pack<float, 4>*>(w + 16 * t);
+        const Pack<float, 4> w1 = *reinterpret_cast<const Pack<float, 4>*>(w + 16 * t + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v8[e] *= w0.v[e];
+            v8[4 + e] *= w1.v[e];
+        }
+        split<N>(v8, wv);
+#pragma unroll
+        for (int kt_i = 0; kt_i < DKP / 32; ++kt_i) {
+            bf16x8 kf[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) kf[n] = fragment(kt + (n * DKP + 32 * kt_i) * CP + 16 * t);
+            S[kt_i] = product<NP, N, N>(kf, wv, S[kt_i]);
+        }
+    }
+}
 
 // OUT: outputs of a segment, from the state before it.  Otherwise the state
 // that a segment leaves alone (from zero), for the scan over segments.
-template <typename T, int DKP, int NW, bool OUT>
-__global__ __launch_bounds__(64 * NW) void la_chunk(LaChunkArgs g) {
+// EXACT: the state is a result, not only a term of 16-bit outputs.
+template <typename T, int DKP, int NW, bool OUT, bool EXACT>
+__global__ __launch_bounds__(64 * NW, 2) void la_chunk(LaChunkArgs g, int col_blocks) {
     constexpr int NP = Parts<T>::NP, LIM = Parts<T>::LIM, C = Parts<T>::C, NT = 64 * NW;
     constexpr int KT = DKP / 32, IT = C / 32;
     __shared__ LaShared<T, DKP, NW, OUT> sh;
     const LaArgs& a = g.a;
-    const int op_i = blockIdx.z;
-    const LaOp& op = a.op[op_i];
-    const int c0 = blockIdx.y * 32 * NW;
-    if (c0 >= op.DV) return;
     const int segs = OUT ? g.n_seg : g.n_seg - 1;
-    const int bh = blockIdx.x / segs, sg = blockIdx.x - bh * segs;
+    int id = neighbour_id(blockIdx.x, gridDim.x);
+    const int c0 = id % col_blocks * 32 * NW;
+    id /= col_blocks;
+    const int op_i = id % a.n_ops;
+    id /= a.n_ops;
+    const int sg = id % segs, bh = id / segs;
+    const LaOp& op = a.op[op_i];
+    const int DK = op.DK, DV = op.DV;
+    if (c0 >= DV) return;
     const int h = bh % a.H, b = bh / a.H;
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, half = lane / 32, l32 = lane % 32, pl = perm(l32);
     const int N = static_cast<int>(a.T), len = seq_len(a.lengths, b, N), vec = g.vec[op_i];
     const bool reverse = op.reverse;
-    const int DK = op.DK, DV = op.DV;
     const int i_begin = static_cast<int>(sg * g.seg);
     const int i_end = static_cast<int>(min(static_cast<int64_t>(N), (sg + 1) * g.seg));
     const int n_end = min(i_end, len);                   // tokens that count
     const double gl = a.log_decay[h];
 
+    constexpr int RP = decltype(sh)::RP, CP = decltype(sh)::CP;
+    Stage<T, C, DKP, NT, true> kst;
+    Stage<T, C, DKP, NT, false> qst;
+    Stage<T, C, 32 * NW, NT, true> vst;
+    {
+        const int64_t t0 = reverse ? len - 1 - i_begin : i_begin;
+        const int sign = reverse ? -1 : 1;
+        kst.open(static_cast<const T*>(op.k.p) + b * op.k.sb + (h / op.k.div) * op.k.sh + t0 * op.k.st, sign * op.k.st, vec & 2, 0, DK);
+        vst.open(static_cast<const T*>(op.v.p) + b * op.v.sb + (h / op.v.div) * op.v.sh + t0 * op.v.st, sign * op.v.st, vec & 4, c0, DV);
+        if (OUT)
+            qst.open(static_cast<const T*>(op.q.p) + b * op.q.sb + (h / op.q.div) * op.q.sh + t0 * op.q.st, sign * op.q.st, vec & 1, 0, DK);
+    }
+    if (i_begin < n_end) {
+        kst.load(n_end - i_begin);
+        vst.load(n_end - i_begin);
+        if (OUT) qst.load(n_end - i_begin);
+    }
+
     if (tid <= C) sh.pw[tid] = tid == 0 ? 1.0f : static_cast<float>(exp(gl * tid));
     __syncthreads();
     if (tid < C) sh.w[tid] = op.ws * sh.pw[C - 1 - tid + (reverse ? 1 : 0)];
+    if (tid < 32) sh.back[tid] = sh.pw[32 - tid];
 
-    // this lane's decays between tokens of a tile pair, times the scale
-    float mdiag[OUT ? 16 : 1], moff[OUT && IT > 1 ? 16 : 1];
+    // this lane's decays between tokens of one tile, times the scale
+    float mdiag[OUT ? 16 : 1];
     const float pscale = op.inter * op.ws;
-    if (OUT) {
+    const float down = pscale * sh.pw[l32];
+    if (OUT)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const int d = l32 - (16 * (r / 8) + 8 * half + r % 8);
             mdiag[r] = d >= 0 ? pscale * sh.pw[d < 0 ? 0 : d] : 0.0f;
-            if (IT > 1) moff[r] = pscale * sh.pw[32 + d];
         }
-    }
 
     const int64_t state_at = static_cast<int64_t>(bh) * DK * DV;
     const int col = c0 + 32 * wave + pl;                 // this lane's column of the state
     f32x16 S[KT];
-    {
-        const float* from = OUT ? (sg > 0 ? g.carry[op_i] + static_cast<int64_t>(sg - 1) * a.B * a.H * DK * DV : op.s_in) : nullptr;
-        const int sk = sg > 0 ? DV : op.s_k, sv = sg > 0 ? 1 : op.s_v;
+    const float* from = OUT ? (sg > 0 ? g.carry[op_i] + static_cast<int64_t>(sg - 1) * a.B * a.H * DK * DV : op.s_in) : nullptr;
+#pragma unroll
+    for (int t = 0; t < KT; ++t) S[t] = (f32x16)(0.0f);
+    if (from) {
+        const int sk = sg > 0 ? g.c_k[op_i] : op.s_k, sv = sg > 0 ? g.c_v[op_i] : op.s_v;
+        const float* at = from + state_at + min(col, DV - 1) * sv;
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int row = 32 * t + 16 * (r / 8) + 8 * half + r % 8;
-                S[t][r] = from && row < DK && col < DV ? from[state_at + row * sk + col * sv] : 0.0f;
+                const float v = at[min(row, DK - 1) * sk];
+                S[t][r] = row < DK && col < DV ? v : 0.0f;
             }
     }
+    const bf16* q_at = sh.q + l32 * RP + 8 * half;       // this lane's first fragments
+    const bf16* k_at = sh.k + pl * RP + 8 * half;
+    const bf16* kt_at = sh.kt + pl * CP + 8 * half;
+    const bf16* vt_at = sh.vt + (32 * wave + pl) * CP + 8 * half;
 
-    const T* kb = static_cast<const T*>(op.k.p) + b * op.k.sb + (h / op.k.div) * op.k.sh;
-    const T* vb = static_cast<const T*>(op.v.p) + b * op.v.sb + (h / op.v.div) * op.v.sh;
-    const T* qb = static_cast<const T*>(op.q.p) + b * op.q.sb + (h / op.q.div) * op.q.sh;
-    Stage<T, C, DKP, NT> kst, qst;
-    Stage<T, C, 32 * NW, NT> vst;
-    if (i_begin < n_end) {
-        kst.load(kb, op.k.st, vec & 2, 0, DK, i_begin, n_end, len - 1, reverse);
-        vst.load(vb, op.v.st, vec & 4, c0, DV, i_begin, n_end, len - 1, reverse);
-        if (OUT) qst.load(qb, op.q.st, vec & 1, 0, DK, i_begin, n_end, len - 1, reverse);
-    }
     for (int i0 = i_begin; i0 < n_end; i0 += C) {
         const int L = min(C, n_end - i0);
         __syncthreads();                                  // the chunk before is read
-        kst.template store<OUT, true>(sh.k, sh.kt);
-        vst.template store<false, true>(nullptr, sh.vt);
-        if (OUT) qst.template store<true, false>(sh.q, nullptr);
+        kst.template store<OUT, RP, CP>(sh.k, sh.kt);
+        vst.template store<false, RP, CP>(nullptr, sh.vt);
+        if (OUT) qst.template store<true, RP, CP>(sh.q, nullptr);
         if (L < C && tid < C) sh.w[tid] = tid < L ? op.ws * sh.pw[L - 1 - tid + (reverse ? 1 : 0)] : 0.0f;
         __syncthreads();
-        if (i0 + C < n_end) {
-            kst.load(kb, op.k.st, vec & 2, 0, DK, i0 + C, n_end, len - 1, reverse);
-            vst.load(vb, op.v.st, vec & 4, c0, DV, i0 + C, n_end, len - 1, reverse);
-            if (OUT) qst.load(qb, op.q.st, vec & 1, 0, DK, i0 + C, n_end, len - 1, reverse);
-        }
         bf16x8 vf[C / 16][NP];
 #pragma unroll
         for (int t = 0; t < C / 16; ++t)
 #pragma unroll
-            for (int n = 0; n < NP; ++n)
-                vf[t][n] = *reinterpret_cast<const bf16x8*>(
-                    sh.vt + n * C * 32 * NW + block_at<C / 8>(32 * wave + pl, 2 * t + half));
+            for (int n = 0; n < NP; ++n) vf[t][n] = fragment(vt_at + n * 32 * NW * CP + 16 * t);
         if (OUT) {
             f32x16 P[IT][IT], O[IT];                       // P[i][j], j <= i
 #pragma unroll
@@ -332,8 +411,8 @@ __global__ __launch_bounds__(64 * NW) void la_chunk(LaChunkArgs g) {
                 for (int i = 0; i < IT; ++i)
 #pragma unroll
                     for (int n = 0; n < NP; ++n) {
-                        qf[i][n] = *reinterpret_cast<const bf16x8*>(sh.q + n * C * DKP + block_at<DKP / 8>(32 * i + l32, 2 * t + half));
-                        kf[i][n] = *reinterpret_cast<const bf16x8*>(sh.k + n * C * DKP + block_at<DKP / 8>(32 * i + pl, 2 * t + half));
+                        qf[i][n] = fragment(q_at + (n * C + 32 * i) * RP + 16 * t);
+                        kf[i][n] = fragment(k_at + (n * C + 32 * i) * RP + 16 * t);
                     }
                 float s8[8];
 #pragma unroll
@@ -347,21 +426,29 @@ __global__ __launch_bounds__(64 * NW) void la_chunk(LaChunkArgs g) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const float f = op.inter * sh.pw[32 * i + l32 + (reverse ? 0 : 1)];
-                O[i] *= f;
+            for (int i = 0; i < IT; ++i) O[i] *= op.inter * sh.pw[32 * i + l32 + (reverse ? 0 : 1)];
 #pragma unroll
-                for (int j = 0; j <= i; ++j) {
+            for (int i = 0; i < IT; ++i)
+#pragma unroll
+                for (int j = 0; j <= i; ++j)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         float p8[8];
                         bf16x8 pf[LIM];
+                        if (i == j) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) p8[e] = P[i][j][8 * t + e] * (i == j ? mdiag[8 * t + e] : moff[8 * t + e]);
+                            for (int e = 0; e < 8; ++e) p8[e] = P[i][j][8 * t + e] * mdiag[8 * t + e];
+                        } else {
+                            const Pack<float, 4> b0 = *reinterpret_cast<const Pack<float, 4>*>(sh.back + 16 * t + 8 * half);
+                            const Pack<float, 4> b1 = *reinterpret_cast<const Pack<float, 4>*>(sh.back + 16 * t + 8 * half + 4);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) p8[e] = P[i][j][8 * t + e] * (down * (e < 4 ? b0.v[e % 4] : b1.v[e % 4]));
+                        }
                         split<LIM>(p8, pf);
                         O[i] = product<NP, LIM, LIM>(vf[2 * j + t], pf, O[i]);
                     }
-                }
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
                 const int row = 32 * i + l32;
                 if (row < L) {
                     const int64_t tok = reverse ? len - 1 - (i0 + row) : i0 + row;
@@ -375,26 +462,17 @@ __global__ __launch_bounds__(64 * NW) void la_chunk(LaChunkArgs g) {
                 }
             }
         }
+        // the next chunk's loads: in flight over the state's products
+        if (i0 + C < n_end) {
+            const int left = n_end - i0 - C;
+            kst.load(left);
+            vst.load(left);
+            if (OUT) qst.load(left);
+        }
         const float decay = sh.pw[L];
 #pragma unroll
         for (int t = 0; t < KT; ++t) S[t] *= decay;
-#pragma unroll
-        for (int t = 0; t < C / 16; ++t) {
-            float v8[8];
-            bf16x8 wv[3];
-            sum_parts<NP>(vf[t], v8);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v8[e] *= sh.w[16 * t + 8 * half + e];
-            split<3>(v8, wv);
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                bf16x8 kf[NP];
-#pragma unroll
-                for (int n = 0; n < NP; ++n)
-                    kf[n] = *reinterpret_cast<const bf16x8*>(sh.kt + n * C * DKP + block_at<C / 8>(32 * kt + pl, 2 * t + half));
-                S[kt] = product<NP, 3, 3>(kf, wv, S[kt]);
-            }
-        }
+        add_tokens<T, DKP, CP, EXACT ? 3 : LIM>(S, kt_at, sh.w + 8 * half, vf);
     }
     if (OUT) {
         // padding rows
@@ -409,14 +487,23 @@ __global__ __launch_bounds__(64 * NW) void la_chunk(LaChunkArgs g) {
         }
     }
     float* to = OUT ? (sg == segs - 1 ? op.s_out : nullptr) : g.carry[op_i] + static_cast<int64_t>(sg) * a.B * a.H * DK * DV;
-    if (to && col < DV)
+    if (to && col < DV) {
+        to += state_at + col;
+        if (DK == DKP) {
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
+            for (int t = 0; t < KT; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = 32 * t + 16 * (r / 8) + 8 * half + r % 8;
-                if (row < DK) to[state_at + static_cast<int64_t>(row) * DV + col] = S[t][r];
-            }
+                for (int r = 0; r < 16; ++r) to[(32 * t + 16 * (r / 8) + 8 * half + r % 8) * DV] = S[t][r];
+        } else {
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int row = 32 * t + 16 * (r / 8) + 8 * half + r % 8;
+                    if (row < DK) to[row * DV] = S[t][r];
+                }
+        }
+    }
 }
 
 // Columns per workgroup of a launch, and its padded rows.
@@ -439,11 +526,19 @@ hipError_t launch_chunks(const LaChunkArgs& g, bool out, hipStream_t st) {
     }
     const int nw = la_waves(g.a);
     const int segs = out ? g.n_seg : g.n_seg - 1;
-    const dim3 grid(static_cast<uint32_t>(g.a.B * g.a.H * segs), (dv + 32 * nw - 1) / (32 * nw), g.a.n_ops);
+    const int col_blocks = (dv + 32 * nw - 1) / (32 * nw);
+    const dim3 grid(static_cast<uint32_t>(g.a.B * g.a.H * segs * g.a.n_ops * col_blocks));
     auto go = [&](auto rows, auto waves) {
         constexpr int DKP = decltype(rows)::value, NW = decltype(waves)::value;
-        if (out) la_chunk<T, DKP, NW, true><<<grid, 64 * NW, 0, st>>>(g);
-        else la_chunk<T, DKP, NW, false><<<grid, 64 * NW, 0, st>>>(g);
+        bool exact = Parts<T>::LIM == 3;
+        for (int w = 0; w < g.a.n_ops; ++w) exact = exact || g.a.op[w].exact;
+        if (exact) {
+            if (out) la_chunk<T, DKP, NW, true, true><<<grid, 64 * NW, 0, st>>>(g, col_blocks);
+            else la_chunk<T, DKP, NW, false, true><<<grid, 64 * NW, 0, st>>>(g, col_blocks);
+        } else if constexpr (Parts<T>::LIM < 3) {
+            if (out) la_chunk<T, DKP, NW, true, false><<<grid, 64 * NW, 0, st>>>(g, col_blocks);
+            else la_chunk<T, DKP, NW, false, false><<<grid, 64 * NW, 0, st>>>(g, col_blocks);
+        }
         return hipGetLastError();
     };
     using std::integral_constant;

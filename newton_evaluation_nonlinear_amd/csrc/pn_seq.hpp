@@ -44,6 +44,8 @@ struct LaOp {
     const float* s_in;       // [B, H, ., .] or null; element (x, y) at x * s_k + y * s_v
     int32_t s_k, s_v;
     float* s_out;            // [B, H, DK, DV] or null
+    int32_t exact;           // 1: the state is a result, not only a term of 16-bit outputs
+    int32_t carry_from;      // the operator whose states between segments this one reads
 };
 struct LaArgs {
     LaOp op[3];

@@ -195,6 +195,7 @@ LinattnPlan plan_linattn(const pn_linattn_args& a, bool backward) {
         f.s_k = dv;
         f.s_v = 1;
         f.s_out = a.final_state;
+        f.exact = a.final_state != nullptr;
         g.n_ops = 1;
     } else {
         if (share > 1) {
@@ -231,6 +232,8 @@ LinattnPlan plan_linattn(const pn_linattn_args& a, bool backward) {
         v.s_k = dv;
         v.s_v = 1;
         v.s_out = a.d_initial_state;
+        v.exact = a.d_initial_state != nullptr;
+        v.carry_from = 1;
         // dk: R again, transposed
         LaOp& k = g.op[2];
         k.q = operand(a.v, share);
@@ -246,6 +249,7 @@ LinattnPlan plan_linattn(const pn_linattn_args& a, bool backward) {
         k.s_in = a.d_final_state;
         k.s_k = 1;
         k.s_v = dv;
+        k.carry_from = 1;
         g.n_ops = 3;
     }
     p.off_carry = p.total;
