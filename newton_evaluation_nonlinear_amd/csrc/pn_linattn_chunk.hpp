@@ -266,8 +266,14 @@ struct alignas(16) LaShared {
     alignas(16) bf16 vt[NP * NW * 32 * CP];
     alignas(16) float w[C];         // weights of V in the state
     alignas(16) float back[32];     // lam^{32 - j}
+    float m[64];                    // at 31 - i + j: scale lam^{i - j}, 0 for i < j
     float pw[C + 4];                // lam^0 .. lam^C
 };
+
+// Waves per SIMD (4 to a compute unit): two where two workgroups of four waves,
+// or four of two, fit into 160 KB of LDS.
+template <typename T, int DKP, int NW, bool OUT>
+constexpr int la_occupancy() { return sizeof(LaShared<T, DKP, NW, OUT>) * (8 / NW) <= 160 * 1024 ? 2 : 1; }
 
 __device__ __forceinline__ bf16x8 fragment(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
@@ -302,7 +308,7 @@ __device__ __forceinline__ void add_tokens(f32x16* S, const bf16* kt, const floa
 // that a segment leaves alone (from zero), for the scan over segments.
 // EXACT: the state is a result, not only a term of 16-bit outputs.
 template <typename T, int DKP, int NW, bool OUT, bool EXACT>
-__global__ __launch_bounds__(64 * NW, 2) void la_chunk(LaChunkArgs g, int col_blocks) {
+__global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, NW, OUT>())) void la_chunk(LaChunkArgs g, int col_blocks) {
     constexpr int NP = Parts<T>::NP, LIM = Parts<T>::LIM, C = Parts<T>::C, NT = 64 * NW;
     constexpr int KT = DKP / 32, IT = C / 32;
     __shared__ LaShared<T, DKP, NW, OUT> sh;
@@ -349,16 +355,9 @@ __global__ __launch_bounds__(64 * NW, 2) void la_chunk(LaChunkArgs g, int col_bl
     if (tid < C) sh.w[tid] = op.ws * sh.pw[C - 1 - tid + (reverse ? 1 : 0)];
     if (tid < 32) sh.back[tid] = sh.pw[32 - tid];
 
-    // this lane's decays between tokens of one tile, times the scale
-    float mdiag[OUT ? 16 : 1];
     const float pscale = op.inter * op.ws;
     const float down = pscale * sh.pw[l32];
-    if (OUT)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int d = l32 - (16 * (r / 8) + 8 * half + r % 8);
-            mdiag[r] = d >= 0 ? pscale * sh.pw[d < 0 ? 0 : d] : 0.0f;
-        }
+    if (OUT && tid < 64) sh.m[tid] = tid < 32 ? pscale * sh.pw[31 - tid] : 0.0f;
 
     const int64_t state_at = static_cast<int64_t>(bh) * DK * DV;
     const int col = c0 + 32 * wave + pl;                 // this lane's column of the state
@@ -391,11 +390,22 @@ __global__ __launch_bounds__(64 * NW, 2) void la_chunk(LaChunkArgs g, int col_bl
         if (OUT) qst.template store<true, RP, CP>(sh.q, nullptr);
         if (L < C && tid < C) sh.w[tid] = tid < L ? op.ws * sh.pw[L - 1 - tid + (reverse ? 1 : 0)] : 0.0f;
         __syncthreads();
+        // the next chunk's loads: in flight over this chunk's products, and ahead
+        // of its stores, which complete in order with them
+        if (i0 + C < n_end) {
+            const int left = n_end - i0 - C;
+            kst.load(left);
+            vst.load(left);
+            if (OUT) qst.load(left);
+        }
         bf16x8 vf[C / 16][NP];
+        auto load_v = [&]() {
 #pragma unroll
-        for (int t = 0; t < C / 16; ++t)
+            for (int t = 0; t < C / 16; ++t)
 #pragma unroll
-            for (int n = 0; n < NP; ++n) vf[t][n] = fragment(vt_at + n * 32 * NW * CP + 16 * t);
+                for (int n = 0; n < NP; ++n) vf[t][n] = fragment(vt_at + n * 32 * NW * CP + 16 * t);
+        };
+        if (!OUT) load_v();
         if (OUT) {
             f32x16 P[IT][IT], O[IT];                       // P[i][j], j <= i
 #pragma unroll
@@ -427,6 +437,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_chunk(LaChunkArgs g, int col_bl
             }
 #pragma unroll
             for (int i = 0; i < IT; ++i) O[i] *= op.inter * sh.pw[32 * i + l32 + (reverse ? 0 : 1)];
+            load_v();
 #pragma unroll
             for (int i = 0; i < IT; ++i)
 #pragma unroll
@@ -435,15 +446,9 @@ __global__ __launch_bounds__(64 * NW, 2) void la_chunk(LaChunkArgs g, int col_bl
                     for (int t = 0; t < 2; ++t) {
                         float p8[8];
                         bf16x8 pf[LIM];
-                        if (i == j) {
+                        const float* m = i == j ? sh.m + 31 - l32 + 8 * half : sh.back + 8 * half;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) p8[e] = P[i][j][8 * t + e] * mdiag[8 * t + e];
-                        } else {
-                            const Pack<float, 4> b0 = *reinterpret_cast<const Pack<float, 4>*>(sh.back + 16 * t + 8 * half);
-                            const Pack<float, 4> b1 = *reinterpret_cast<const Pack<float, 4>*>(sh.back + 16 * t + 8 * half + 4);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) p8[e] = P[i][j][8 * t + e] * (down * (e < 4 ? b0.v[e % 4] : b1.v[e % 4]));
-                        }
+                        for (int e = 0; e < 8; ++e) p8[e] = P[i][j][8 * t + e] * (i == j ? m[16 * t + e] : down * m[16 * t + e]);
                         split<LIM>(p8, pf);
                         O[i] = product<NP, LIM, LIM>(vf[2 * j + t], pf, O[i]);
                     }
@@ -461,13 +466,6 @@ __global__ __launch_bounds__(64 * NW, 2) void la_chunk(LaChunkArgs g, int col_bl
                     }
                 }
             }
-        }
-        // the next chunk's loads: in flight over the state's products
-        if (i0 + C < n_end) {
-            const int left = n_end - i0 - C;
-            kst.load(left);
-            vst.load(left);
-            if (OUT) qst.load(left);
         }
         const float decay = sh.pw[L];
 #pragma unroll
