@@ -371,8 +371,9 @@ int pn_qk_norm_rotary(const pn_rotary_args* a);
  * gradients of q and k, dqw and dkw those of the weights (sums in a fixed
  * order: the same bits on every run).  No output may overlap an input. */
 int pn_qk_norm_rotary_backward(const pn_rotary_args* a);
-/* Workspace bytes of pn_qk_norm_rotary_backward (the other two need none);
- * 0 with the error set for invalid arguments.  Pointers are not looked at. */
+/* Workspace bytes of pn_qk_norm_rotary_backward (the other two need none), a
+ * function of sizes alone; 256 means that none is needed, 0 invalid
+ * arguments, with the error set.  Pointers are not looked at. */
 size_t pn_qk_norm_rotary_workspace_bytes(const pn_rotary_args* a);
 
 /* Linear attention with a decay per head.  For each sequence and head,
@@ -409,8 +410,9 @@ int pn_linear_attention(const pn_linattn_args* a);
 /* Gradients of q, k, v (summed over the heads that share them) and of the
  * initial state; the decay is a constant of the layer. */
 int pn_linear_attention_backward(const pn_linattn_args* a);
-/* Workspace bytes of the two; 0 with the error set for invalid arguments.
- * Pointers are not looked at, except for NULL. */
+/* Workspace bytes of the two, a function of dtype and sizes alone; 256 means
+ * that none is needed (workspace may be NULL), 0 invalid arguments, with the
+ * error set.  Pointers are not looked at. */
 size_t pn_linear_attention_workspace_bytes(const pn_linattn_args* a, int32_t backward);
 
 /* One token for each of B sequences (serving): the state is updated in place

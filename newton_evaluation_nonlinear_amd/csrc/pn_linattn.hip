@@ -14,8 +14,6 @@
 namespace pn {
 namespace {
 
-constexpr int kCols = 64;
-
 // The state before each segment from the states the segments leave alone:
 //     S_{n+1} = lam^{tokens of n} S_n + U_n,
 // in place, element by element; slot n holds U_n, then S_{n+1}.
@@ -33,11 +31,19 @@ __global__ __launch_bounds__(256) void la_carry(LaChunkArgs g) {
     const float whole = static_cast<float>(exp(gl * static_cast<double>(g.seg)));
     float s = op.s_in ? op.s_in[bh * n + row * op.s_k + col * op.s_v] : 0.0f;
     float* u = g.carry[blockIdx.y] + e;
-    for (int i = 0; i + 1 < g.n_seg; ++i) {
-        const int64_t left = len - i * g.seg;
-        const float d = left >= g.seg ? whole : (left <= 0 ? 1.0f : static_cast<float>(exp(gl * static_cast<double>(left))));
-        s = d * s + u[i * total];
-        u[i * total] = s;
+    const int slots = g.n_seg - 1;
+    for (int i0 = 0; i0 < slots; i0 += 8) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = i0 + j < slots ? u[(i0 + j) * total] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (i0 + j >= slots) break;
+            const int64_t left = len - (i0 + j) * g.seg;
+            const float d = left >= g.seg ? whole : (left <= 0 ? 1.0f : static_cast<float>(exp(gl * static_cast<double>(left))));
+            s = d * s + x[j];
+            u[(i0 + j) * total] = s;
+        }
     }
 }
 
@@ -80,41 +86,105 @@ __global__ __launch_bounds__(256) void la_group_sum(const float* in, T* out, int
     out[e] = from_f32<T>(s);
 }
 
-template <typename T>
+// One token.  The state is read and written once, 8 DK DV bytes for 5 DK DV
+// operations: bandwidth, or latency where there are few heads.  A workgroup
+// takes LC * V columns of a head: LC lanes of V columns by 256 / LC groups of
+// rows, every group 8 rows at a time, all loads of which are issued before
+// the first store.  For a slow decay lam S + k v is taken as
+// S + (S (lam - 1) + k v): lam - 1 keeps it exact over many steps, where lam
+// itself, rounded, would be off by up to 2^-25 at each.
+template <typename T, int V, int LC>
 __global__ __launch_bounds__(256) void la_step(pn_linattn_step_args a) {
-    __shared__ float sq[256], sk[256], part[4][kCols];
-    const int tid = threadIdx.x, col = tid % kCols, wv = tid / kCols;
+    constexpr int RG = 256 / LC, ROWS = 8;
+    __shared__ float sq[256 + RG * ROWS], sk[256 + RG * ROWS], part[4][LC * V];
+    const int tid = threadIdx.x, lane = tid % LC, group = tid / LC;
     const int H = static_cast<int>(a.H), DK = static_cast<int>(a.dk), DV = static_cast<int>(a.dv);
     const int h = blockIdx.x % H, b = blockIdx.x / H;
-    const int vv = blockIdx.y * kCols + col;
-    const bool live = vv < DV;
+    const int c = (blockIdx.y * LC + lane) * V;
+    const bool live = c < DV;                            // V divides DV
     const int64_t slot = a.slots ? a.slots[b] : b;
+    const bool idle = slot < 0 || slot >= a.n_slots;
     T* o = static_cast<T*>(a.o) + (static_cast<int64_t>(b) * H + h) * DV;
-    if (slot < 0 || slot >= a.n_slots) {
-        if (wv == 0 && live) o[vv] = from_f32<T>(0.0f);
+    if (idle) {
+        if (group == 0 && live)
+            for (int i = 0; i < V; ++i) o[c + i] = from_f32<T>(0.0f);
         return;
     }
     const int hk = h / static_cast<int>(a.H / a.HK);
     const T* qp = static_cast<const T*>(a.q.p) + b * a.q.sb + h * a.q.sh;
     const T* kp = static_cast<const T*>(a.k.p) + b * a.k.sb + hk * a.k.sh;
     const T* vp = static_cast<const T*>(a.v.p) + b * a.v.sb + hk * a.v.sh;
-    sq[tid] = tid < DK ? to_f32(qp[tid]) : 0.0f;
-    sk[tid] = tid < DK ? to_f32(kp[tid]) : 0.0f;
-    const float v = live ? to_f32(vp[vv]) : 0.0f;
-    __syncthreads();
-    const float lam = expf(a.log_decay[h]);
-    float* S = a.state + (slot * H + h) * DK * DV;
-    float s = 0.0f;
-    for (int r = wv; r < DK; r += 4)
-        if (live) {
-            const float n = lam * S[r * DV + vv] + sk[r] * v;
-            S[r * DV + vv] = n;
-            s += sq[r] * n;
+    float* S = a.state + (slot * H + h) * DK * DV + c;
+    const float g = a.log_decay[h];
+    const bool slow = g > -0.5f;
+    const float f = slow ? expm1f(g) : expf(g);
+    float x[ROWS][V], acc[V], v[V];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+            const int r = r0 + j * RG + group;
+            Pack<float, V> p{};
+            if (live && r < DK) p = *reinterpret_cast<const Pack<float, V>*>(S + r * DV);
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[j][i] = p.v[i];
         }
-    part[wv][col] = s;
+    };
+    load(0);
+    for (int r = tid; r < 256 + RG * ROWS; r += 256) {
+        sq[r] = r < DK ? to_f32(qp[r]) : 0.0f;
+        sk[r] = r < DK ? to_f32(kp[r]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        v[i] = live ? to_f32(vp[c + i]) : 0.0f;
+        acc[i] = 0.0f;
+    }
     __syncthreads();
-    if (wv == 0 && live)
-        o[vv] = from_f32<T>(static_cast<float>(a.scale) * (part[0][col] + part[1][col] + part[2][col] + part[3][col]));
+    for (int r0 = 0;;) {
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+            const int r = r0 + j * RG + group;
+            const float k = sk[r], q = sq[r];
+            Pack<float, V> n;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float t = fmaf(x[j][i], f, k * v[i]);
+                n.v[i] = slow ? x[j][i] + t : t;
+                acc[i] = fmaf(q, n.v[i], acc[i]);
+            }
+            if (live && r < DK) *reinterpret_cast<Pack<float, V>*>(S + r * DV) = n;
+        }
+        r0 += RG * ROWS;
+        if (r0 >= DK) break;
+        load(r0);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int m = LC; m < 64; m *= 2) acc[i] += __shfl_xor(acc[i], m);
+    if (tid % 64 < LC)
+#pragma unroll
+        for (int i = 0; i < V; ++i) part[tid / 64][lane * V + i] = acc[i];
+    __syncthreads();
+    if (group == 0 && live)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            o[c + i] = from_f32<T>(static_cast<float>(a.scale) * (part[0][lane * V + i] + part[1][lane * V + i] +
+                                                                  part[2][lane * V + i] + part[3][lane * V + i]));
+}
+
+template <typename T>
+hipError_t step_typed(const pn_linattn_step_args& a, hipStream_t st) {
+    const uint32_t heads = static_cast<uint32_t>(a.B * a.H);
+    const uint32_t dv = static_cast<uint32_t>(a.dv);
+    if (a.dv % 4 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0) {
+        // 32 columns per workgroup while that is what fills the device
+        if (heads * ((dv + 127) / 128) >= 2048) la_step<T, 4, 32><<<dim3(heads, (dv + 127) / 128), 256, 0, st>>>(a);
+        else la_step<T, 4, 8><<<dim3(heads, (dv + 31) / 32), 256, 0, st>>>(a);
+    } else {
+        la_step<T, 1, 32><<<dim3(heads, (dv + 31) / 32), 256, 0, st>>>(a);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -187,13 +257,11 @@ hipError_t launch_group_sum(const float* in, void* out, int dtype, int64_t rows,
 }
 
 hipError_t launch_linattn_step(const pn_linattn_step_args& a, hipStream_t st) {
-    const dim3 grid(static_cast<uint32_t>(a.B * a.H), static_cast<uint32_t>((a.dv + kCols - 1) / kCols));
     switch (a.dtype) {
-        case PN_F32: la_step<float><<<grid, 256, 0, st>>>(a); break;
-        case PN_BF16: la_step<bf16><<<grid, 256, 0, st>>>(a); break;
-        default: la_step<f16><<<grid, 256, 0, st>>>(a); break;
+        case PN_F32: return step_typed<float>(a, st);
+        case PN_BF16: return step_typed<bf16>(a, st);
+        default: return step_typed<f16>(a, st);
     }
-    return hipGetLastError();
 }
 
 }  // namespace pn

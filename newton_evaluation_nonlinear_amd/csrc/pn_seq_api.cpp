@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -73,6 +74,9 @@ int check_tokens(const pn_tokens& x, const char* name, int64_t elem) {
         const int rc_ = (call);           \
         if (rc_ != PN_OK) return rc_;     \
     } while (0)
+
+// Never kAlign, which says that none is needed.
+size_t norm_workspace(const pn_rotary_args& a) { return std::max(align_up(rotary_backward_workspace(a)), 2 * kAlign); }
 
 int check_rotary_sizes(const pn_rotary_args& a, bool norm) {
     if (a.dtype < PN_F32 || a.dtype > PN_F16) return fail(PN_EINVAL, "unknown storage type %lld", (long long)a.dtype);
@@ -254,6 +258,7 @@ LinattnPlan plan_linattn(const pn_linattn_args& a, bool backward) {
     }
     p.off_carry = p.total;
     p.total += align_up(linattn_workspace(g));
+    if (p.total > 0) p.total = std::max(p.total, 2 * kAlign);
     return p;
 }
 
@@ -350,7 +355,7 @@ size_t pn_qk_norm_rotary_workspace_bytes(const pn_rotary_args* a) {
     }
     if (check_rotary_sizes(*a, true) != PN_OK) return 0;
     if (a->B == 0 || a->T == 0 || a->hq == 0) return kAlign;
-    return align_up(rotary_backward_workspace(*a));
+    return norm_workspace(*a);
 }
 
 int pn_qk_norm_rotary_backward(const pn_rotary_args* a) {
@@ -366,7 +371,7 @@ int pn_qk_norm_rotary_backward(const pn_rotary_args* a) {
         }
         return PN_OK;
     }
-    const size_t need = align_up(rotary_backward_workspace(*a));
+    const size_t need = norm_workspace(*a);
     if (!a->workspace || a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < need)
         return fail(PN_EWORKSPACE, "a workspace of %zu bytes is needed", need);
     if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign)

@@ -14,13 +14,16 @@ import struct
 import torch
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_raw_stream = torch.cuda.current_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 # Argument blocks of include/pn.h: every field is 8 bytes wide.
-_ROTARY = struct.Struct("=9q8q2q3q4qd2q2q8q2q3q")
-_ATTENTION = struct.Struct("=7qd2q12q3q4q5q3q")
-_STEP = struct.Struct("=6qdq12q5q")
+_ROTARY = struct.Struct("=9q8q2q3q4qd2q2q8q2q3q").pack
+_ATTENTION = struct.Struct("=7qd2q12q3q4q5q3q").pack
+_STEP = struct.Struct("=6qdq12q5q").pack
 _NO_TOKENS = (0, 0, 0, 0)
+_entries = {}            # entries of the loaded library
+_sizes = {}              # workspace bytes by entry and sizes
 
 
 def declare(L):
@@ -43,67 +46,87 @@ EXPORTED = ("pn_rotary_table", "pn_rotary", "pn_qk_norm_rotary", "pn_qk_norm_rot
             "pn_linear_attention_workspace_bytes", "pn_linear_attention_step")
 
 
-def _run(device, name, *args):
-    from . import PnError, last_error, lib
+def _entry(name):
+    from . import lib
     fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
+    _entries[name] = fn
+    return fn
+
+
+def _fail(rc):
+    from . import PnError, last_error
+    raise PnError(rc, last_error())
+
+
+def _run(index, name, *args):
+    """Call an entry on the device of its tensors."""
+    fn = _entries.get(name) or _entry(name)
+    if index == _current_device():
         rc = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args)
     if rc < 0:
-        raise PnError(rc, last_error())
+        _fail(rc)
 
 
-def _workspace(device, name, *args):
-    """A 256-byte aligned workspace of the size the entry asks for: (tensor, address, bytes)."""
-    from . import EINVAL, PnError, last_error, lib
-    n = getattr(lib(), name)(*args)
-    if n == 0:
-        raise PnError(EINVAL, last_error())
-    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
-    base = ws.data_ptr()
-    aligned = (base + 255) // 256 * 256
-    return ws, aligned, n
+def _workspace(like, name, key, *args):
+    """(tensor, address, bytes) of a 256-byte aligned workspace; the size is asked for once for the sizes in ``key``."""
+    n = _sizes.get(key)
+    if n is None:
+        n = (_entries.get(name) or _entry(name))(*args)
+        if n == 0:
+            _fail(-1)
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        _sizes[key] = n
+    if n <= 256:                                         # none needed
+        return None, 0, 0
+    ws = torch.empty(n + 256, dtype=torch.uint8, device=like.device)
+    return ws, (ws.data_ptr() + 255) & -256, n
 
 
-def _tokens(t, name, shape, dtype, device):
+def _tokens(t, name, shape, dtype, index):
     """(address, strides) of a token tensor; raises on what the library cannot take."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
     s = t.stride()
     if s[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"the channels of {name} must be adjacent (stride 1, got {s[-1]})")
     return (t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else (t.data_ptr(), s[0], 0, s[1])
 
 
-def _array(t, name, dtype, shape, device):
+def _array(t, name, dtype, shape, index):
     """Address of a contiguous array (None: 0)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} CUDA (HIP) tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
     return t.data_ptr()
 
 
 def _first(t, name, dims):
+    """(shape, dtype, its code, device index) of the tensor that the others have to agree with."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
-    return t.shape, t.dtype, t.device
+    dt = t.dtype
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dt}")
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(shape)}")
+    return shape, dt, code, t.get_device()
 
 
 # ---------------------------------------------------------------- rotary positions
@@ -156,47 +179,49 @@ def rotary_table(n_pos, frequencies, magnitude=1.0, device="cuda"):
         device = torch.device("cuda", torch.cuda.current_device())
     f = [float(x) for x in frequencies]
     table = torch.empty((int(n_pos), len(f), 2), dtype=torch.float32, device=device)
-    _run(device, "pn_rotary_table", (ctypes.c_double * max(1, len(f)))(*f), len(f), int(n_pos), float(magnitude),
-         table.data_ptr(), _raw_stream(device).cuda_stream)
+    _run(device.index, "pn_rotary_table", (ctypes.c_double * max(1, len(f)))(*f), len(f), int(n_pos), float(magnitude),
+         table.data_ptr(), _raw_stream(device.index))
     return table
 
 
-def _positions(positions, B, T, device):
+def _positions(positions, B, T, index):
     """(address, is int64, batch stride, token stride) of positions [B, T] or [T]."""
     if positions is None:
         return 0, 0, 0, 0
-    if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype not in (torch.int32, torch.int64):
+    if not isinstance(positions, torch.Tensor) or not positions.is_cuda:
         raise TypeError("positions must be an int32 or int64 CUDA (HIP) tensor")
-    if positions.device != device:
-        raise ValueError(f"positions must be on {device}")
+    dt = positions.dtype
+    if dt is not torch.int32 and dt is not torch.int64:
+        raise TypeError("positions must be an int32 or int64 CUDA (HIP) tensor")
+    if positions.get_device() != index:
+        raise ValueError(f"positions must be on cuda:{index}")
     s = positions.stride()
     if positions.shape == (B, T):
-        sb, st = s
-    elif positions.shape == (T,):
-        sb, st = 0, s[0]
-    else:
-        raise ValueError(f"positions must have shape {(B, T)} or {(T,)}, got {tuple(positions.shape)}")
-    return positions.data_ptr(), int(positions.dtype == torch.int64), sb, st
+        return positions.data_ptr(), int(dt is torch.int64), s[0], s[1]
+    if positions.shape == (T,):
+        return positions.data_ptr(), int(dt is torch.int64), 0, s[0]
+    raise ValueError(f"positions must have shape {(B, T)} or {(T,)}, got {tuple(positions.shape)}")
 
 
-def _table(table, D, device):
-    if not isinstance(table, torch.Tensor) or not table.is_cuda or table.dtype != torch.float32 or not table.is_contiguous():
+def _table(table, D, index):
+    if not isinstance(table, torch.Tensor) or not table.is_cuda or table.dtype is not torch.float32 or not table.is_contiguous():
         raise TypeError("table must be a contiguous float32 CUDA (HIP) tensor")
-    if table.dim() != 3 or table.shape[2] != 2 or 2 * table.shape[1] > D:
-        raise ValueError(f"table must be [positions, R/2, 2] with R <= {D}, got {tuple(table.shape)}")
-    if table.device != device:
-        raise ValueError(f"table must be on {device}")
-    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2 or 2 * shape[1] > D:
+        raise ValueError(f"table must be [positions, R/2, 2] with R <= {D}, got {tuple(shape)}")
+    if table.get_device() != index:
+        raise ValueError(f"table must be on cuda:{index}")
+    return table.data_ptr(), shape[0], 2 * shape[1]
 
 
-def _weight(w, name, heads, D, device):
+def _weight(w, name, heads, D, index):
     """(address, head stride) of a norm's weight [D] or [heads, D]; None: ones."""
     if w is None:
         return 0, 0
-    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype != torch.float32 or not w.is_contiguous():
+    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype is not torch.float32 or not w.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 CUDA (HIP) tensor")
-    if w.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if w.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
     if w.shape == (D,):
         return w.data_ptr(), 0
     if w.shape == (heads, D):
@@ -209,37 +234,43 @@ def rotary(x, table, positions=None, offset=0, interleaved=False, inverse=False,
 
     The first R = 2 * table.shape[1] channels rotate, as pairs (i, i + R/2), or (2i, 2i + 1) if ``interleaved``; the others
     pass.  ``inverse`` turns back: the gradient of the forward turn.  ``out`` may be x itself (contiguous)."""
-    (B, T, H, D), dt, dev = _first(x, "x", 4)
-    tok = _tokens(x, "x", x.shape, dt, dev)
+    shape, dt, code, dev = _first(x, "x", 4)
+    B, T, H, D = shape
+    tok = _tokens(x, "x", shape, dt, dev)
+    tp, n_pos, R = _table(table, D, dev)
+    pp, p64, psb, pst = _positions(positions, B, T, dev)
+    if out is None:
+        out = x.new_empty(shape)
+    else:
+        _array(out, "out", dt, shape, dev)
+    _run(dev, "pn_rotary", _ROTARY(
+        code, B, T, D, R, bool(interleaved), bool(inverse), H, 0, *tok, *_NO_TOKENS, out.data_ptr(), 0, tp, n_pos, pp, p64,
+        psb, pst, int(offset), 0.0, 0, 0, 0, 0, *_NO_TOKENS, *_NO_TOKENS, 0, 0, 0, 0, _raw_stream(dev)))
+    return out
+
+
+def _norm_inputs(q, k, q_weight, k_weight, table, positions):
+    shape, dt, code, dev = _first(q, "q", 4)
+    B, T, H, D = shape
+    HK = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+    kshape = (B, T, HK, D)
+    tok = _tokens(q, "q", shape, dt, dev) + _tokens(k, "k", kshape, dt, dev)
     tp, n_pos, R = _table(table, D, dev)
     pos = _positions(positions, B, T, dev)
-    if out is None:
-        out = torch.empty((B, T, H, D), dtype=dt, device=dev)
-    else:
-        _array(out, "out", dt, x.shape, dev)
-    _run(dev, "pn_rotary", _ROTARY.pack(
-        _DTYPES[dt], B, T, D, R, int(bool(interleaved)), int(bool(inverse)), H, 0, *tok, *_NO_TOKENS, out.data_ptr(), 0,
-        tp, n_pos, pos[0], pos[1], pos[2], pos[3], int(offset), 0.0, 0, 0, 0, 0, *_NO_TOKENS, *_NO_TOKENS, 0, 0, 0, 0,
-        _raw_stream(dev).cuda_stream))
-    return out
+    qw, qs = _weight(q_weight, "q_weight", H, D, dev)
+    kw, ks = _weight(k_weight, "k_weight", HK, D, dev)
+    return dt, code, dev, shape, kshape, R, tok, (tp, n_pos, *pos), (qw, kw, qs, ks)
 
 
 def qk_norm_rotary(q, k, q_weight, k_weight, table, positions=None, offset=0, eps=1e-6, interleaved=False):
     """Norm of each head of q [B, T, H, D] and k [B, T, HK, D] over its channels, times its float32 weight ([D], one per
     head [heads, D], or None), then the rotation of ``rotary``, in one pass.  Returns (q', k')."""
-    (B, T, H, D), dt, dev = _first(q, "q", 4)
-    HK = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
-    tq, tk = _tokens(q, "q", q.shape, dt, dev), _tokens(k, "k", (B, T, HK, D), dt, dev)
-    tp, n_pos, R = _table(table, D, dev)
-    pos = _positions(positions, B, T, dev)
-    qw, qs = _weight(q_weight, "q_weight", H, D, dev)
-    kw, ks = _weight(k_weight, "k_weight", HK, D, dev)
-    qo = torch.empty((B, T, H, D), dtype=dt, device=dev)
-    ko = torch.empty((B, T, HK, D), dtype=dt, device=dev)
-    _run(dev, "pn_qk_norm_rotary", _ROTARY.pack(
-        _DTYPES[dt], B, T, D, R, int(bool(interleaved)), 0, H, HK, *tq, *tk, qo.data_ptr(), ko.data_ptr(), tp, n_pos,
-        pos[0], pos[1], pos[2], pos[3], int(offset), float(eps), qw, kw, qs, ks, *_NO_TOKENS, *_NO_TOKENS, 0, 0, 0, 0,
-        _raw_stream(dev).cuda_stream))
+    dt, code, dev, shape, kshape, R, tok, at, w = _norm_inputs(q, k, q_weight, k_weight, table, positions)
+    B, T, H, D = shape
+    qo, ko = q.new_empty(shape), q.new_empty(kshape)
+    _run(dev, "pn_qk_norm_rotary", _ROTARY(
+        code, B, T, D, R, bool(interleaved), 0, H, kshape[2], *tok, qo.data_ptr(), ko.data_ptr(), *at, int(offset), float(eps),
+        *w, *_NO_TOKENS, *_NO_TOKENS, 0, 0, 0, 0, _raw_stream(dev)))
     return qo, ko
 
 
@@ -247,45 +278,35 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight, k_weight, table, pos
                             interleaved=False):
     """Gradients of ``qk_norm_rotary`` from those of its outputs: (dq, dk, dq_weight, dk_weight), a weight's gradient
     None where the weight is."""
-    (B, T, H, D), dt, dev = _first(q, "q", 4)
-    HK = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
-    tq, tk = _tokens(q, "q", q.shape, dt, dev), _tokens(k, "k", (B, T, HK, D), dt, dev)
-    gq, gk = _tokens(dq_out, "dq_out", q.shape, dt, dev), _tokens(dk_out, "dk_out", k.shape, dt, dev)
-    tp, n_pos, R = _table(table, D, dev)
-    pos = _positions(positions, B, T, dev)
-    qw, qs = _weight(q_weight, "q_weight", H, D, dev)
-    kw, ks = _weight(k_weight, "k_weight", HK, D, dev)
-    dq = torch.empty((B, T, H, D), dtype=dt, device=dev)
-    dk = torch.empty((B, T, HK, D), dtype=dt, device=dev)
-    dqw = torch.empty_like(q_weight) if qw else None
-    dkw = torch.empty_like(k_weight) if kw else None
+    dt, code, dev, shape, kshape, R, tok, at, w = _norm_inputs(q, k, q_weight, k_weight, table, positions)
+    B, T, H, D = shape
+    grad = _tokens(dq_out, "dq_out", shape, dt, dev) + _tokens(dk_out, "dk_out", kshape, dt, dev)
+    dq, dk = q.new_empty(shape), q.new_empty(kshape)
+    dqw = torch.empty_like(q_weight) if w[0] else None
+    dkw = torch.empty_like(k_weight) if w[1] else None
 
     def block(ws, nbytes):
-        return _ROTARY.pack(
-            _DTYPES[dt], B, T, D, R, int(bool(interleaved)), 0, H, HK, *tq, *tk, dq.data_ptr(), dk.data_ptr(), tp, n_pos,
-            pos[0], pos[1], pos[2], pos[3], int(offset), float(eps), qw, kw, qs, ks, *gq, *gk, dqw.data_ptr() if qw else 0,
-            dkw.data_ptr() if kw else 0, ws, nbytes, _raw_stream(dev).cuda_stream)
+        return _ROTARY(
+            code, B, T, D, R, bool(interleaved), 0, H, kshape[2], *tok, dq.data_ptr(), dk.data_ptr(), *at, int(offset),
+            float(eps), *w, *grad, dqw.data_ptr() if w[0] else 0, dkw.data_ptr() if w[1] else 0, ws, nbytes, _raw_stream(dev))
 
-    ws, at, n = _workspace(dev, "pn_qk_norm_rotary_workspace_bytes", block(0, 0))
-    _run(dev, "pn_qk_norm_rotary_backward", block(at, n))
+    ws, base, n = _workspace(q, "pn_qk_norm_rotary_workspace_bytes", (0, B, T, H, kshape[2], D), block(0, 0))
+    _run(dev, "pn_qk_norm_rotary_backward", block(base, n))
     return dq, dk, dqw, dkw
 
 
 # ---------------------------------------------------------------- linear attention
 
 
-def _attention_inputs(q, k, v, log_decay, initial_state, lengths, dims):
-    (*lead, H, DK), dt, dev = _first(q, "q", dims)
+def _attention_inputs(q, k, v, log_decay, dims):
+    shape, dt, code, dev = _first(q, "q", dims)
     for t, name in ((k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor) or t.dim() != dims:
             raise ValueError(f"{name} must have {dims} dimensions")
-    HK, DV = k.shape[-2], v.shape[-1]
-    tok = (_tokens(q, "q", q.shape, dt, dev) + _tokens(k, "k", (*lead, HK, DK), dt, dev) +
+    lead, HK, DV = shape[:-2], k.shape[-2], v.shape[-1]
+    tok = (_tokens(q, "q", shape, dt, dev) + _tokens(k, "k", (*lead, HK, shape[-1]), dt, dev) +
            _tokens(v, "v", (*lead, HK, DV), dt, dev))
-    g = _array(log_decay, "log_decay", torch.float32, (H,), dev)
-    s0 = _array(initial_state, "initial_state", torch.float32, (lead[0], H, DK, DV), dev)
-    n = _array(lengths, "lengths", torch.int32, (lead[0],), dev)
-    return dt, dev, lead, H, HK, DK, DV, tok, g, s0, n
+    return shape, HK, DV, dt, code, dev, tok, _array(log_decay, "log_decay", torch.float32, (shape[-2],), dev)
 
 
 def linear_attention(q, k, v, log_decay, initial_state=None, scale=None, lengths=None):
@@ -294,16 +315,18 @@ def linear_attention(q, k, v, log_decay, initial_state=None, scale=None, lengths
     q [B, T, H, dk], k [B, T, HK, dk], v [B, T, HK, dv] (head h reads key and value head h / (H / HK)), log_decay float32
     [H], initial_state float32 [B, H, dk, dv] or None (zeros), scale dk^-1/2 by default.  ``lengths`` (int32 [B]) ends
     sequences early: later tokens are not read and give zero rows.  Returns (o [B, T, H, dv], final state float32)."""
-    dt, dev, (B, T), H, HK, DK, DV, tok, g, s0, n = _attention_inputs(q, k, v, log_decay, initial_state, lengths, 4)
-    o = torch.empty((B, T, H, DV), dtype=dt, device=dev)
-    final = torch.empty((B, H, DK, DV), dtype=torch.float32, device=dev)
+    (B, T, H, DK), HK, DV, dt, code, dev, tok, g = _attention_inputs(q, k, v, log_decay, 4)
+    s0 = _array(initial_state, "initial_state", torch.float32, (B, H, DK, DV), dev)
+    n = _array(lengths, "lengths", torch.int32, (B,), dev)
+    o = q.new_empty((B, T, H, DV))
+    final = log_decay.new_empty((B, H, DK, DV))
     a = DK ** -0.5 if scale is None else float(scale)
 
     def block(ws, nbytes):
-        return _ATTENTION.pack(_DTYPES[dt], B, T, H, HK, DK, DV, a, g, n, *tok, s0, o.data_ptr(), final.data_ptr(),
-                               *_NO_TOKENS, 0, 0, 0, 0, 0, ws, nbytes, _raw_stream(dev).cuda_stream)
+        return _ATTENTION(code, B, T, H, HK, DK, DV, a, g, n, *tok, s0, o.data_ptr(), final.data_ptr(), *_NO_TOKENS, 0, 0, 0,
+                          0, 0, ws, nbytes, _raw_stream(dev))
 
-    ws, at, size = _workspace(dev, "pn_linear_attention_workspace_bytes", block(0, 0), 0)
+    ws, at, size = _workspace(q, "pn_linear_attention_workspace_bytes", (1, code, B, T, H, HK, DK, DV), block(0, 0), 0)
     _run(dev, "pn_linear_attention", block(at, size))
     return o, final
 
@@ -311,21 +334,20 @@ def linear_attention(q, k, v, log_decay, initial_state=None, scale=None, lengths
 def linear_attention_backward(do, q, k, v, log_decay, initial_state=None, d_final_state=None, scale=None, lengths=None):
     """Gradients of ``linear_attention`` from those of o and (if given) of the final state: (dq, dk, dv,
     d_initial_state), the last None without an initial state.  The decay is a constant."""
-    dt, dev, (B, T), H, HK, DK, DV, tok, g, s0, n = _attention_inputs(q, k, v, log_decay, initial_state, lengths, 4)
+    (B, T, H, DK), HK, DV, dt, code, dev, tok, g = _attention_inputs(q, k, v, log_decay, 4)
+    s0 = _array(initial_state, "initial_state", torch.float32, (B, H, DK, DV), dev)
+    n = _array(lengths, "lengths", torch.int32, (B,), dev)
     td = _tokens(do, "do", (B, T, H, DV), dt, dev)
     df = _array(d_final_state, "d_final_state", torch.float32, (B, H, DK, DV), dev)
-    dq = torch.empty((B, T, H, DK), dtype=dt, device=dev)
-    dk = torch.empty((B, T, HK, DK), dtype=dt, device=dev)
-    dv = torch.empty((B, T, HK, DV), dtype=dt, device=dev)
-    d0 = torch.empty_like(initial_state) if initial_state is not None else None
+    dq, dk, dv = q.new_empty((B, T, H, DK)), q.new_empty((B, T, HK, DK)), q.new_empty((B, T, HK, DV))
+    d0 = torch.empty_like(initial_state) if s0 else None
     a = DK ** -0.5 if scale is None else float(scale)
 
     def block(ws, nbytes):
-        return _ATTENTION.pack(_DTYPES[dt], B, T, H, HK, DK, DV, a, g, n, *tok, s0, 0, 0, *td, df, dq.data_ptr(),
-                               dk.data_ptr(), dv.data_ptr(), 0 if d0 is None else d0.data_ptr(), ws, nbytes,
-                               _raw_stream(dev).cuda_stream)
+        return _ATTENTION(code, B, T, H, HK, DK, DV, a, g, n, *tok, s0, 0, 0, *td, df, dq.data_ptr(), dk.data_ptr(),
+                          dv.data_ptr(), d0.data_ptr() if s0 else 0, ws, nbytes, _raw_stream(dev))
 
-    ws, at, size = _workspace(dev, "pn_linear_attention_workspace_bytes", block(0, 0), 1)
+    ws, at, size = _workspace(q, "pn_linear_attention_workspace_bytes", (2, code, B, T, H, HK, DK, DV), block(0, 0), 1)
     _run(dev, "pn_linear_attention_backward", block(at, size))
     return dq, dk, dv, d0
 
@@ -335,11 +357,12 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
 
     q [B, H, dk], k [B, HK, dk], v [B, HK, dv]; state float32 [n_slots, H, dk, dv], sequence b at slots[b] (int32) or at b.
     A slot outside the pool (by custom -1) marks an idle row: its o is 0 and nothing is updated."""
-    dt, dev, (B,), H, HK, DK, DV, tok, g, _, n = _attention_inputs(q, k, v, log_decay, None, slots, 3)
+    (B, H, DK), HK, DV, dt, code, dev, tok, g = _attention_inputs(q, k, v, log_decay, 3)
+    n = _array(slots, "slots", torch.int32, (B,), dev)
     pool = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 4 else 0
     sp = _array(state, "state", torch.float32, (pool, H, DK, DV), dev)
-    o = torch.empty((B, H, DV), dtype=dt, device=dev)
-    _run(dev, "pn_linear_attention_step", _STEP.pack(
-        _DTYPES[dt], B, H, HK, DK, DV, DK ** -0.5 if scale is None else float(scale), g, *tok, sp, n, pool, o.data_ptr(),
-        _raw_stream(dev).cuda_stream))
+    o = q.new_empty((B, H, DV))
+    _run(dev, "pn_linear_attention_step", _STEP(
+        code, B, H, HK, DK, DV, DK ** -0.5 if scale is None else float(scale), g, *tok, sp, n, pool, o.data_ptr(),
+        _raw_stream(dev)))
     return o

@@ -138,7 +138,7 @@ TOK = lambda i, sb=64, st=32, sh=8: (i * GIB, sb, st, sh)  # noqa: E731
 def _rotary_block(dtype=0, B=2, T=2, D=8, R=4, inter=0, inverse=0, hq=4, hk=4, q=TOK(4), k=TOK(5), qo=6 * GIB, ko=7 * GIB,
                   table=8 * GIB, n_pos=16, pos=0, pos64=0, psb=0, pst=0, off=0, eps=1e-6, qw=0, kw=0, qsh=0, ksh=0,
                   dq=TOK(9), dk=TOK(10), dqw=0, dkw=0, ws=0, wsn=0):
-    return seq._ROTARY.pack(dtype, B, T, D, R, inter, inverse, hq, hk, *q, *k, qo, ko, table, n_pos, pos, pos64, psb, pst, off,
+    return seq._ROTARY(dtype, B, T, D, R, inter, inverse, hq, hk, *q, *k, qo, ko, table, n_pos, pos, pos64, psb, pst, off,
                             eps, qw, kw, qsh, ksh, *dq, *dk, dqw, dkw, ws, wsn, 0)
 
 
@@ -215,7 +215,7 @@ def test_rotary_table_refusals():
 
 def _attention_block(dtype=0, B=2, T=2, H=4, HK=4, dk=8, dv=8, scale=1.0, g=3 * GIB, lengths=0, q=TOK(4), k=TOK(5), v=TOK(6),
                      s0=0, o=7 * GIB, final=0, do=TOK(8), dfin=0, dq=9 * GIB, dk_=10 * GIB, dv_=11 * GIB, d0=0, ws=0, wsn=0):
-    return seq._ATTENTION.pack(dtype, B, T, H, HK, dk, dv, scale, g, lengths, *q, *k, *v, s0, o, final, *do, dfin, dq, dk_, dv_,
+    return seq._ATTENTION(dtype, B, T, H, HK, dk, dv, scale, g, lengths, *q, *k, *v, s0, o, final, *do, dfin, dq, dk_, dv_,
                                d0, ws, wsn, 0)
 
 
@@ -253,7 +253,7 @@ def test_attention_output_and_workspace_refusals():
 
 def _step_block(dtype=0, B=2, H=4, HK=4, dk=8, dv=8, scale=1.0, g=3 * GIB, q=TOK(4), k=TOK(5), v=TOK(6), state=7 * GIB, slots=0,
                 n_slots=2, o=9 * GIB):
-    return seq._STEP.pack(dtype, B, H, HK, dk, dv, scale, g, *q, *k, *v, state, slots, n_slots, o, 0)
+    return seq._STEP(dtype, B, H, HK, dk, dv, scale, g, *q, *k, *v, state, slots, n_slots, o, 0)
 
 
 @pytest.mark.parametrize("kw, code", [
