@@ -50,25 +50,25 @@ __global__ __launch_bounds__(256) void la_carry(LaChunkArgs g) {
 // Segments of the time axis: one where sequences, heads and columns fill the
 // device, else as many as fill it, of whole chunks.
 constexpr int64_t kFillGroups = 512;
-
-int chunk_tokens(int dtype) { return dtype == PN_BF16 ? Parts<bf16>::C : Parts<float>::C; }
+constexpr int64_t kLeastChunks = 4;      // of a segment: below, the passes over its state cost more than they save
 
 void segments(const LaArgs& a, int64_t* seg, int* n_seg) {
     int dv = 0;
     for (int w = 0; w < a.n_ops; ++w) dv = a.op[w].DV > dv ? a.op[w].DV : dv;
-    const int64_t C = chunk_tokens(a.dtype), chunks = (a.T + C - 1) / C, cols = 32 * la_waves(a);
+    const int64_t C = kChunk, chunks = (a.T + C - 1) / C, cols = 32 * la_waves(a);
     const int64_t groups = static_cast<int64_t>(a.B) * a.H * ((dv + cols - 1) / cols) * a.n_ops;
     int64_t n = (kFillGroups + groups - 1) / groups;
-    if (n > chunks) n = chunks;
+    if (n > chunks / kLeastChunks) n = chunks / kLeastChunks;
     if (n < 1) n = 1;
     const int64_t per = chunks > 0 ? (chunks + n - 1) / n : 1;
     *seg = per * C;
     *n_seg = chunks > 0 ? static_cast<int>((chunks + per - 1) / per) : 1;
 }
 
-// An operand that can be read (or the output written) 16 bytes at a time.
+// An operand that can be read (or the output written) 16 bytes at a time, the
+// tokens of a chunk within 2^31 bytes.
 bool wide(const void* p, int64_t sb, int64_t st, int64_t sh, int D, int elem) {
-    return D % 8 == 0 && ((reinterpret_cast<intptr_t>(p) | sb * elem | st * elem | sh * elem) & 15) == 0;
+    return D % 8 == 0 && st < (int64_t(1) << 24) && ((reinterpret_cast<intptr_t>(p) | sb * elem | st * elem | sh * elem) & 15) == 0;
 }
 bool wide(const LaOperand& x, int D, const LaArgs& a) {
     const int elem = a.dtype == PN_F32 ? 4 : 2;
@@ -211,8 +211,8 @@ hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st) {
     int64_t most = 0;
     for (int w = 0; w < a.n_ops; ++w) {
         const LaOp& op = a.op[w];
-        g.vec[w] = (wide(op.q, op.DK, a) ? 1 : 0) | (wide(op.k, op.DK, a) ? 2 : 0) | (wide(op.v, op.DV, a) ? 4 : 0) |
-                   (wide(op.o, 0, 0, 0, op.DV, 4) ? 8 : 0);
+        g.wide[w] = wide(op.q, op.DK, a) && wide(op.k, op.DK, a) && wide(op.v, op.DV, a) &&
+                    wide(op.o, 0, static_cast<int64_t>(a.H) * op.DV, 0, op.DV, 4);
         const int64_t n = static_cast<int64_t>(a.B) * a.H * op.DK * op.DV;
         if (op.carry_from == w) {
             g.carry[w] = ws;
@@ -241,6 +241,21 @@ hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st) {
         la_carry<<<dim3(static_cast<uint32_t>((most + 255) / 256), c.a.n_ops), 256, 0, st>>>(c);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
+    }
+    if (a.n_ops == 3 && a.op[1].o_f32) {                 // a launch has one type of output
+        LaChunkArgs c = g;
+        c.a.n_ops = 1;
+        const hipError_t e = run(c, true);
+        if (e != hipSuccess) return e;
+        for (int w = 0; w < 2; ++w) {
+            c.a.op[w] = g.a.op[w + 1];
+            c.carry[w] = g.carry[w + 1];
+            c.c_k[w] = g.c_k[w + 1];
+            c.c_v[w] = g.c_v[w + 1];
+            c.wide[w] = g.wide[w + 1];
+        }
+        c.a.n_ops = 2;
+        return run(c, true);
     }
     return run(g, true);
 }
