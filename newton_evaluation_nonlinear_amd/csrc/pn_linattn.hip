@@ -47,21 +47,22 @@ __global__ __launch_bounds__(256) void la_carry(LaChunkArgs g) {
     }
 }
 
-// Segments of the time axis: one where sequences, heads and columns fill the
-// device, else as many as fill it, of whole chunks.
-constexpr int64_t kFillGroups = 512;
+// Segments of the time axis: one where sequences, heads and columns fill most
+// of the device, else as many as fill it, of whole chunks.  kFillWaves: two
+// waves on each of the 4 SIMDs of 256 compute units.
+constexpr int64_t kFillWaves = 2048;
 constexpr int64_t kLeastChunks = 4;      // of a segment: below, the passes over its state cost more than they save
 
 void segments(const LaArgs& a, int64_t* seg, int* n_seg) {
     int dv = 0;
     for (int w = 0; w < a.n_ops; ++w) dv = a.op[w].DV > dv ? a.op[w].DV : dv;
-    const int64_t C = kChunk, chunks = (a.T + C - 1) / C, cols = 32 * la_waves(a);
-    const int64_t groups = static_cast<int64_t>(a.B) * a.H * ((dv + cols - 1) / cols) * a.n_ops;
-    int64_t n = (kFillGroups + groups - 1) / groups;
+    const int64_t chunks = (a.T + kChunk - 1) / kChunk, nw = la_waves(a), cols = 32 * nw;
+    const int64_t waves = static_cast<int64_t>(a.B) * a.H * ((dv + cols - 1) / cols) * a.n_ops * nw;
+    int64_t n = 4 * waves >= 3 * kFillWaves ? 1 : (kFillWaves + waves - 1) / waves;
     if (n > chunks / kLeastChunks) n = chunks / kLeastChunks;
     if (n < 1) n = 1;
     const int64_t per = chunks > 0 ? (chunks + n - 1) / n : 1;
-    *seg = per * C;
+    *seg = per * kChunk;
     *n_seg = chunks > 0 ? static_cast<int>((chunks + per - 1) / per) : 1;
 }
 

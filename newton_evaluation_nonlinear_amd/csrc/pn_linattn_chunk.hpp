@@ -509,19 +509,26 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
                 for (int e = 0; e < 8; ++e) s8[e] = S[t / 2][8 * (t % 2) + e];
                 split<LIM, false>(s8, sf[t % 2], minus);
             };
-            load_step(0);
-            split_step(0);
-            __builtin_amdgcn_sched_barrier(0);
+            // (of three parts there are too many to hold ahead: the compiler's order)
+            constexpr bool AHEAD = NP < 3;
+            if (AHEAD) {
+                load_step(0);
+                split_step(0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
                 constexpr int M = products<NP, NP, 3>() + products<LIM, NP, LIM>();
-                if (t + 1 < TT) load_step(t + 1);
+                if (!AHEAD || t + 1 < TT) load_step(AHEAD ? t + 1 : t);
+                if (!AHEAD) split_step(t);
                 P = product<NP, NP, 3>(kf[t % 2], qf[t % 2], P);
                 O = product<LIM, NP, LIM>(sf[t % 2], qf[t % 2], O);
-                if (t + 1 < TT) split_step(t + 1);
-                __builtin_amdgcn_sched_group_barrier(0x100, 2 * NP, 0);
-                interleave<M, (LIM == 2 ? 24 : 44) / M + 1>();
-                __builtin_amdgcn_sched_barrier(0);
+                if (AHEAD) {
+                    if (t + 1 < TT) split_step(t + 1);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 2 * NP, 0);
+                    interleave<M, 24 / M + 1>();
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
             float m[2][8];
 #pragma unroll
