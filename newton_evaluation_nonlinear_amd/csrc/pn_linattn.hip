@@ -16,52 +16,85 @@ namespace {
 
 // The state before each segment from the states the segments leave alone:
 //     S_{n+1} = lam^{tokens of n} S_n + U_n,
-// in place, element by element; slot n holds U_n, then S_{n+1}.
-__global__ __launch_bounds__(256) void la_carry(LaChunkArgs g) {
+// in place, element by element; slot n holds U_n, then S_{n+1}.  Bandwidth: a
+// workgroup takes 1024 elements of one state, so that few form its decays.
+constexpr int kCarryElems = 1024;
+__global__ __launch_bounds__(256) void la_carry(LaChunkArgs g, int blocks) {
+    __shared__ float decay[2];                           // over a whole segment, over the last one
     const LaOp& op = g.a.op[blockIdx.y];
-    const int n = op.DK * op.DV;
+    const int n = op.DK * op.DV, bh = blockIdx.x / blocks, first = (blockIdx.x - bh * blocks) * kCarryElems;
+    if (first >= n) return;
     const int64_t total = static_cast<int64_t>(g.a.B) * g.a.H * n;
-    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= total) return;
-    const int64_t bh = e / n;
-    const int at = static_cast<int>(e - bh * n), row = at / op.DV, col = at - row * op.DV;
-    const int h = static_cast<int>(bh % g.a.H), b = static_cast<int>(bh / g.a.H);
+    const int h = bh % g.a.H, b = bh / g.a.H;
     const int64_t len = seq_len(g.a.lengths, b, static_cast<int>(g.a.T));
-    const double gl = g.a.log_decay[h];
-    const float whole = static_cast<float>(exp(gl * static_cast<double>(g.seg)));
-    float s = op.s_in ? op.s_in[bh * n + row * op.s_k + col * op.s_v] : 0.0f;
-    float* u = g.carry[blockIdx.y] + e;
+    if (threadIdx.x < 2)
+        decay[threadIdx.x] = decay_power(g.a.log_decay[h], static_cast<float>(threadIdx.x == 0 ? g.seg : len % g.seg));
+    __syncthreads();
+    float s[4];
+    float* u[4];
+    bool on[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int at = first + k * 256 + threadIdx.x, row = at / op.DV, col = at - row * op.DV;
+        on[k] = at < n;
+        u[k] = g.carry[blockIdx.y] + static_cast<int64_t>(bh) * n + (on[k] ? at : 0);
+        s[k] = on[k] && op.s_in ? op.s_in[static_cast<int64_t>(bh) * n + row * op.s_k + col * op.s_v] : 0.0f;
+    }
     const int slots = g.n_seg - 1;
-    for (int i0 = 0; i0 < slots; i0 += 8) {
-        float x[8];
+    for (int i0 = 0; i0 < slots; i0 += 4) {
+        float x[4][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = i0 + j < slots ? u[(i0 + j) * total] : 0.0f;
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+            for (int k = 0; k < 4; ++k) x[j][k] = u[k][min(i0 + j, slots - 1) * total];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
             if (i0 + j >= slots) break;
             const int64_t left = len - (i0 + j) * g.seg;
-            const float d = left >= g.seg ? whole : (left <= 0 ? 1.0f : static_cast<float>(exp(gl * static_cast<double>(left))));
-            s = d * s + x[j];
-            u[(i0 + j) * total] = s;
+            const float d = left >= g.seg ? decay[0] : (left <= 0 ? 1.0f : decay[1]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s[k] = d * s[k] + x[j][k];
+                if (on[k]) u[k][(i0 + j) * total] = s[k];
+            }
         }
     }
 }
 
-// Segments of the time axis: one where sequences, heads and columns fill most
-// of the device, else as many as fill it, of whole chunks.  kFillWaves: two
-// waves on each of the 4 SIMDs of 256 compute units.
-constexpr int64_t kFillWaves = 2048;
-constexpr int64_t kLeastChunks = 4;      // of a segment: below, the passes over its state cost more than they save
+// Operators whose states between segments are formed: the first ones that
+// read their own (dk reads dv's, transposed).
+int carried(const LaArgs& a) { return a.n_ops == 3 ? 2 : a.n_ops; }
+
+// Segments of the time axis: the number n with the least estimated time.  In
+// units of a chunk's outputs, the device full: a workgroup takes its chunks and
+// kStart before them, and runs alone in kAlone of the time; the pass for the
+// segments' states takes kStates of it, with half as many workgroups more at a
+// time.  Measured on one training pass (8 x 4096 tokens, 16 heads of 128,
+// bfloat16): outputs 5.1 us a chunk and pair of workgroups, 3.6 alone; states 2.5.
+constexpr int64_t kFillWaves = 2048;     // two on each of the 4 SIMDs of 256 compute units
+constexpr double kStart = 2.0, kAlone = 0.7, kStates = 0.5;
+constexpr double kClear = 0.85;          // more segments, with their traffic, only for a clear gain
 
 void segments(const LaArgs& a, int64_t* seg, int* n_seg) {
     int dv = 0;
     for (int w = 0; w < a.n_ops; ++w) dv = a.op[w].DV > dv ? a.op[w].DV : dv;
     const int64_t chunks = (a.T + kChunk - 1) / kChunk, nw = la_waves(a), cols = 32 * nw;
-    const int64_t waves = static_cast<int64_t>(a.B) * a.H * ((dv + cols - 1) / cols) * a.n_ops * nw;
-    int64_t n = 4 * waves >= 3 * kFillWaves ? 1 : (kFillWaves + waves - 1) / waves;
-    if (n > chunks / kLeastChunks) n = chunks / kLeastChunks;
-    if (n < 1) n = 1;
-    const int64_t per = chunks > 0 ? (chunks + n - 1) / n : 1;
+    const int64_t heads = static_cast<int64_t>(a.B) * a.H * ((dv + cols - 1) / cols), slots = kFillWaves / nw;
+    auto rounds = [](int64_t groups, int64_t at_once) {
+        return groups <= at_once / 2 ? kAlone : static_cast<double>((groups + at_once - 1) / at_once);
+    };
+    double least = 0.0;
+    int64_t best = 1;
+    for (int64_t n = 1; n <= chunks / 4 && n <= 128; ++n) {
+        const double per = static_cast<double>((chunks + n - 1) / n) + kStart;
+        double t = per * rounds(heads * a.n_ops * n, slots);
+        if (n > 1) t += kStates * per * rounds(heads * carried(a) * (n - 1), slots * 3 / 2) + kStart;
+        if (n == 1 || t < kClear * least) {
+            least = t;
+            best = n;
+        }
+    }
+    const int64_t per = chunks > 0 ? (chunks + best - 1) / best : 1;
     *seg = per * kChunk;
     *n_seg = chunks > 0 ? static_cast<int>((chunks + per - 1) / per) : 1;
 }
@@ -190,10 +223,6 @@ hipError_t step_typed(const pn_linattn_step_args& a, hipStream_t st) {
 
 }  // namespace
 
-// Operators whose states between segments are formed: the first ones that
-// read their own (dk reads dv's, transposed).
-static int carried(const LaArgs& a) { return a.n_ops == 3 ? 2 : a.n_ops; }
-
 size_t linattn_workspace(const LaArgs& a) {
     int64_t seg;
     int n_seg;
@@ -209,12 +238,14 @@ hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st) {
     g.a = a;
     segments(a, &g.seg, &g.n_seg);
     float* ws = static_cast<float*>(workspace);
-    int64_t most = 0;
+    int most = 0;
     for (int w = 0; w < a.n_ops; ++w) {
         const LaOp& op = a.op[w];
         g.wide[w] = wide(op.q, op.DK, a) && wide(op.k, op.DK, a) && wide(op.v, op.DV, a) &&
                     wide(op.o, 0, static_cast<int64_t>(a.H) * op.DV, 0, op.DV, 4);
         const int64_t n = static_cast<int64_t>(a.B) * a.H * op.DK * op.DV;
+        const int blocks = (op.DK * op.DV + kCarryElems - 1) / kCarryElems;
+        most = blocks > most ? blocks : most;
         if (op.carry_from == w) {
             g.carry[w] = ws;
             g.c_k[w] = op.DV;
@@ -225,7 +256,6 @@ hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st) {
             g.c_k[w] = 1;
             g.c_v[w] = op.DK;
         }
-        most = n > most ? n : most;
     }
     auto run = [&](const LaChunkArgs& c, bool out) {
         switch (a.dtype) {
@@ -239,7 +269,7 @@ hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st) {
         c.a.n_ops = carried(a);
         hipError_t e = run(c, false);
         if (e != hipSuccess) return e;
-        la_carry<<<dim3(static_cast<uint32_t>((most + 255) / 256), c.a.n_ops), 256, 0, st>>>(c);
+        la_carry<<<dim3(static_cast<uint32_t>(a.B * a.H * most), c.a.n_ops), 256, 0, st>>>(c, most);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

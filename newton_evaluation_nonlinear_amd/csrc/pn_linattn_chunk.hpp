@@ -76,6 +76,15 @@ __device__ __forceinline__ int seq_len(const int32_t* lengths, int b, int T) {
     return n < 0 ? 0 : (n > T ? T : n);
 }
 
+// e^{g n}, 1 for n = 0, to a few 2^-24: the rounding of g n, which the
+// exponential would magnify, is put back as its first-order factor.
+__device__ __forceinline__ float decay_power(float g, float n) {
+    const float x = g * n;
+    if (n == 0.0f) return 1.0f;
+    const float e = expf(x);
+    return e == 0.0f || __builtin_isinf(x) ? e : fmaf(e, fmaf(g, n, -x), e);
+}
+
 // Row (or column) of a 32-wide tile that lane index m stands for: register r
 // of half h of an accumulator tile then holds row 16 (r / 8) + 8 h + r % 8.
 __device__ __forceinline__ int perm(int m) { return 16 * (m >> 4) + 8 * ((m >> 2) & 1) + 4 * ((m >> 3) & 1) + (m & 3); }
@@ -370,7 +379,7 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
     const int i_begin = static_cast<int>(sg * g.seg);
     const int i_end = static_cast<int>(min(static_cast<int64_t>(N), (sg + 1) * g.seg));
     const int n_end = min(i_end, len);                   // tokens that count
-    const double gl = a.log_decay[h];
+    const float gl = a.log_decay[h];
     const Minus minus;
 
     Stage<T, DKP, NT, true, VEC> kst;
@@ -395,7 +404,7 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
             reinterpret_cast<u32x4*>(sh.k)[e] = (u32x4)(0u);
             if (OUT) reinterpret_cast<u32x4*>(sh.q)[e] = (u32x4)(0u);
         }
-    if (tid <= kChunk) sh.pw[tid] = tid == 0 ? 1.0f : static_cast<float>(exp(gl * tid));
+    if (tid <= kChunk) sh.pw[tid] = decay_power(gl, static_cast<float>(tid));
     __syncthreads();
     if (tid < kChunk) sh.w[tid] = op.ws * sh.pw[kChunk - 1 - tid + (reverse ? 1 : 0)];
     if (OUT && tid < 64) sh.m[tid] = tid < 32 ? op.inter * op.ws * sh.pw[31 - tid] : 0.0f;

@@ -16,6 +16,7 @@ import torch
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_empty_like = torch.empty_like
 
 # Argument blocks of include/pn.h: every field is 8 bytes wide.
 _ROTARY = struct.Struct("=9q8q2q3q4qd2q2q8q2q3q").pack
@@ -86,47 +87,72 @@ def _workspace(like, name, key, *args):
     return ws, (ws.data_ptr() + 255) & -256, n
 
 
-def _tokens(t, name, shape, dtype, index):
-    """(address, strides) of a token tensor; raises on what the library cannot take."""
+# The checks below are written for calls of a few microseconds: each property is read once, and only a check that has
+# failed looks for the reason.
+
+
+def _refuse(t, name, dtype, index, contiguous=False):
+    """The reason why a tensor is not on the device, of the type or (if asked) contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}")
+    if contiguous and not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be on cuda:{index}")
+
+
+def _shape_is(t, name, *shapes):
+    raise ValueError(f"{name} must have shape {' or '.join(str(tuple(s)) for s in shapes)}, got {tuple(t.shape)}")
+
+
+def _strides(t, name, shape):
+    """(address, batch, token and head stride) of a token tensor of the right shape, whose channels have to be adjacent."""
     s = t.stride()
     if s[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"the channels of {name} must be adjacent (stride 1, got {s[-1]})")
     return (t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else (t.data_ptr(), s[0], 0, s[1])
 
 
+def _tokens(t, name, shape, dtype, index):
+    """(address, strides) of a token tensor; raises on what the library cannot take."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+        _refuse(t, name, dtype, index)
+    if t.shape != shape:
+        _shape_is(t, name, shape)
+    return _strides(t, name, shape)
+
+
 def _array(t, name, dtype, shape, index):
     """Address of a contiguous array (None: 0)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {dtype} CUDA (HIP) tensor")
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, name, dtype, index, True)
     if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}")
+        _shape_is(t, name, shape)
     return t.data_ptr()
 
 
 def _first(t, name, dims):
-    """(shape, dtype, its code, device index) of the tensor that the others have to agree with."""
+    """(shape, dtype, its code, device index, address and strides) of the tensor that the others have to agree with."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
     dt = t.dtype
     code = _DTYPES.get(dt)
     if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dt}")
-    shape = t.shape
+    shape = tuple(t.shape)
     if len(shape) != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(shape)}")
-    return shape, dt, code, t.get_device()
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {shape}")
+    return shape, dt, code, t.get_device(), _strides(t, name, shape)
+
+
+def _new(like, shape):
+    """An uninitialised contiguous tensor of `like`'s type and device."""
+    if like.is_contiguous() and like.shape == shape:
+        return _empty_like(like)
+    return like.new_empty(shape)
 
 
 # ---------------------------------------------------------------- rotary positions
@@ -188,29 +214,26 @@ def _positions(positions, B, T, index):
     """(address, is int64, batch stride, token stride) of positions [B, T] or [T]."""
     if positions is None:
         return 0, 0, 0, 0
-    if not isinstance(positions, torch.Tensor) or not positions.is_cuda:
-        raise TypeError("positions must be an int32 or int64 CUDA (HIP) tensor")
-    dt = positions.dtype
-    if dt is not torch.int32 and dt is not torch.int64:
-        raise TypeError("positions must be an int32 or int64 CUDA (HIP) tensor")
-    if positions.get_device() != index:
+    dt = positions.dtype if isinstance(positions, torch.Tensor) else None
+    if dt is not torch.int32 and dt is not torch.int64 or positions.get_device() != index:
+        if dt is None or not positions.is_cuda or dt not in (torch.int32, torch.int64):
+            raise TypeError("positions must be an int32 or int64 CUDA (HIP) tensor")
         raise ValueError(f"positions must be on cuda:{index}")
     s = positions.stride()
     if positions.shape == (B, T):
-        return positions.data_ptr(), int(dt is torch.int64), s[0], s[1]
+        return positions.data_ptr(), dt is torch.int64, s[0], s[1]
     if positions.shape == (T,):
-        return positions.data_ptr(), int(dt is torch.int64), 0, s[0]
-    raise ValueError(f"positions must have shape {(B, T)} or {(T,)}, got {tuple(positions.shape)}")
+        return positions.data_ptr(), dt is torch.int64, 0, s[0]
+    _shape_is(positions, "positions", (B, T), (T,))
 
 
 def _table(table, D, index):
-    if not isinstance(table, torch.Tensor) or not table.is_cuda or table.dtype is not torch.float32 or not table.is_contiguous():
-        raise TypeError("table must be a contiguous float32 CUDA (HIP) tensor")
+    if (not isinstance(table, torch.Tensor) or table.dtype is not torch.float32 or table.get_device() != index or
+            not table.is_contiguous()):
+        _refuse(table, "table", torch.float32, index, True)
     shape = table.shape
     if len(shape) != 3 or shape[2] != 2 or 2 * shape[1] > D:
         raise ValueError(f"table must be [positions, R/2, 2] with R <= {D}, got {tuple(shape)}")
-    if table.get_device() != index:
-        raise ValueError(f"table must be on cuda:{index}")
     return table.data_ptr(), shape[0], 2 * shape[1]
 
 
@@ -218,15 +241,13 @@ def _weight(w, name, heads, D, index):
     """(address, head stride) of a norm's weight [D] or [heads, D]; None: ones."""
     if w is None:
         return 0, 0
-    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype is not torch.float32 or not w.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous float32 CUDA (HIP) tensor")
-    if w.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}")
+    if not isinstance(w, torch.Tensor) or w.dtype is not torch.float32 or w.get_device() != index or not w.is_contiguous():
+        _refuse(w, name, torch.float32, index, True)
     if w.shape == (D,):
         return w.data_ptr(), 0
     if w.shape == (heads, D):
         return w.data_ptr(), D
-    raise ValueError(f"{name} must have shape {(D,)} or {(heads, D)}, got {tuple(w.shape)}")
+    _shape_is(w, name, (D,), (heads, D))
 
 
 def rotary(x, table, positions=None, offset=0, interleaved=False, inverse=False, out=None):
@@ -234,13 +255,12 @@ def rotary(x, table, positions=None, offset=0, interleaved=False, inverse=False,
 
     The first R = 2 * table.shape[1] channels rotate, as pairs (i, i + R/2), or (2i, 2i + 1) if ``interleaved``; the others
     pass.  ``inverse`` turns back: the gradient of the forward turn.  ``out`` may be x itself (contiguous)."""
-    shape, dt, code, dev = _first(x, "x", 4)
+    shape, dt, code, dev, tok = _first(x, "x", 4)
     B, T, H, D = shape
-    tok = _tokens(x, "x", shape, dt, dev)
     tp, n_pos, R = _table(table, D, dev)
     pp, p64, psb, pst = _positions(positions, B, T, dev)
     if out is None:
-        out = x.new_empty(shape)
+        out = _new(x, shape)
     else:
         _array(out, "out", dt, shape, dev)
     _run(dev, "pn_rotary", _ROTARY(
@@ -250,11 +270,11 @@ def rotary(x, table, positions=None, offset=0, interleaved=False, inverse=False,
 
 
 def _norm_inputs(q, k, q_weight, k_weight, table, positions):
-    shape, dt, code, dev = _first(q, "q", 4)
+    shape, dt, code, dev, tok = _first(q, "q", 4)
     B, T, H, D = shape
     HK = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
     kshape = (B, T, HK, D)
-    tok = _tokens(q, "q", shape, dt, dev) + _tokens(k, "k", kshape, dt, dev)
+    tok += _tokens(k, "k", kshape, dt, dev)
     tp, n_pos, R = _table(table, D, dev)
     pos = _positions(positions, B, T, dev)
     qw, qs = _weight(q_weight, "q_weight", H, D, dev)
@@ -267,7 +287,7 @@ def qk_norm_rotary(q, k, q_weight, k_weight, table, positions=None, offset=0, ep
     head [heads, D], or None), then the rotation of ``rotary``, in one pass.  Returns (q', k')."""
     dt, code, dev, shape, kshape, R, tok, at, w = _norm_inputs(q, k, q_weight, k_weight, table, positions)
     B, T, H, D = shape
-    qo, ko = q.new_empty(shape), q.new_empty(kshape)
+    qo, ko = _new(q, shape), _new(k, kshape)
     _run(dev, "pn_qk_norm_rotary", _ROTARY(
         code, B, T, D, R, bool(interleaved), 0, H, kshape[2], *tok, qo.data_ptr(), ko.data_ptr(), *at, int(offset), float(eps),
         *w, *_NO_TOKENS, *_NO_TOKENS, 0, 0, 0, 0, _raw_stream(dev)))
@@ -281,9 +301,9 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight, k_weight, table, pos
     dt, code, dev, shape, kshape, R, tok, at, w = _norm_inputs(q, k, q_weight, k_weight, table, positions)
     B, T, H, D = shape
     grad = _tokens(dq_out, "dq_out", shape, dt, dev) + _tokens(dk_out, "dk_out", kshape, dt, dev)
-    dq, dk = q.new_empty(shape), q.new_empty(kshape)
-    dqw = torch.empty_like(q_weight) if w[0] else None
-    dkw = torch.empty_like(k_weight) if w[1] else None
+    dq, dk = _new(q, shape), _new(k, kshape)
+    dqw = _empty_like(q_weight) if w[0] else None
+    dkw = _empty_like(k_weight) if w[1] else None
 
     def block(ws, nbytes):
         return _ROTARY(
@@ -299,13 +319,12 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight, k_weight, table, pos
 
 
 def _attention_inputs(q, k, v, log_decay, dims):
-    shape, dt, code, dev = _first(q, "q", dims)
+    shape, dt, code, dev, tok = _first(q, "q", dims)
     for t, name in ((k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor) or t.dim() != dims:
             raise ValueError(f"{name} must have {dims} dimensions")
     lead, HK, DV = shape[:-2], k.shape[-2], v.shape[-1]
-    tok = (_tokens(q, "q", shape, dt, dev) + _tokens(k, "k", (*lead, HK, shape[-1]), dt, dev) +
-           _tokens(v, "v", (*lead, HK, DV), dt, dev))
+    tok += _tokens(k, "k", (*lead, HK, shape[-1]), dt, dev) + _tokens(v, "v", (*lead, HK, DV), dt, dev)
     return shape, HK, DV, dt, code, dev, tok, _array(log_decay, "log_decay", torch.float32, (shape[-2],), dev)
 
 
@@ -318,8 +337,8 @@ def linear_attention(q, k, v, log_decay, initial_state=None, scale=None, lengths
     (B, T, H, DK), HK, DV, dt, code, dev, tok, g = _attention_inputs(q, k, v, log_decay, 4)
     s0 = _array(initial_state, "initial_state", torch.float32, (B, H, DK, DV), dev)
     n = _array(lengths, "lengths", torch.int32, (B,), dev)
-    o = q.new_empty((B, T, H, DV))
-    final = log_decay.new_empty((B, H, DK, DV))
+    o = _new(q, (B, T, H, DV))
+    final = _empty_like(initial_state) if s0 else log_decay.new_empty((B, H, DK, DV))
     a = DK ** -0.5 if scale is None else float(scale)
 
     def block(ws, nbytes):
@@ -339,8 +358,8 @@ def linear_attention_backward(do, q, k, v, log_decay, initial_state=None, d_fina
     n = _array(lengths, "lengths", torch.int32, (B,), dev)
     td = _tokens(do, "do", (B, T, H, DV), dt, dev)
     df = _array(d_final_state, "d_final_state", torch.float32, (B, H, DK, DV), dev)
-    dq, dk, dv = q.new_empty((B, T, H, DK)), q.new_empty((B, T, HK, DK)), q.new_empty((B, T, HK, DV))
-    d0 = torch.empty_like(initial_state) if s0 else None
+    dq, dk, dv = _new(q, (B, T, H, DK)), _new(k, (B, T, HK, DK)), _new(v, (B, T, HK, DV))
+    d0 = _empty_like(initial_state) if s0 else None
     a = DK ** -0.5 if scale is None else float(scale)
 
     def block(ws, nbytes):
@@ -361,7 +380,7 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     n = _array(slots, "slots", torch.int32, (B,), dev)
     pool = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 4 else 0
     sp = _array(state, "state", torch.float32, (pool, H, DK, DV), dev)
-    o = q.new_empty((B, H, DV))
+    o = _new(q, (B, H, DV))
     _run(dev, "pn_linear_attention_step", _STEP(
         code, B, H, HK, DK, DV, DK ** -0.5 if scale is None else float(scale), g, *tok, sp, n, pool, o.data_ptr(),
         _raw_stream(dev)))
