@@ -312,11 +312,15 @@ __device__ __forceinline__ char* uniform(char* p) {
     return reinterpret_cast<char*>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
+// Channels of an LDS row that DKP of are used: a power of two, for q_block()
+// and kv_block().
+constexpr int row_width(int DKP) { return DKP == 96 ? 128 : DKP; }
+
 template <typename T, int DKP, int NW, bool OUT>
 struct alignas(16) LaShared {
     static constexpr int NP = Parts<T>::NP;
-    alignas(16) bf16 q[OUT ? NP * kChunk * DKP : 8];       // [part][token][channel]
-    alignas(16) bf16 k[NP * kChunk * DKP];
+    alignas(16) bf16 q[OUT ? NP * kChunk * row_width(DKP) : 8];       // [part][token][channel]
+    alignas(16) bf16 k[NP * kChunk * row_width(DKP)];
     alignas(16) bf16 v[NP * kChunk * NW * 32];
     alignas(16) bf16 spare[8];
     alignas(16) float w[kChunk];    // weights of V in the state
@@ -358,7 +362,7 @@ __device__ __forceinline__ int across_at(int lane, int x) {
 // output's type.
 template <typename T, typename TO, int DKP, int NW, bool OUT, bool EXACT, bool VEC>
 __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chunk(LaChunkArgs g, int col_blocks) {
-    constexpr int NP = Parts<T>::NP, LIM = Parts<T>::LIM, NT = 64 * NW, KT = DKP / 32, VW = 32 * NW;
+    constexpr int NP = Parts<T>::NP, LIM = Parts<T>::LIM, NT = 64 * NW, KT = DKP / 32, VW = 32 * NW, RW = row_width(DKP);
     constexpr int SP = EXACT ? 3 : LIM;                  // parts of w V
     __shared__ LaShared<T, DKP, NW, OUT> sh;
     const LaArgs& a = g.a;
@@ -382,8 +386,8 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
     const float gl = a.log_decay[h];
     const Minus minus;
 
-    Stage<T, DKP, NT, true, VEC> kst;
-    Stage<T, DKP, NT, false, VEC> qst;
+    Stage<T, RW, NT, true, VEC> kst;
+    Stage<T, RW, NT, false, VEC> qst;
     Stage<T, VW, NT, true, VEC> vst;
     const int64_t t0 = reverse ? len - 1 - i_begin : i_begin;            // the first token
     kst.open(static_cast<const T*>(op.k.p) + b * op.k.sb + (h / op.k.div) * op.k.sh + t0 * op.k.st, op.k.st, reverse, DK,
@@ -400,7 +404,7 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
     }
 
     if (DK < DKP)                                        // channels that no store reaches
-        for (int e = tid; e < NP * kChunk * DKP / 8; e += NT) {
+        for (int e = tid; e < NP * kChunk * RW / 8; e += NT) {
             reinterpret_cast<u32x4*>(sh.k)[e] = (u32x4)(0u);
             if (OUT) reinterpret_cast<u32x4*>(sh.q)[e] = (u32x4)(0u);
         }
@@ -437,8 +441,8 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
     }
     // this lane's first fragments; the others are at a distance or, where the
     // block changes, at an exclusive or
-    const int q_at = l32 * DKP + 8 * q_block<DKP>(l32, half), k_at = pl * DKP + 8 * kv_block<DKP>(pl, half);
-    const int kt_at = across_at<DKP>(lane, 0), vt_at = across_at<VW>(lane, wave);
+    const int q_at = l32 * RW + 8 * q_block<RW>(l32, half), k_at = pl * RW + 8 * kv_block<RW>(pl, half);
+    const int kt_at = across_at<RW>(lane, 0), vt_at = across_at<VW>(lane, wave);
 
     // the output's rows of the chunk: the lowest address, and this lane's bytes
     // from it (up to 2^31)
@@ -480,7 +484,7 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
             for (int n = 0; n < NP; ++n) vf[t][n] = fragment_across<VW>(sh.v + (n * kChunk + 16 * t) * VW + vt_at);
         auto across_k = [&](int t, int x, bf16x8* f) {
 #pragma unroll
-            for (int n = 0; n < NP; ++n) f[n] = fragment_across<DKP>(sh.k + (n * kChunk + 16 * t) * DKP + (kt_at ^ (32 * x)));
+            for (int n = 0; n < NP; ++n) f[n] = fragment_across<RW>(sh.k + (n * kChunk + 16 * t) * RW + (kt_at ^ (32 * x)));
         };
         auto load_kx = [&](int t) {
             if constexpr (HOLD)
@@ -508,8 +512,8 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
             auto load_step = [&](int t) {
 #pragma unroll
                 for (int n = 0; n < NP; ++n) {
-                    qf[t % 2][n] = fragment(sh.q + n * kChunk * DKP + (q_at ^ (16 * t)));
-                    kf[t % 2][n] = fragment(sh.k + n * kChunk * DKP + (k_at ^ (16 * t)));
+                    qf[t % 2][n] = fragment(sh.q + n * kChunk * RW + (q_at ^ (16 * t)));
+                    kf[t % 2][n] = fragment(sh.k + n * kChunk * RW + (k_at ^ (16 * t)));
                 }
             };
             auto split_step = [&](int t) {
@@ -664,6 +668,7 @@ hipError_t launch_chunks(const LaChunkArgs& g, bool out, hipStream_t st) {
     };
     if (dk <= 32) return rows(integral_constant<int, 32>{});
     if (dk <= 64) return rows(integral_constant<int, 64>{});
+    if (dk <= 96) return rows(integral_constant<int, 96>{});
     if (dk <= 128) return rows(integral_constant<int, 128>{});
     return rows(integral_constant<int, 256>{});
 }
