@@ -16,7 +16,6 @@ import torch
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
-_empty_like = torch.empty_like
 
 # Argument blocks of include/pn.h: every field is 8 bytes wide.
 _ROTARY = struct.Struct("=9q8q2q3q4qd2q2q8q2q3q").pack
@@ -148,13 +147,6 @@ def _first(t, name, dims):
     return shape, dt, code, t.get_device(), _strides(t, name, shape)
 
 
-def _new(like, shape):
-    """An uninitialised contiguous tensor of `like`'s type and device."""
-    if like.is_contiguous() and like.shape == shape:
-        return _empty_like(like)
-    return like.new_empty(shape)
-
-
 # ---------------------------------------------------------------- rotary positions
 
 
@@ -260,7 +252,7 @@ def rotary(x, table, positions=None, offset=0, interleaved=False, inverse=False,
     tp, n_pos, R = _table(table, D, dev)
     pp, p64, psb, pst = _positions(positions, B, T, dev)
     if out is None:
-        out = _new(x, shape)
+        out = x.new_empty(B, T, H, D)
     else:
         _array(out, "out", dt, shape, dev)
     _run(dev, "pn_rotary", _ROTARY(
@@ -287,7 +279,7 @@ def qk_norm_rotary(q, k, q_weight, k_weight, table, positions=None, offset=0, ep
     head [heads, D], or None), then the rotation of ``rotary``, in one pass.  Returns (q', k')."""
     dt, code, dev, shape, kshape, R, tok, at, w = _norm_inputs(q, k, q_weight, k_weight, table, positions)
     B, T, H, D = shape
-    qo, ko = _new(q, shape), _new(k, kshape)
+    qo, ko = q.new_empty(*shape), q.new_empty(*kshape)
     _run(dev, "pn_qk_norm_rotary", _ROTARY(
         code, B, T, D, R, bool(interleaved), 0, H, kshape[2], *tok, qo.data_ptr(), ko.data_ptr(), *at, int(offset), float(eps),
         *w, *_NO_TOKENS, *_NO_TOKENS, 0, 0, 0, 0, _raw_stream(dev)))
@@ -301,9 +293,9 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight, k_weight, table, pos
     dt, code, dev, shape, kshape, R, tok, at, w = _norm_inputs(q, k, q_weight, k_weight, table, positions)
     B, T, H, D = shape
     grad = _tokens(dq_out, "dq_out", shape, dt, dev) + _tokens(dk_out, "dk_out", kshape, dt, dev)
-    dq, dk = _new(q, shape), _new(k, kshape)
-    dqw = _empty_like(q_weight) if w[0] else None
-    dkw = _empty_like(k_weight) if w[1] else None
+    dq, dk = q.new_empty(*shape), q.new_empty(*kshape)
+    dqw = torch.empty_like(q_weight) if w[0] else None
+    dkw = torch.empty_like(k_weight) if w[1] else None
 
     def block(ws, nbytes):
         return _ROTARY(
@@ -337,8 +329,8 @@ def linear_attention(q, k, v, log_decay, initial_state=None, scale=None, lengths
     (B, T, H, DK), HK, DV, dt, code, dev, tok, g = _attention_inputs(q, k, v, log_decay, 4)
     s0 = _array(initial_state, "initial_state", torch.float32, (B, H, DK, DV), dev)
     n = _array(lengths, "lengths", torch.int32, (B,), dev)
-    o = _new(q, (B, T, H, DV))
-    final = _empty_like(initial_state) if s0 else log_decay.new_empty((B, H, DK, DV))
+    o = q.new_empty(B, T, H, DV)
+    final = log_decay.new_empty(B, H, DK, DV)
     a = DK ** -0.5 if scale is None else float(scale)
 
     def block(ws, nbytes):
@@ -358,8 +350,8 @@ def linear_attention_backward(do, q, k, v, log_decay, initial_state=None, d_fina
     n = _array(lengths, "lengths", torch.int32, (B,), dev)
     td = _tokens(do, "do", (B, T, H, DV), dt, dev)
     df = _array(d_final_state, "d_final_state", torch.float32, (B, H, DK, DV), dev)
-    dq, dk, dv = _new(q, (B, T, H, DK)), _new(k, (B, T, HK, DK)), _new(v, (B, T, HK, DV))
-    d0 = _empty_like(initial_state) if s0 else None
+    dq, dk, dv = q.new_empty(B, T, H, DK), q.new_empty(B, T, HK, DK), q.new_empty(B, T, HK, DV)
+    d0 = torch.empty_like(initial_state) if s0 else None
     a = DK ** -0.5 if scale is None else float(scale)
 
     def block(ws, nbytes):
@@ -380,7 +372,7 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     n = _array(slots, "slots", torch.int32, (B,), dev)
     pool = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 4 else 0
     sp = _array(state, "state", torch.float32, (pool, H, DK, DV), dev)
-    o = _new(q, (B, H, DV))
+    o = q.new_empty(B, H, DV)
     _run(dev, "pn_linear_attention_step", _STEP(
         code, B, H, HK, DK, DV, DK ** -0.5 if scale is None else float(scale), g, *tok, sp, n, pool, o.data_ptr(),
         _raw_stream(dev)))
