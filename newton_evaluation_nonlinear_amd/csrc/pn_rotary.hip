@@ -306,7 +306,13 @@ __global__ __launch_bounds__(1024) void weight_sum(const float* part, int D, int
     const float* p = part + static_cast<int64_t>(head) * n_wg * D + c;
     double s = 0.0;
     if (c < D)
-        for (int64_t r = lane; r < rows; r += 16) s += p[r * D];
+        for (int64_t r0 = lane; r0 < rows; r0 += 16 * 16) {
+            float x[16];                                 // 16 loads in flight, added in order
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = p[min(r0 + 16 * i, rows - 1) * D];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s += r0 + 16 * i < rows ? x[i] : 0.0f;
+        }
     red[lane][col] = s;
     __syncthreads();
     if (lane == 0 && c < D) {
