@@ -385,8 +385,9 @@ size_t pn_qk_norm_rotary_workspace_bytes(const pn_rotary_args* a);
  * lengths (int32 [B], NULL = T each; values are clamped to [0, T]): tokens at
  * and after lengths[b] are padding: never read, their rows of the outputs 0,
  * and final_state is the state after lengths[b] tokens.  A NaN or infinity
- * in a token reaches the outputs from that token on, and may reach those of
- * the up to 63 tokens before it. */
+ * in a token reaches the outputs from that token on, as NaN or infinity, and
+ * may reach those of the up to 31 tokens before it (in the gradients of k and
+ * v, which run backwards, after it). */
 typedef struct pn_linattn_args {
     int64_t dtype, B, T, H, HK, dk, dv;
     double scale;

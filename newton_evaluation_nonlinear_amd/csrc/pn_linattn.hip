@@ -17,7 +17,8 @@ namespace {
 // The state before each segment from the states the segments leave alone:
 //     S_{n+1} = lam^{tokens of n} S_n + U_n,
 // in place, element by element; slot n holds U_n, then S_{n+1}.  Bandwidth: a
-// workgroup takes 1024 elements of one state, so that few form its decays.
+// workgroup takes 1024 elements of one state, so that few form its decays (a
+// thread for each element took 23 us for 3 x 128 states of 128 x 128, so 12).
 constexpr int kCarryElems = 1024;
 __global__ __launch_bounds__(256) void la_carry(LaChunkArgs g, int blocks) {
     __shared__ float decay[2];                           // over a whole segment, over the last one
@@ -127,6 +128,8 @@ __global__ __launch_bounds__(256) void la_group_sum(const float* in, T* out, int
 // the first store.  For a slow decay lam S + k v is taken as
 // S + (S (lam - 1) + k v): lam - 1 keeps it exact over many steps, where lam
 // itself, rounded, would be off by up to 2^-25 at each.
+// Measured: 256 sequences of 16 heads, 128 x 128 (537 MB), 112 us, 4.8 TB/s, the
+// rate of a large copy; 4 sequences 5.4 us.
 template <typename T, int V, int LC>
 __global__ __launch_bounds__(256) void la_step(pn_linattn_step_args a) {
     constexpr int RG = 256 / LC, ROWS = 8;
