@@ -378,8 +378,9 @@ size_t pn_qk_norm_rotary_workspace_bytes(const pn_rotary_args* a);
 
 /* Linear attention with a decay per head.  For each sequence and head,
  *     S_t = lam S_{t-1} + k_t^T v_t,   o_t = scale * q_t S_t,
- * lam = exp(log_decay[h]) (log_decay <= 0 in use; -inf, a state that holds
- * the current token only, and growth are allowed), S_0 = initial_state or 0.
+ * lam = exp(log_decay[h]), S_0 = initial_state or 0.  log_decay <= 0 in use;
+ * -inf is a state that holds the current token only, and growth is allowed as
+ * far as lam^T is finite in float32.
  * q has H heads; k and v have HK heads, H a multiple of HK: head h uses key
  * and value head h / (H / HK).  1 <= dk, dv <= 256.
  * lengths (int32 [B], NULL = T each; values are clamped to [0, T]): tokens at

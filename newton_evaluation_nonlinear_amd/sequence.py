@@ -4,7 +4,8 @@ decay per head (include/pn.h holds the definitions, layouts and limits).
 Argument marshalling only, as in the package's other entries.  Token tensors are [B, T, heads, channels] in float32,
 bfloat16 or float16 with adjacent channels and any other strides (views of a packed projection need no copy); states are
 contiguous float32 [B, H, dk, dv].  Every call enqueues on the current stream of the tensors' device and returns without
-waiting; outputs are new contiguous tensors unless stated.
+waiting; outputs are new contiguous tensors unless stated.  Gradients are calls of their own: nothing is recorded for
+autograd (examples/sequence_layer.py wraps the calls in autograd functions).
 """
 
 import ctypes

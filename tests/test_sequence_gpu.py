@@ -416,6 +416,21 @@ def test_norm_of_zero_rows_and_no_eps():
     assert bool(torch.isnan(q[0, 0]).all()) and bool(torch.isfinite(q[0, 1]).all())     # 0 / 0, as the formula says
 
 
+@pytest.mark.parametrize("B, T", [(2, 0), (0, 5)])
+@pytest.mark.parametrize("per_head", [False, True])
+def test_norm_gradients_of_no_token(B, T, per_head):
+    """The weights' gradients are sums over nothing; nothing else is written."""
+    q, k = torch.empty(B, T, 4, 24, device=DEV), torch.empty(B, T, 2, 24, device=DEV)
+    qw, kw = (torch.ones(*((h,) if per_head else ()), 24, device=DEV) for h in (4, 2))
+    table = pn.rotary_table(8, pn.rotary_frequencies(24), device=DEV)
+    for _ in range(3):                                    # over memory that held other values
+        used = torch.full((1 << 16,), 7.0, device=DEV)
+        del used
+        dq, dk, dqw, dkw = pn.qk_norm_rotary_backward(q, k, q, k, qw, kw, table)
+        assert dq.shape == q.shape and dk.shape == k.shape
+        assert dqw.shape == qw.shape and not dqw.any() and dkw.shape == kw.shape and not dkw.any()
+
+
 def test_binding_refusals():
     x = torch.zeros(2, 3, 4, 8, device=DEV)
     t = torch.zeros(16, 4, 2, device=DEV)
