@@ -107,7 +107,7 @@ bool wide(const void* p, int64_t sb, int64_t st, int64_t sh, int D, int elem) {
 }
 bool wide(const LaOperand& x, int D, const LaArgs& a) {
     const int elem = a.dtype == PN_F32 ? 4 : 2;
-    return wide(x.p, a.B > 1 ? x.sb : 0, a.T > 1 ? x.st : 0, a.H / x.div > 1 ? x.sh : 0, D, elem);
+    return wide(x.p, a.B > 1 ? x.sb : 0, x.st, a.H / x.div > 1 ? x.sh : 0, D, elem);
 }
 
 template <typename T>

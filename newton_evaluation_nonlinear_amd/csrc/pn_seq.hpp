@@ -29,7 +29,7 @@ hipError_t launch_rotary_backward(const pn_rotary_args& a, hipStream_t st);
 // with the operands in other places and, for k and v, time reversed.
 struct LaOperand {
     const void* p;
-    int64_t sb, st, sh;
+    int64_t sb, st, sh;      // st is 0 for a single token
     int32_t div;             // head h of the operator reads head h / div
 };
 struct LaOp {

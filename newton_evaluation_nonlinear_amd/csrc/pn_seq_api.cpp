@@ -165,7 +165,9 @@ int check_linattn_sizes(int64_t dtype, int64_t B, int64_t T, int64_t H, int64_t 
     return PN_OK;
 }
 
-LaOperand operand(const pn_tokens& x, int div) { return LaOperand{x.p, x.sb, x.st, x.sh, div}; }
+// The token stride of one token is any number, and is left out: over reversed
+// time the kernel steps back over the tokens that a chunk lacks.
+LaOperand operand(const pn_tokens& x, int64_t T, int div) { return LaOperand{x.p, x.sb, T > 1 ? x.st : 0, x.sh, div}; }
 
 // The operators of a call and the regions of its workspace.
 struct LinattnPlan {
@@ -187,9 +189,9 @@ LinattnPlan plan_linattn(const pn_linattn_args& a, bool backward) {
     char* ws = static_cast<char*>(a.workspace);
     if (!backward) {
         LaOp& f = g.op[0];
-        f.q = operand(a.q, 1);
-        f.k = operand(a.k, share);
-        f.v = operand(a.v, share);
+        f.q = operand(a.q, a.T, 1);
+        f.k = operand(a.k, a.T, share);
+        f.v = operand(a.v, a.T, share);
         f.o = a.o;
         f.DK = dk;
         f.DV = dv;
@@ -209,9 +211,9 @@ LinattnPlan plan_linattn(const pn_linattn_args& a, bool backward) {
         }
         // dq: the state S again, transposed
         LaOp& q = g.op[0];
-        q.q = operand(a.do_, 1);
-        q.k = operand(a.v, share);
-        q.v = operand(a.k, share);
+        q.q = operand(a.do_, a.T, 1);
+        q.k = operand(a.v, a.T, share);
+        q.v = operand(a.k, a.T, share);
         q.o = a.dq;
         q.DK = dv;
         q.DV = dk;
@@ -222,9 +224,9 @@ LinattnPlan plan_linattn(const pn_linattn_args& a, bool backward) {
         q.s_v = dv;
         // dv: the state's gradient R, backwards in time
         LaOp& v = g.op[1];
-        v.q = operand(a.k, share);
-        v.k = operand(a.q, 1);
-        v.v = operand(a.do_, 1);
+        v.q = operand(a.k, a.T, share);
+        v.k = operand(a.q, a.T, 1);
+        v.v = operand(a.do_, a.T, 1);
         v.o = share > 1 ? static_cast<void*>(ws + p.off_dv) : a.dv_;
         v.o_f32 = share > 1;
         v.reverse = 1;
@@ -240,9 +242,9 @@ LinattnPlan plan_linattn(const pn_linattn_args& a, bool backward) {
         v.carry_from = 1;
         // dk: R again, transposed
         LaOp& k = g.op[2];
-        k.q = operand(a.v, share);
-        k.k = operand(a.do_, 1);
-        k.v = operand(a.q, 1);
+        k.q = operand(a.v, a.T, share);
+        k.k = operand(a.do_, a.T, 1);
+        k.v = operand(a.q, a.T, 1);
         k.o = share > 1 ? static_cast<void*>(ws + p.off_dk) : a.dk_;
         k.o_f32 = share > 1;
         k.reverse = 1;
