@@ -363,21 +363,22 @@ size_t pn_qk_norm_rotary_workspace_bytes(const pn_rotary_args* a) {
 int pn_qk_norm_rotary_backward(const pn_rotary_args* a) {
     PN_TRY(check_rotary(a, true, true));
     hipStream_t st = static_cast<hipStream_t>(a->stream);
-    if (a->B == 0 || a->T == 0 || a->hq == 0) {
-        // no token: the weights' gradients are sums over nothing
-        for (int k = 0; k < 2; ++k) {
-            float* d = k ? a->dkw : a->dqw;
-            const int64_t heads = k ? a->hk : a->hq;
-            if (!d || !(k ? a->kw : a->qw)) continue;
-            PN_TRY(launched(launch_fill(d, ((k ? a->kw_sh : a->qw_sh) ? heads : 1) * a->D, st)));
-        }
-        return PN_OK;
+    const bool empty = a->B == 0 || a->T == 0 || a->hq == 0;
+    if (!empty) {
+        const size_t need = norm_workspace(*a);
+        if (!a->workspace || a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < need)
+            return fail(PN_EWORKSPACE, "a workspace of %zu bytes is needed", need);
+        if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign)
+            return fail(PN_EWORKSPACE, "workspace must be 256-byte aligned");
     }
-    const size_t need = norm_workspace(*a);
-    if (!a->workspace || a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < need)
-        return fail(PN_EWORKSPACE, "a workspace of %zu bytes is needed", need);
-    if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign)
-        return fail(PN_EWORKSPACE, "workspace must be 256-byte aligned");
+    // no token, or k without heads: the weights' gradients are sums over nothing
+    for (int k = 0; k < 2; ++k) {
+        float* d = k ? a->dkw : a->dqw;
+        const int64_t heads = k ? a->hk : a->hq;
+        if (!d || !(k ? a->kw : a->qw) || !(empty || heads == 0)) continue;
+        PN_TRY(launched(launch_fill(d, ((k ? a->kw_sh : a->qw_sh) ? heads : 1) * a->D, st)));
+    }
+    if (empty) return PN_OK;
     return launched(launch_rotary_backward(*a, st));
 }
 

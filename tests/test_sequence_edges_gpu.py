@@ -34,3 +34,21 @@ def test_one_token_with_any_token_stride(dtype, st):
         assert torch.equal(x, y)
     table = pn.rotary_table(4, pn.rotary_frequencies(32), device=DEV)
     assert torch.equal(pn.rotary(far["q"], table), pn.rotary(a["q"], table))
+
+
+# ---------------------------------------------------------------- norm gradients
+
+
+def test_norm_gradients_without_key_heads():
+    """k with no heads: the gradient of its weight is a sum over nothing."""
+    D = 24
+    q, k = torch.randn(2, 5, 4, D, device=DEV), torch.empty(2, 5, 0, D, device=DEV)
+    qw, kw = torch.rand(D, device=DEV) + 0.5, torch.ones(D, device=DEV)
+    table = pn.rotary_table(8, pn.rotary_frequencies(D), device=DEV)
+    want = pn.qk_norm_rotary_backward(q, q[:, :, :1], q, q[:, :, :1], qw, None, table)
+    for value in (7.0, float("nan")):                     # over memory that held other values
+        used = [torch.full((D,), value, device=DEV) for _ in range(64)]
+        del used
+        dq, dk, dqw, dkw = pn.qk_norm_rotary_backward(q, k, q, k, qw, kw, table)
+        assert dk.shape == k.shape and torch.equal(dq, want[0]) and torch.equal(dqw, want[2])
+        assert dkw.shape == kw.shape and torch.equal(dkw, torch.zeros_like(kw))
