@@ -19,9 +19,11 @@ namespace {
 // in place, element by element; slot n holds U_n, then S_{n+1}.  Bandwidth: a
 // workgroup takes 1024 elements of one state, so that few form its decays (a
 // thread for each element took 23 us for 3 x 128 states of 128 x 128, so 12).
+// Decays and running state are float64: a float32 decay would be off to the same
+// side at each of up to 127 steps.
 constexpr int kCarryElems = 1024;
 __global__ __launch_bounds__(256) void la_carry(LaChunkArgs g, int blocks) {
-    __shared__ float decay[2];                           // over a whole segment, over the last one
+    __shared__ double decay[2];                          // over a whole segment, over the last one
     const LaOp& op = g.a.op[blockIdx.y];
     const int n = op.DK * op.DV, bh = blockIdx.x / blocks, first = (blockIdx.x - bh * blocks) * kCarryElems;
     if (first >= n) return;
@@ -29,9 +31,9 @@ __global__ __launch_bounds__(256) void la_carry(LaChunkArgs g, int blocks) {
     const int h = bh % g.a.H, b = bh / g.a.H;
     const int64_t len = seq_len(g.a.lengths, b, static_cast<int>(g.a.T));
     if (threadIdx.x < 2)
-        decay[threadIdx.x] = decay_power(g.a.log_decay[h], static_cast<float>(threadIdx.x == 0 ? g.seg : len % g.seg));
+        decay[threadIdx.x] = exp(static_cast<double>(g.a.log_decay[h]) * static_cast<double>(threadIdx.x == 0 ? g.seg : len % g.seg));
     __syncthreads();
-    float s[4];
+    double s[4];
     float* u[4];
     bool on[4];
 #pragma unroll
@@ -39,7 +41,7 @@ __global__ __launch_bounds__(256) void la_carry(LaChunkArgs g, int blocks) {
         const int at = first + k * 256 + threadIdx.x, row = at / op.DV, col = at - row * op.DV;
         on[k] = at < n;
         u[k] = g.carry[blockIdx.y] + static_cast<int64_t>(bh) * n + (on[k] ? at : 0);
-        s[k] = on[k] && op.s_in ? op.s_in[static_cast<int64_t>(bh) * n + row * op.s_k + col * op.s_v] : 0.0f;
+        s[k] = on[k] && op.s_in ? op.s_in[static_cast<int64_t>(bh) * n + row * op.s_k + col * op.s_v] : 0.0;
     }
     const int slots = g.n_seg - 1;
     for (int i0 = 0; i0 < slots; i0 += 4) {
@@ -52,11 +54,11 @@ __global__ __launch_bounds__(256) void la_carry(LaChunkArgs g, int blocks) {
         for (int j = 0; j < 4; ++j) {
             if (i0 + j >= slots) break;
             const int64_t left = len - (i0 + j) * g.seg;
-            const float d = left >= g.seg ? decay[0] : (left <= 0 ? 1.0f : decay[1]);
+            const double d = left >= g.seg ? decay[0] : (left <= 0 ? 1.0 : decay[1]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 s[k] = d * s[k] + x[j][k];
-                if (on[k]) u[k][(i0 + j) * total] = s[k];
+                if (on[k]) u[k][(i0 + j) * total] = static_cast<float>(s[k]);
             }
         }
     }

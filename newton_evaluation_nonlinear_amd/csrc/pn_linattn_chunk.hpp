@@ -426,10 +426,15 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
             reinterpret_cast<u32x4*>(sh.k)[e] = (u32x4)(0u);
             if (OUT) reinterpret_cast<u32x4*>(sh.q)[e] = (u32x4)(0u);
         }
-    if (tid <= kChunk) sh.pw[tid] = decay_power(gl, static_cast<float>(tid));
+    // The tables are written by every thread, the same values to the same places,
+    // not by as many threads as they have entries: after a branch on the thread
+    // the compiler has saved registers to scratch before it restored the mask of
+    // lanes, and lost those of the others (256 rows, float32 and binary16).
+    const int n32 = min(tid, kChunk), m32 = tid % kChunk, m64 = tid % 64;
+    sh.pw[n32] = decay_power(gl, static_cast<float>(n32));
     __syncthreads();
-    if (tid < kChunk) sh.w[tid] = op.ws * sh.pw[kChunk - 1 - tid + (reverse ? 1 : 0)];
-    if (OUT && tid < 64) sh.m[tid] = tid < 32 ? op.inter * op.ws * sh.pw[31 - tid] : 0.0f;
+    sh.w[m32] = op.ws * sh.pw[kChunk - 1 - m32 + (reverse ? 1 : 0)];
+    if (OUT) sh.m[m64] = m64 < 32 ? op.inter * op.ws * sh.pw[31 - m32] : 0.0f;
     const float inter = op.inter * sh.pw[l32 + (reverse ? 0 : 1)];      // of this lane's token
 
     const int64_t state_at = static_cast<int64_t>(bh) * DK * DV;
@@ -477,12 +482,14 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
         kst.store(sh.k, minus);
         vst.store(sh.v, minus);
         if (OUT) qst.store(sh.q, minus);
-        if (L < kChunk && tid < kChunk) sh.w[tid] = tid < L ? op.ws * sh.pw[L - 1 - tid + (reverse ? 1 : 0)] : 0.0f;
+        if (L < kChunk) sh.w[m32] = m32 < L ? op.ws * sh.pw[max(L - 1 - m32, 0) + (reverse ? 1 : 0)] : 0.0f;
     };
     if (i_begin < n_end) {
         __syncthreads();
         stage(n_end - i_begin);
     }
+    float fade = 1.0f;                                   // the state is fade S, fade = lam^since
+    int since = 0;
     for (int i0 = i_begin; i0 < n_end; i0 += kChunk) {
         const int left = n_end - i0, L = min(kChunk, left);
         __syncthreads();
@@ -509,6 +516,12 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
 #pragma unroll
                 for (int x = 0; x < KT; ++x) across_k(t, x, kx[t][x]);
         };
+        // S is faded once lam^since leaves [1/2, 2]; until then what comes in is
+        // scaled up instead.  A factor lam^32 for every chunk, rounded, would
+        // take a state kept for 1024 chunks 7e-5 from its value.
+        const float after = decay_power(gl, static_cast<float>(since + L));
+        const bool keep = after >= 0.5f && after <= 2.0f;
+        const float up = keep ? __builtin_amdgcn_rcpf(after) : 1.0f;
         auto weigh_v = [&](int t) {
             float v8[8];
             sum_parts<NP>(vf[t], v8);
@@ -516,8 +529,8 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
             const Pack<float, 4> w0 = *reinterpret_cast<const Pack<float, 4>*>(w), w1 = *reinterpret_cast<const Pack<float, 4>*>(w + 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                v8[e] *= w0.v[e];
-                v8[4 + e] *= w1.v[e];
+                v8[e] *= up * w0.v[e];
+                v8[4 + e] *= up * w1.v[e];
             }
             split<SP>(v8, wv[t], minus);
         };
@@ -567,7 +580,7 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
 #pragma unroll
                 for (int e = 0; e < 8; ++e) m[t][e] = sh.m[31 - l32 + 16 * t + 8 * half + e];
             load_kx(0);
-            O *= inter;
+            O *= inter * fade;
             bf16x8 pf[2][LIM];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -591,11 +604,15 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
             load_kx(0);
             weigh_v(0);
         }
-        // S = lam^L S + K^T (w V)
-        const float decay = sh.pw[L];
+        // fade S = lam^L fade S + K^T (w V)
         load_kx(1);
+        // (of three parts without a branch, 152 us for 156 of a ragged float32
+        // batch; of one and two with it, 618 for 636 of a bfloat16 training pass)
+        if (NP == 3 || !keep)
 #pragma unroll
-        for (int t = 0; t < KT; ++t) S[t] *= decay;
+            for (int t = 0; t < KT; ++t) S[t] *= keep ? 1.0f : after;
+        fade = keep ? after : 1.0f;
+        since = keep ? since + L : 0;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -627,14 +644,14 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) to[(32 * t + 16 * (r / 8) + 8 * half + r % 8) * DV] = S[t][r];
+                for (int r = 0; r < 16; ++r) to[(32 * t + 16 * (r / 8) + 8 * half + r % 8) * DV] = fade * S[t][r];
         } else {
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int row = 32 * t + 16 * (r / 8) + 8 * half + r % 8;
-                    if (row < DK) to[row * DV] = S[t][r];
+                    if (row < DK) to[row * DV] = fade * S[t][r];
                 }
         }
     }

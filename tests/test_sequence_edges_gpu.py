@@ -3,13 +3,25 @@
 Tolerances are those of test_sequence_gpu.py unless a test derives its own.
 """
 
+import numpy as np
 import pytest
 import torch
 
 import newton_evaluation_nonlinear_amd as pn
-from test_sequence_gpu import DEV, TYPES, _inputs
+from newton_evaluation_nonlinear_amd import sequence as seq
+from test_sequence_gpu import DEV, TYPES, _close, _inputs, _np
 
 pytestmark = pytest.mark.gpu
+
+EPS = 2.0 ** -24
+
+
+def _segments(dtype, B, T, H, HK, DK, DV):
+    """Segments of the time axis of a forward call, from the workspace that holds the states between them."""
+    code = {"f32": 0, "bf16": 1, "f16": 2}[dtype]
+    block = seq._ATTENTION(code, B, T, H, HK, DK, DV, 1.0, *[0] * 29)
+    n = pn.lib().pn_linear_attention_workspace_bytes(block, 0)
+    return 1 if n <= 256 else 1 + n // (4 * B * H * DK * DV)
 
 
 # ---------------------------------------------------------------- strides
@@ -52,3 +64,32 @@ def test_norm_gradients_without_key_heads():
         dq, dk, dqw, dkw = pn.qk_norm_rotary_backward(q, k, q, k, qw, kw, table)
         assert dk.shape == k.shape and torch.equal(dq, want[0]) and torch.equal(dqw, want[2])
         assert dkw.shape == kw.shape and torch.equal(dkw, torch.zeros_like(kw))
+
+
+# ---------------------------------------------------------------- long memories
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("B, H, T, segments", [(64, 8, 32768, 1), (1, 8, 65536, 0)])
+def test_long_memories_do_not_drift(dtype, B, H, T, segments):
+    """A state carried over tokens that add nothing is e^{g T} of itself, and its gradient likewise.
+
+    Bound: of the decay's power (4 roundings, and the float32 exponent's 2^-24 of it per step of the result's size), and one
+    rounding for each factor of about 2 that the state fades by, or each segment; nothing else may grow with T."""
+    D = 4
+    g = torch.Generator().manual_seed(2)
+    ld = -torch.tensor([1.3e-7, 1e-6, 3e-6, 1e-5, 3e-5, 9.3e-5, 3e-4, 1e-3], device=DEV)
+    s0, dS = (1.0 + torch.rand(B, H, D, D, generator=g).to(DEV) for _ in range(2))
+    n = _segments(dtype, B, T, H, H, D, D)
+    assert n == segments if segments else n > 1
+    print(f"[long memories] {dtype} B={B} T={T} segments={n}", flush=True)
+    zero = torch.zeros(1, 1, 1, D, dtype=TYPES[dtype], device=DEV).expand(B, T, H, D)
+    one = torch.ones(1, 1, 1, D, dtype=TYPES[dtype], device=DEV).expand(B, T, H, D)
+    S = pn.linear_attention(one, zero, one, ld, initial_state=s0, scale=1.0)[1]
+    back = pn.linear_attention_backward(zero, one, zero, one, ld, initial_state=s0, d_final_state=dS, scale=1.0)
+    g64 = _np(ld)
+    fade = np.exp(g64 * T)[None, :, None, None]
+    steps = (1.0 + np.abs(g64) * T / np.log(2.0) + n)[None, :, None, None]
+    for got, x, what in ((S, s0, "state"), (back[3], dS, "d initial state")):
+        want = _np(x) * fade
+        _close(got, want, 6 * EPS * steps * want, what)
