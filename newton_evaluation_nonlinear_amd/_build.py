@@ -7,6 +7,7 @@ file is self-contained), then the objects are linked into libpn.so; the
 ceiling microbenchmarks (pn_ceiling.hip) become libpn_ceiling.so.
 """
 
+import glob
 import os
 import subprocess
 import sys
@@ -50,13 +51,42 @@ def _run(cmd):
     return r.stderr
 
 
+def lost_lanes(asm):
+    """Kernels in gfx950 assembly (its lines) that save a register to scratch after a branch on lanes, in the block where they
+    meet, before the mask of all lanes is restored: the compiler has done so, and the other lanes then read back garbage."""
+    found, name, saved = [], "", False
+    for line in asm:
+        code = line.split(";")[0].split()
+        if line.startswith("_Z"):
+            name, saved = line.split(":")[0], False
+        elif line.startswith(".LBB") or "; %bb." in line or code and code[0].startswith(("s_cbranch", "s_branch", "s_endpgm")):
+            saved = False
+        elif code and code[0].startswith("scratch_store"):
+            saved = True
+        elif saved and code and code[0] == "s_or_b64" and code[1:3] == ["exec,", "exec,"]:
+            found.append(name)
+            saved = False
+    return found
+
+
+def check_lanes(folder):
+    """Raise if assembly files of ``folder`` hold such kernels."""
+    for path in sorted(glob.glob(os.path.join(folder, "*gfx950.s"))):
+        with open(path) as f:
+            found = lost_lanes(f)
+        if found:
+            raise RuntimeError(f"{os.path.basename(path)}: registers saved under a narrowed lane mask in {', '.join(found)}; "
+                               "write the branch on the thread index before it without a branch")
+
+
 def build(verbose=False):
     with tempfile.TemporaryDirectory(prefix="pn_build_") as tmpd:
         objs, cmds = [], []
         for src in SOURCES:
             obj = os.path.join(tmpd, src + ".o")
             objs.append(obj)
-            cmds.append([hipcc()] + FLAGS + ["-I", os.path.join(ROOT, "include"), "-c",
+            # the assembly is kept beside the object for check_lanes()
+            cmds.append([hipcc()] + FLAGS + ["--save-temps=obj", "-I", os.path.join(ROOT, "include"), "-c",
                                              os.path.join(CSRC, src), "-o", obj])
         cobjs = []
         for src in CEILING_SOURCES:
@@ -67,6 +97,7 @@ def build(verbose=False):
         workers = min(len(cmds), max(1, (os.cpu_count() or 1)))
         with ThreadPoolExecutor(max_workers=workers) as ex:
             logs = list(ex.map(_run, cmds))
+        check_lanes(tmpd)
         tmp = LIB + ".tmp"
         logs.append(_run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs))
         ctmp = CEILING_LIB + ".tmp"
