@@ -9,6 +9,8 @@
 // so the gradients are the same operator: dq with (Q, K, V) = (do, v, k), and,
 // over reversed time, dv with (k, q, do) and dk with (v, do, q).
 
+#include <algorithm>
+
 #include "pn_linattn_chunk.hpp"
 
 namespace pn {
@@ -114,7 +116,7 @@ bool wide(const LaOperand& x, int D, const LaArgs& a) {
 
 template <typename T>
 __global__ __launch_bounds__(256) void la_group_sum(const float* in, T* out, int64_t n, int G, int D) {
-    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t e = static_cast<int64_t>(block_id()) * 256 + threadIdx.x;
     if (e >= n) return;
     const int64_t row = e / D;
     const int d = static_cast<int>(e - row * D);
@@ -238,6 +240,19 @@ size_t linattn_workspace(const LaArgs& a) {
     return n;
 }
 
+bool linattn_fits(const LaArgs& a) {
+    int64_t seg, state = 0;
+    int n_seg, dv = 0;
+    segments(a, &seg, &n_seg);
+    for (int w = 0; w < a.n_ops; ++w) {
+        dv = a.op[w].DV > dv ? a.op[w].DV : dv;
+        state = std::max<int64_t>(state, a.op[w].DK * a.op[w].DV);
+    }
+    const int64_t heads = static_cast<int64_t>(a.B) * a.H, limit = int64_t(1) << 32;
+    const int64_t cols = 32 * la_waves(a), chunks = heads * n_seg * a.n_ops * ((dv + cols - 1) / cols);
+    return chunks * 2 * cols < limit && (n_seg == 1 || heads * ((state + kCarryElems - 1) / kCarryElems) * 256 < limit);
+}
+
 hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st) {
     LaChunkArgs g{};
     g.a = a;
@@ -298,7 +313,7 @@ hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st) {
 
 hipError_t launch_group_sum(const float* in, void* out, int dtype, int64_t rows, int G, int D, hipStream_t st) {
     const int64_t n = rows * D;
-    const dim3 grid(static_cast<uint32_t>((n + 255) / 256));
+    const dim3 grid = grid_of((n + 255) / 256, 256);
     switch (dtype) {
         case PN_F32: la_group_sum<float><<<grid, 256, 0, st>>>(in, static_cast<float*>(out), n, G, D); break;
         case PN_BF16: la_group_sum<bf16><<<grid, 256, 0, st>>>(in, static_cast<bf16*>(out), n, G, D); break;

@@ -32,7 +32,7 @@ struct TableFreq {
 };
 __global__ __launch_bounds__(kBlock) void fill_table(TableFreq freq, int n_freq, int64_t n, double magnitude,
                                                      float* table) {
-    const int64_t e = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+    const int64_t e = static_cast<int64_t>(block_id()) * kBlock + threadIdx.x;
     if (e >= n) return;
     const int64_t p = e / n_freq;
     double s, c;
@@ -187,7 +187,7 @@ __device__ __forceinline__ int64_t position(const pn_rotary_args& a, int64_t b, 
 // tokens of 16 heads of 128).
 template <typename T, int V, int NU, bool INTER, bool NORM>
 __global__ __launch_bounds__(kBlock) void rotate(pn_rotary_args a, Cut cut, int per, int splits) {
-    const int64_t g = static_cast<int64_t>(blockIdx.x) * (kBlock / cut.L) + threadIdx.x / cut.L;
+    const int64_t g = static_cast<int64_t>(block_id()) * (kBlock / cut.L) + threadIdx.x / cut.L;
     const int lane = threadIdx.x & (cut.L - 1);
     const int64_t token = g / splits;
     if (token >= a.B * a.T) return;
@@ -237,8 +237,9 @@ __global__ __launch_bounds__(kBlock) void norm_rotate_backward(pn_rotary_args a,
     extern __shared__ float red[];
     const int D = static_cast<int>(a.D), R = static_cast<int>(a.R), hq = static_cast<int>(a.hq);
     const int groups = kBlock / cut.L, group = threadIdx.x / cut.L, lane = threadIdx.x & (cut.L - 1);
-    const int heads = static_cast<int>(a.hq + a.hk);
-    const int h = blockIdx.x % heads, wg = blockIdx.x / heads;
+    const uint32_t id = block_id(), heads = static_cast<uint32_t>(a.hq + a.hk);
+    const int h = static_cast<int>(id % heads), wg = static_cast<int>(id / heads);
+    if (wg >= n_wg) return;
     const bool isq = h < hq;
     const int hh = isq ? h : h - hq;
     const Lane<T, V, NU, INTER> ln(cut, lane, D, R);
@@ -305,12 +306,16 @@ __global__ __launch_bounds__(1024) void weight_sum(const float* part, int D, int
     __shared__ double red[16][65];
     const int col = threadIdx.x % 64, lane = threadIdx.x / 64;
     const int nq = dqw ? (q_own ? hq : 1) : 0;
-    const bool isq = static_cast<int>(blockIdx.y) < nq;
-    const int own = isq ? blockIdx.y : blockIdx.y - nq;
+    const int nk = dkw ? (k_own ? hk : 1) : 0;
+    const uint32_t col_blocks = (D + 63) / 64, id = block_id();
+    const int sum = static_cast<int>(id / col_blocks);
+    if (sum >= nq + nk) return;
+    const bool isq = sum < nq;
+    const int own = isq ? sum : sum - nq;
     const bool each = isq ? q_own : k_own;
     const int head = (isq ? 0 : hq) + (each ? own : 0);
     const int64_t rows = static_cast<int64_t>(each ? 1 : (isq ? hq : hk)) * n_wg;
-    const int c = blockIdx.x * 64 + col;
+    const int c = static_cast<int>(id % col_blocks) * 64 + col;
     const float* p = part + static_cast<int64_t>(head) * n_wg * D + c;
     double s = 0.0;
     if (c < D)
@@ -326,7 +331,7 @@ __global__ __launch_bounds__(1024) void weight_sum(const float* part, int D, int
     if (lane == 0 && c < D) {
         double v = 0.0;
         for (int i = 0; i < 16; ++i) v += red[i][col];
-        (isq ? dqw : dkw)[(each ? own : 0) * D + c] = static_cast<float>(v);
+        (isq ? dqw : dkw)[static_cast<int64_t>(each ? own : 0) * D + c] = static_cast<float>(v);
     }
 }
 
@@ -395,7 +400,7 @@ hipError_t rotate_typed(const pn_rotary_args& a, hipStream_t st) {
     while (per < 8 && per < heads && rows / rows_per_wave / (2 * per) >= kFillWaves) per *= 2;
     const int splits = (heads + per - 1) / per;
     const int64_t groups = a.B * a.T * splits, per_block = kBlock / c.L;
-    const dim3 grid(static_cast<uint32_t>((groups + per_block - 1) / per_block));
+    const dim3 grid = grid_of((groups + per_block - 1) / per_block, kBlock);
     return with_form<T>(V, c, [&](auto form) {
         constexpr int W = decltype(form)::V, NU = decltype(form)::NU;
         if (a.interleaved) rotate<T, W, NU, true, NORM><<<grid, kBlock, 0, st>>>(a, c, per, splits);
@@ -422,7 +427,7 @@ hipError_t backward_typed(const pn_rotary_args& a, hipStream_t st) {
     int64_t tokens;
     backward_split(a, &n_wg, &tokens);
     float* part = static_cast<float*>(a.workspace);
-    const dim3 grid(static_cast<uint32_t>(n_wg * (a.hq + a.hk)));
+    const dim3 grid = grid_of(n_wg * (a.hq + a.hk), kBlock);
     const size_t lds = sizeof(float) * (kBlock / c.L) * a.D;
     hipError_t e = with_form<T>(V, c, [&](auto form) {
         constexpr int W = decltype(form)::V, NU = decltype(form)::NU;
@@ -436,8 +441,8 @@ hipError_t backward_typed(const pn_rotary_args& a, hipStream_t st) {
     float* dkw = a.kw && a.hk ? a.dkw : nullptr;
     if (e != hipSuccess || (!dqw && !dkw)) return e;
     const int q_own = a.qw_sh != 0, k_own = a.kw_sh != 0;
-    const uint32_t sums = (dqw ? (q_own ? a.hq : 1) : 0) + (dkw ? (k_own ? a.hk : 1) : 0);
-    weight_sum<<<dim3(static_cast<uint32_t>((a.D + 63) / 64), sums), 1024, 0, st>>>(
+    const int64_t sums = (dqw ? (q_own ? a.hq : 1) : 0) + (dkw ? (k_own ? a.hk : 1) : 0);
+    weight_sum<<<grid_of((a.D + 63) / 64 * sums, 1024), 1024, 0, st>>>(
         part, static_cast<int>(a.D), n_wg, static_cast<int>(a.hq), static_cast<int>(a.hk), q_own, k_own, dqw, dkw);
     return hipGetLastError();
 }
@@ -454,18 +459,18 @@ hipError_t launch_rotary_table(const double* freq, int n_freq, int64_t n_pos, do
     TableFreq f{};
     for (int i = 0; i < n_freq; ++i) f.f[i] = freq[i];
     const int64_t n = n_pos * n_freq;
-    fill_table<<<dim3(static_cast<uint32_t>((n + kBlock - 1) / kBlock)), kBlock, 0, st>>>(f, n_freq, n, magnitude, table);
+    fill_table<<<grid_of((n + kBlock - 1) / kBlock, kBlock), kBlock, 0, st>>>(f, n_freq, n, magnitude, table);
     return hipGetLastError();
 }
 
 __global__ __launch_bounds__(kBlock) void fill_zero(float* p, int64_t n) {
-    const int64_t e = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+    const int64_t e = static_cast<int64_t>(block_id()) * kBlock + threadIdx.x;
     if (e < n) p[e] = 0.0f;
 }
 
 hipError_t launch_fill(float* p, int64_t n, hipStream_t st) {
     if (n <= 0) return hipSuccess;
-    fill_zero<<<dim3(static_cast<uint32_t>((n + kBlock - 1) / kBlock)), kBlock, 0, st>>>(p, n);
+    fill_zero<<<grid_of((n + kBlock - 1) / kBlock, kBlock), kBlock, 0, st>>>(p, n);
     return hipGetLastError();
 }
 

@@ -14,6 +14,13 @@ namespace pn {
 int set_error(int code, const char* msg);
 void clear_error();
 
+// A launch of `blocks` workgroups, along x and y: HIP takes less than 2^32
+// threads along one of them.  The last of them have no work (block_id()).
+inline dim3 grid_of(int64_t blocks, int threads) {
+    const int64_t most = (int64_t(1) << 31) / threads, x = blocks < most ? blocks : most;
+    return dim3(static_cast<uint32_t>(x), static_cast<uint32_t>((blocks + x - 1) / x));
+}
+
 hipError_t launch_rotary_table(const double* freq, int n_freq, int64_t n_pos, double magnitude, float* table,
                                hipStream_t st);
 
@@ -57,6 +64,7 @@ struct LaArgs {
     const int32_t* lengths;
 };
 size_t linattn_workspace(const LaArgs& a);      // bytes; sizes of `a` only
+bool linattn_fits(const LaArgs& a);             // whether its launches can be made
 hipError_t launch_linattn(const LaArgs& a, void* workspace, hipStream_t st);
 // out[b, t, x, d] = sum over g of in[b, t, x * G + g, d]
 hipError_t launch_group_sum(const float* in, void* out, int dtype, int64_t rows, int G, int D, hipStream_t st);

@@ -300,7 +300,9 @@ int check_linattn(const pn_linattn_args* p, bool backward) {
         out[0] = range(a.o, e * a.B * a.T * a.H * a.dv);
         out[1] = range(a.final_state, ns);
     }
-    const size_t need = plan_linattn(a, backward).total;
+    const LinattnPlan plan = plan_linattn(a, backward);
+    if (!linattn_fits(plan.la)) return fail(PN_EUNSUPPORTED, "too many sequences and heads for one launch");
+    const size_t need = plan.total;
     if (need > 0) {
         if (!a.workspace || a.workspace_bytes < 0 || static_cast<size_t>(a.workspace_bytes) < need)
             return fail(PN_EWORKSPACE, "a workspace of %zu bytes is needed", need);
@@ -390,8 +392,12 @@ size_t pn_linear_attention_workspace_bytes(const pn_linattn_args* a, int32_t bac
     }
     if (check_linattn_sizes(a->dtype, a->B, a->T, a->H, a->HK, a->dk, a->dv, a->scale) != PN_OK) return 0;
     if (a->B == 0 || a->H == 0) return kAlign;
-    const size_t n = plan_linattn(*a, backward != 0).total;
-    return n > 0 ? n : kAlign;
+    const LinattnPlan plan = plan_linattn(*a, backward != 0);
+    if (!linattn_fits(plan.la)) {
+        fail(PN_EUNSUPPORTED, "too many sequences and heads for one launch");
+        return 0;
+    }
+    return plan.total > 0 ? plan.total : kAlign;
 }
 
 int pn_linear_attention(const pn_linattn_args* a) {
@@ -424,6 +430,7 @@ int pn_linear_attention_step(const pn_linattn_step_args* p) {
     if (!p) return fail(PN_EINVAL, "the arguments are NULL");
     const pn_linattn_step_args& a = *p;
     PN_TRY(check_linattn_sizes(a.dtype, a.B, 1, a.H, a.HK, a.dk, a.dv, a.scale));
+    if (a.B * a.H * 256 >= int64_t(1) << 32) return fail(PN_EUNSUPPORTED, "too many sequences and heads for one launch");
     if (a.n_slots < 0 || a.n_slots > (int64_t(1) << 31)) return fail(PN_EINVAL, "n_slots out of range");
     if (a.B == 0 || a.H == 0) return PN_OK;
     const int64_t e = elem_bytes(a.dtype);

@@ -15,6 +15,9 @@ struct alignas(sizeof(T) * N) Pack {
     T v[N];
 };
 
+// The workgroup's number in a launch of grid_of(); below 2^32.
+__device__ __forceinline__ uint32_t block_id() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Round to nearest even; NaN stays NaN.
 template <typename T>
 __device__ __forceinline__ T from_f32(float x) { return static_cast<T>(x); }

@@ -9,7 +9,8 @@ import torch
 
 import newton_evaluation_nonlinear_amd as pn
 from newton_evaluation_nonlinear_amd import sequence as seq
-from test_sequence_gpu import DEV, TYPES, _close, _inputs, _np
+from oracle import sequence as ref
+from test_sequence_gpu import DEV, TYPES, _close, _inputs, _np, _rand
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +94,61 @@ def test_long_memories_do_not_drift(dtype, B, H, T, segments):
     for got, x, what in ((S, s0, "state"), (back[3], dS, "d initial state")):
         want = _np(x) * fade
         _close(got, want, 6 * EPS * steps * want, what)
+
+
+# ---------------------------------------------------------------- launches past 2^32 threads
+
+
+def test_shared_head_gradients_past_2_32_elements():
+    """With a state that holds the current token only and v = do = 1, dk is the sum of scale q over the heads that share it:
+    exact in float32, so that every one of 2^32 elements is known to the bit."""
+    B, T, H, HK, D = 16, 65536, 64, 32, 128
+    q = _rand(torch.Generator().manual_seed(1), (1, 1, H, D), "bf16")
+    one = torch.ones(1, 1, 1, 1, dtype=torch.bfloat16, device=DEV)
+    ld = torch.full((H,), float("-inf"), device=DEV)
+    print("[shared heads] 2^32 elements", flush=True)
+    _, dk, dv, _ = pn.linear_attention_backward(one.expand(B, T, H, 1), q.expand(B, T, H, D), q[:, :, :HK].expand(B, T, HK, D),
+                                                one.expand(B, T, HK, 1), ld, scale=0.5)
+    want = (0.5 * q.float()).view(HK, 2, D).sum(1).bfloat16()
+    for b in range(B):
+        assert bool((dk[b] == want).all()), b
+    assert bool((dv == dv[:1, :1]).all())
+
+
+def test_rotary_past_2_32_threads():
+    T, D = 1 << 27, 33                                    # single channels: 32 lanes a row
+    x = _rand(torch.Generator().manual_seed(1), (1, 1, 1, D), "bf16")
+    table = pn.rotary_table(8, pn.rotary_frequencies(2), device=DEV)
+    at = torch.tensor([3], device=DEV)
+    print("[rotary] 2^27 rows of 33 channels", flush=True)
+    y = pn.rotary(x.expand(1, T, 1, D), table, at.expand(T))
+    want = pn.rotary(x, table, at)
+    for t in range(0, T, T // 16):
+        assert bool((y[:, t:t + T // 16] == want).all()), t
+
+
+def test_rotary_table_past_2_32_entries():
+    n_pos, n_freq = 1 << 25, 128
+    f = pn.rotary_frequencies(2 * n_freq)
+    print("[rotary table] 2^32 entries", flush=True)
+    t = pn.rotary_table(n_pos, f, device=DEV)
+    at = np.array([0, 1, 12345, n_pos // 2, n_pos - 2, n_pos - 1])
+    got = _np(t[torch.tensor(at, device=DEV)])
+    c, s = ref.angles(at, f)
+    assert np.all(np.abs(got[..., 0] - c) <= EPS * np.abs(c) + 2.0 ** -50 * n_pos)
+    assert np.all(np.abs(got[..., 1] - s) <= EPS * np.abs(s) + 2.0 ** -50 * n_pos)
+
+
+def test_norm_gradients_of_many_heads():
+    """A weight for each of 70000 heads: more sums than a launch has workgroups along y."""
+    H, D, eps = 70000, 2, 1e-5
+    g = torch.Generator().manual_seed(8)
+    q, dy = _rand(g, (1, 2, H, D), "f32"), _rand(g, (1, 2, H, D), "f32")
+    w = 1.0 + 0.3 * _rand(g, (H, D), "f32")
+    table = pn.rotary_table(4, pn.rotary_frequencies(D), device=DEV)
+    none = q[:, :, :0]
+    dq, _, dqw, _ = pn.qk_norm_rotary_backward(dy, none, q, none, w, None, table, eps=eps)
+    t = _np(table)[np.arange(2)][None]
+    dx, dw, bdx, bdw = ref.norm_rotate_backward(_np(dy), _np(q), _np(w), t[..., 0], t[..., 1], eps)
+    _close(dq, dx, EPS * np.abs(dx) + (3 * D + 32) * EPS * bdx, "dq")
+    _close(dqw, dw, (2 + D + 16) * EPS * bdw, "dw")

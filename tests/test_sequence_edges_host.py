@@ -1,0 +1,26 @@
+"""Refusals of the sequence-layer entries at extreme sizes and arguments, without a GPU (placeholder addresses; nothing is
+dereferenced)."""
+
+import pytest
+
+import newton_evaluation_nonlinear_amd as pn
+from test_sequence_host import GIB, TOK, _attention_block, _no_error_left, _rotary_block, _step_block  # noqa: F401
+
+
+@pytest.mark.parametrize("sizes, backward", [(dict(B=1 << 24, H=1, HK=1, T=1, dk=1, dv=1), True),
+                                             (dict(B=1 << 12, H=1 << 12, HK=1, T=1, dk=8, dv=130), False),
+                                             (dict(B=1 << 12, H=1 << 10, HK=1, T=1, dk=200, dv=8), True)])
+def test_launches_past_2_32_threads_are_refused_first(sizes, backward):
+    """What no launch can hold is an error of the arguments, found before any work is queued."""
+    lib = pn.lib()
+    far = TOK(4, 8, 8, 8), TOK(5, 8, 8, 8), TOK(6, 8, 8, 8)
+    block = _attention_block(dtype=1, q=far[0], k=far[1], v=far[2], **sizes)
+    f = lib.pn_linear_attention_backward if backward else lib.pn_linear_attention
+    assert f(block) == pn.EUNSUPPORTED and pn.last_error() != ""
+    assert lib.pn_linear_attention_workspace_bytes(block, int(backward)) == 0 and pn.last_error() != ""
+
+
+def test_steps_past_2_32_threads_are_refused():
+    f = pn.lib().pn_linear_attention_step
+    assert f(_step_block(B=1 << 24, H=1, HK=1, dk=1, dv=1, n_slots=1 << 24)) == pn.EUNSUPPORTED
+    assert f(_step_block(B=1 << 12, H=1 << 12, HK=1, dk=1, dv=1, n_slots=1 << 12)) == pn.EUNSUPPORTED
