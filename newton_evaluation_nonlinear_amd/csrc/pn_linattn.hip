@@ -131,7 +131,8 @@ __global__ __launch_bounds__(256) void la_group_sum(const float* in, T* out, int
 // rows, every group 8 rows at a time, all loads of which are issued before
 // the first store.  For a slow decay lam S + k v is taken as
 // S + (S (lam - 1) + k v): lam - 1 keeps it exact over many steps, where lam
-// itself, rounded, would be off by up to 2^-25 at each.
+// itself, rounded, would be off by up to 2^-25 at each.  (S times
+// lam - 1 takes an infinite S as the largest finite one, or the sum were a NaN.)
 // Measured: 256 sequences of 16 heads, 128 x 128 (537 MB), 112 us, 4.8 TB/s, the
 // rate of a large copy; 4 sequences 5.4 us.
 template <typename T, int V, int LC>
@@ -189,7 +190,8 @@ __global__ __launch_bounds__(256) void la_step(pn_linattn_step_args a) {
             Pack<float, V> n;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float t = fmaf(x[j][i], f, k * v[i]);
+                const float finite = __builtin_amdgcn_fmed3f(x[j][i], -3.402823466e38f, 3.402823466e38f);
+                const float t = fmaf(slow ? finite : x[j][i], f, k * v[i]);
                 n.v[i] = slow ? x[j][i] + t : t;
                 acc[i] = fmaf(q, n.v[i], acc[i]);
             }

@@ -96,6 +96,50 @@ def test_long_memories_do_not_drift(dtype, B, H, T, segments):
         _close(got, want, 6 * EPS * steps * want, what)
 
 
+# ---------------------------------------------------------------- non-finite values
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_nan_reaches_at_most_31_tokens_the_other_way(dtype):
+    """Of a NaN token: the outputs from it on; of the ones before it at most 31; in the gradients of k and v, which run
+    backwards, the tokens after it; other heads and sequences not at all."""
+    a = _inputs(dtype, 2, 300, 2, 2, 32, 32, False)
+    at, args = 200, ("q", "k", "v", "log_decay")
+    clean = pn.linear_attention(*(a[n] for n in args))[0]
+    for name in ("k", "v"):
+        x = {**a, name: a[name].clone()}
+        x[name][1, at, 1] = float("nan")
+        o = pn.linear_attention(*(x[n] for n in args))[0]
+        assert torch.equal(o[0], clean[0]) and torch.equal(o[1, :, 0], clean[1, :, 0]), name
+        assert torch.equal(o[1, :at - 31, 1], clean[1, :at - 31, 1]), name
+        assert bool(torch.isnan(o[1, at:, 1]).all()), name
+    clean = pn.linear_attention_backward(*(a[n] for n in ("do",) + args))
+    for name in ("q", "do"):
+        x = {**a, name: a[name].clone()}
+        x[name][1, at, 1] = float("nan")
+        got = pn.linear_attention_backward(*(x[n] for n in ("do",) + args))
+        for y, z in zip(got[1:3], clean[1:3]):            # dk, dv
+            assert torch.equal(y[0], z[0]) and torch.equal(y[1, :, 0], z[1, :, 0]), name
+            assert torch.equal(y[1, at + 32:, 1], z[1, at + 32:, 1]), name
+            assert bool(torch.isnan(y[1, :at + 1, 1]).all()), name
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("DV", [32, 7])
+def test_step_keeps_infinities(dtype, DV):
+    """lam S + k v of an infinite S is that infinity, for any decay above 0; of the others nothing changes."""
+    B, H, DK = 2, 4, 16
+    a = _inputs(dtype, B, 1, H, H, DK, DV, True, seed=9)
+    a["log_decay"] = torch.tensor([0.0, -1e-5, -0.3, -3.0], device=DEV)
+    state = a["initial_state"].clone()
+    state[:, :, 3, 2], state[:, :, 5, 4] = float("inf"), float("-inf")
+    clean = a["initial_state"].clone()
+    pn.linear_attention_step(a["q"][:, 0], a["k"][:, 0], a["v"][:, 0], a["log_decay"], clean)
+    pn.linear_attention_step(a["q"][:, 0], a["k"][:, 0], a["v"][:, 0], a["log_decay"], state)
+    clean[:, :, 3, 2], clean[:, :, 5, 4] = float("inf"), float("-inf")
+    assert torch.equal(state, clean)
+
+
 # ---------------------------------------------------------------- launches past 2^32 threads
 
 
