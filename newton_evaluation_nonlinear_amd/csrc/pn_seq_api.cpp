@@ -148,6 +148,8 @@ int check_rotary(const pn_rotary_args* p, bool norm, bool backward) {
             for (const Range& r : aux) bad = bad || overlap(o, r);
         }
         bad = bad || overlap(w[0], w[1]);
+        const Range ws = range(a.workspace, static_cast<int64_t>(norm_workspace(a)));
+        for (const Range& r : {qi, ki, dqi, dki, qo, ko, w[0], w[1], aux[0], aux[1], aux[2], aux[3]}) bad = bad || overlap(ws, r);
     }
     if (bad) return fail(PN_EINVAL, "an output overlaps an input or another output");
     return PN_OK;

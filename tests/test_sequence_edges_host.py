@@ -24,3 +24,11 @@ def test_steps_past_2_32_threads_are_refused():
     f = pn.lib().pn_linear_attention_step
     assert f(_step_block(B=1 << 24, H=1, HK=1, dk=1, dv=1, n_slots=1 << 24)) == pn.EUNSUPPORTED
     assert f(_step_block(B=1 << 12, H=1 << 12, HK=1, dk=1, dv=1, n_slots=1 << 12)) == pn.EUNSUPPORTED
+
+
+@pytest.mark.parametrize("at", [4, 5, 6, 7, 8, 9, 10, 12, 14, 15])
+def test_norm_gradients_refuse_a_workspace_over_other_arrays(at):
+    kw = dict(qw=12 * GIB, kw=12 * GIB + 4096, dqw=14 * GIB, dkw=15 * GIB)
+    n = pn.lib().pn_qk_norm_rotary_workspace_bytes(_rotary_block(**kw))
+    assert pn.lib().pn_qk_norm_rotary_backward(_rotary_block(**kw, ws=at * GIB, wsn=n)) == pn.EINVAL
+    assert "overlaps" in pn.last_error()
