@@ -108,6 +108,8 @@ int check_rotary(const pn_rotary_args* p, bool norm, bool backward) {
     if (a.R > 0) {
         if (!a.table) return fail(PN_EINVAL, "table is NULL");
         if (a.n_pos < 0 || !small_product({a.n_pos, a.R}, int64_t(1) << 40)) return fail(PN_EINVAL, "n_pos out of range");
+    }
+    if (a.positions) {                                   // read whatever R is
         if (a.pos64 < 0 || a.pos64 > 1) return fail(PN_EINVAL, "pos64 must be 0 or 1");
         if (a.pos_sb < 0 || a.pos_st < 0 || a.pos_sb > kMaxStride || a.pos_st > kMaxStride)
             return fail(PN_EINVAL, "a stride of positions is out of range");
@@ -133,9 +135,7 @@ int check_rotary(const pn_rotary_args* p, bool norm, bool backward) {
     bad = bad || (overlap(qo, qi) && !in_place(a.q, a.q_out, a.hq));
     bad = bad || (a.hk && overlap(ko, ki) && !in_place(a.k, a.k_out, a.hk));
     const Range aux[4] = {range(a.table, a.R > 0 ? 4 * a.n_pos * a.R : 0),
-                          range(a.positions, a.R > 0 && a.positions
-                                                 ? (a.pos64 ? 8 : 4) * ((a.B - 1) * a.pos_sb + (a.T - 1) * a.pos_st + 1)
-                                                 : 0),
+                          range(a.positions, a.positions ? (a.pos64 ? 8 : 4) * ((a.B - 1) * a.pos_sb + (a.T - 1) * a.pos_st + 1) : 0),
                           range(norm ? a.qw : nullptr, 4 * (a.qw_sh ? a.hq * a.D : a.D)),
                           range(norm ? a.kw : nullptr, 4 * (a.kw_sh ? a.hk * a.D : a.D))};
     for (const Range& r : aux) bad = bad || overlap(qo, r) || overlap(ko, r);

@@ -32,3 +32,10 @@ def test_norm_gradients_refuse_a_workspace_over_other_arrays(at):
     n = pn.lib().pn_qk_norm_rotary_workspace_bytes(_rotary_block(**kw))
     assert pn.lib().pn_qk_norm_rotary_backward(_rotary_block(**kw, ws=at * GIB, wsn=n)) == pn.EINVAL
     assert "overlaps" in pn.last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(pos=12 * GIB, pos64=2), dict(pos=12 * GIB + 4, pos64=1), dict(pos=12 * GIB, pst=-1),
+                                dict(pos=12 * GIB, psb=1 << 41), dict(pos=6 * GIB)])
+def test_positions_are_checked_without_a_rotation_too(kw):
+    for name in ("pn_rotary", "pn_qk_norm_rotary", "pn_qk_norm_rotary_backward"):
+        assert getattr(pn.lib(), name)(_rotary_block(R=0, **kw)) == pn.EINVAL, name
