@@ -15,8 +15,9 @@ import struct
 import torch
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (a torch without device bindings has no tensors to call them for)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 # Argument blocks of include/pn.h: every field is 8 bytes wide.
 _ROTARY = struct.Struct("=9q8q2q3q4qd2q2q8q2q3q").pack

@@ -1,10 +1,16 @@
 """Refusals of the sequence-layer entries at extreme sizes and arguments, without a GPU (placeholder addresses; nothing is
 dereferenced)."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 
 import newton_evaluation_nonlinear_amd as pn
 from test_sequence_host import GIB, TOK, _attention_block, _no_error_left, _rotary_block, _step_block  # noqa: F401
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("sizes, backward", [(dict(B=1 << 24, H=1, HK=1, T=1, dk=1, dv=1), True),
@@ -39,3 +45,13 @@ def test_norm_gradients_refuse_a_workspace_over_other_arrays(at):
 def test_positions_are_checked_without_a_rotation_too(kw):
     for name in ("pn_rotary", "pn_qk_norm_rotary", "pn_qk_norm_rotary_backward"):
         assert getattr(pn.lib(), name)(_rotary_block(R=0, **kw)) == pn.EINVAL, name
+
+
+def test_import_needs_no_cuda_build_of_torch():
+    """The package loads, and its helpers of plain numbers work, on a torch that lacks the device bindings."""
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda_')]: delattr(torch._C, n)\n"
+            "import newton_evaluation_nonlinear_amd as pn\n"
+            "assert pn.rotary_frequencies(4)[0] == 1.0 and pn.param_count(pn.CELL_DIAG_TANH, 5, 1) == 5\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
