@@ -77,8 +77,8 @@ def _workspace(like, name, key, *args):
     n = _sizes.get(key)
     if n is None:
         n = (_entries.get(name) or _entry(name))(*args)
-        if n == 0:
-            _fail(-1)
+        if n == 0:                                       # refused, as the call itself will be, which tells why
+            return None, 0, 0
         if len(_sizes) >= 4096:
             _sizes.clear()
         _sizes[key] = n
@@ -322,6 +322,10 @@ def _attention_inputs(q, k, v, log_decay, dims):
     return shape, HK, DV, dt, code, dev, tok, _array(log_decay, "log_decay", torch.float32, (shape[-2],), dev)
 
 
+def _scale(scale, channels):
+    return float(scale) if scale is not None else channels ** -0.5 if channels else 1.0        # no channels: the library refuses them
+
+
 def linear_attention(q, k, v, log_decay, initial_state=None, scale=None, lengths=None):
     """o_t = scale * q_t S_t with S_t = exp(log_decay) S_{t-1} + k_t^T v_t, for all T tokens.
 
@@ -333,7 +337,7 @@ def linear_attention(q, k, v, log_decay, initial_state=None, scale=None, lengths
     n = _array(lengths, "lengths", torch.int32, (B,), dev)
     o = q.new_empty(B, T, H, DV)
     final = log_decay.new_empty(B, H, DK, DV)
-    a = DK ** -0.5 if scale is None else float(scale)
+    a = _scale(scale, DK)
 
     def block(ws, nbytes):
         return _ATTENTION(code, B, T, H, HK, DK, DV, a, g, n, *tok, s0, o.data_ptr(), final.data_ptr(), *_NO_TOKENS, 0, 0, 0,
@@ -354,7 +358,7 @@ def linear_attention_backward(do, q, k, v, log_decay, initial_state=None, d_fina
     df = _array(d_final_state, "d_final_state", torch.float32, (B, H, DK, DV), dev)
     dq, dk, dv = q.new_empty(B, T, H, DK), q.new_empty(B, T, HK, DK), q.new_empty(B, T, HK, DV)
     d0 = torch.empty_like(initial_state) if s0 else None
-    a = DK ** -0.5 if scale is None else float(scale)
+    a = _scale(scale, DK)
 
     def block(ws, nbytes):
         return _ATTENTION(code, B, T, H, HK, DK, DV, a, g, n, *tok, s0, 0, 0, *td, df, dq.data_ptr(), dk.data_ptr(),
@@ -376,6 +380,6 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     sp = _array(state, "state", torch.float32, (pool, H, DK, DV), dev)
     o = q.new_empty(B, H, DV)
     _run(dev, "pn_linear_attention_step", _STEP(
-        code, B, H, HK, DK, DV, DK ** -0.5 if scale is None else float(scale), g, *tok, sp, n, pool, o.data_ptr(),
+        code, B, H, HK, DK, DV, _scale(scale, DK), g, *tok, sp, n, pool, o.data_ptr(),
         _raw_stream(dev)))
     return o

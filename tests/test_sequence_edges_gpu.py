@@ -196,3 +196,16 @@ def test_norm_gradients_of_many_heads():
     dx, dw, bdx, bdw = ref.norm_rotate_backward(_np(dy), _np(q), _np(w), t[..., 0], t[..., 1], eps)
     _close(dq, dx, EPS * np.abs(dx) + (3 * D + 32) * EPS * bdx, "dq")
     _close(dqw, dw, (2 + D + 16) * EPS * bdw, "dw")
+
+
+# ---------------------------------------------------------------- refusals
+
+
+def test_heads_without_channels_are_refused():
+    """As the library refuses them, with its error, not with one of the default scale."""
+    x, v, g = torch.zeros(1, 2, 1, 0, device=DEV), torch.zeros(1, 2, 1, 4, device=DEV), torch.zeros(1, device=DEV)
+    for call in (lambda: pn.linear_attention(x, x, v, g), lambda: pn.linear_attention_backward(v, x, x, v, g),
+                 lambda: pn.linear_attention_step(x[:, 0], x[:, 0], v[:, 0], g, torch.zeros(1, 1, 0, 4, device=DEV))):
+        with pytest.raises(pn.PnError) as e:
+            call()
+        assert e.value.code == pn.EUNSUPPORTED
