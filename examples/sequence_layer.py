@@ -11,6 +11,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import newton_evaluation_nonlinear_amd as pn  # noqa: E402
@@ -25,6 +26,7 @@ class NormRotary(torch.autograd.Function):
         return pn.qk_norm_rotary(q, k, q_weight, k_weight, table, positions)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         q, k, q_weight, k_weight, table, positions = ctx.saved_tensors
         grads = pn.qk_norm_rotary_backward(dq.contiguous(), dk.contiguous(), q, k, q_weight, k_weight, table, positions)
@@ -41,6 +43,7 @@ class LinearAttention(torch.autograd.Function):
         return pn.linear_attention(q, k, v, log_decay, initial_state=initial_state)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, d_final):
         q, k, v, log_decay, initial_state = ctx.saved_tensors
         do = torch.zeros((*q.shape[:3], v.shape[-1]), dtype=q.dtype, device=q.device) if do is None else do.contiguous()

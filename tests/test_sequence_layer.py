@@ -57,3 +57,14 @@ def test_training_lowers_the_loss():
     model = ex.Recall(8)
     losses = ex.train(model, 60, 8, 4, B=32)
     assert sum(losses[-10:]) < 0.7 * sum(losses[:10])
+
+
+def test_second_derivatives_are_refused():
+    """The gradients are calls of their own, not differentiable ones: asked for theirs, they say so."""
+    layer = ex.SequenceLayer(8, H=1, HK=1, D=8, positions=8)
+    x = torch.randn(1, 4, 8, device="cuda", requires_grad=True)
+    s0 = torch.zeros(1, 1, 8, 8, device="cuda", requires_grad=True)
+    y, _ = layer(x, s0)
+    d, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        d.sum().backward()
