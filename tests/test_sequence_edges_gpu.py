@@ -10,7 +10,7 @@ import torch
 import newton_evaluation_nonlinear_amd as pn
 from newton_evaluation_nonlinear_amd import sequence as seq
 from oracle import sequence as ref
-from test_sequence_gpu import DEV, TYPES, _close, _inputs, _np, _rand
+from test_sequence_gpu import DEV, ROUND, TINY, TYPES, _close, _inputs, _np, _oracle, _rand
 
 pytestmark = pytest.mark.gpu
 
@@ -94,6 +94,45 @@ def test_long_memories_do_not_drift(dtype, B, H, T, segments):
     for got, x, what in ((S, s0, "state"), (back[3], dS, "d initial state")):
         want = _np(x) * fade
         _close(got, want, 6 * EPS * steps * want, what)
+
+
+# ---------------------------------------------------------------- several segments
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("heads", [(4, 2), (4, 4)])
+def test_segments_against_the_oracle(dtype, heads):
+    """Sequences that end before, at and after the ends of segments, a decay of its own for every head (none, fast, slow,
+    growing), states in and out, shared heads.
+
+    c: dk + dv products, at most 12 sums into a state for every 32 tokens, 64 for the decays and the joins."""
+    (H, HK), B, T, DK, DV, scale = heads, 6, 1100, 32, 48, 0.3
+    n = _segments(dtype, B, T, H, HK, DK, DV)
+    assert n > 2
+    seg = 32 * (-(-T // 32) // n + (-(-T // 32) % n > 0))
+    lengths = [0, seg, seg + 1, T, 5, 2 * seg - 1]
+    print(f"[segments] {dtype} H={H} HK={HK}: {n} of {seg} tokens, lengths {lengths}", flush=True)
+    a = _inputs(dtype, B, T, H, HK, DK, DV, True, seed=11)
+    a["log_decay"] = torch.tensor([float("-inf"), -5.0, -1e-4, 0.01], device=DEV)
+    m = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    kw = dict(initial_state=a["initial_state"], scale=scale, lengths=m)
+    o, S = pn.linear_attention(a["q"], a["k"], a["v"], a["log_decay"], **kw)
+    c32 = (DK + DV + 12 * T / 32 + 64) * EPS
+    c, u, tiny = c32 + (0.0 if dtype == "f32" else 4 * 2.0 ** -16), ROUND[dtype], TINY[dtype]
+    top = 65504.0 if dtype == "f16" else np.inf           # with the growing decay some outputs pass binary16's largest number
+
+    def close(got, want, bound, what):
+        _close(got.double().clamp(-top, top), np.clip(want, -top, top), bound, what)
+
+    (wo, wS), (Ao, AS) = _oracle(ref.linear_attention, a, ("q", "k", "v", "log_decay", "initial_state"), scale=scale, lengths=lengths)
+    close(o, wo, u * np.abs(wo) + c * Ao + tiny, "o")
+    _close(S, wS.astype(np.float32).astype(np.float64), c32 * AS, "final state")
+    got = pn.linear_attention_backward(a["do"], a["q"], a["k"], a["v"], a["log_decay"], d_final_state=a["d_final_state"], **kw)
+    want, mag = _oracle(ref.linear_attention_backward, a, ("do", "q", "k", "v", "log_decay", "initial_state", "d_final_state"),
+                        scale=scale, lengths=lengths)
+    for name, x, w, A in zip(("dq", "dk", "dv"), got, want, mag):
+        close(x, w, u * np.abs(w) + c * A + tiny, name)
+    _close(got[3], want[3].astype(np.float32).astype(np.float64), c32 * mag[3], "d initial state")
 
 
 # ---------------------------------------------------------------- non-finite values
