@@ -179,6 +179,24 @@ def test_step_keeps_infinities(dtype, DV):
     assert torch.equal(state, clean)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T", [1, 70, 1100])
+def test_prompts_keep_infinities(dtype, T):
+    """An infinite element of the initial state is infinite in the final one, reaches the outputs of its channel as NaN or
+    infinity, and nothing else."""
+    B, H, DK, DV = 2, 4, 16, 40
+    a = _inputs(dtype, B, T, H, H, DK, DV, True, seed=9)
+    a["log_decay"] = torch.tensor([0.0, -1e-5, -1e-3, 1e-3], device=DEV)
+    args = (a["q"], a["k"], a["v"], a["log_decay"])
+    o, S = pn.linear_attention(*args, initial_state=a["initial_state"])
+    a["initial_state"][:, :, 3, 2], a["initial_state"][:, :, 5, 34] = float("inf"), float("-inf")
+    y, R = pn.linear_attention(*args, initial_state=a["initial_state"])
+    S[:, :, 3, 2], S[:, :, 5, 34] = float("inf"), float("-inf")
+    assert torch.equal(R, S)
+    rest = [c for c in range(DV) if c not in (2, 34)]
+    assert torch.equal(y[..., rest], o[..., rest]) and not bool(torch.isfinite(y[..., [2, 34]]).any())
+
+
 # ---------------------------------------------------------------- launches past 2^32 threads
 
 
