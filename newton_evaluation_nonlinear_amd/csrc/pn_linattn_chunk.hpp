@@ -329,6 +329,10 @@ __device__ __forceinline__ char* uniform(char* p) {
     return reinterpret_cast<char*>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
+__device__ __forceinline__ float uniform(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, x)));
+}
+
 // Channels of an LDS row that DKP of are used: a power of two, for q_block()
 // and kv_block().
 constexpr int row_width(int DKP) { return DKP == 96 ? 128 : DKP; }
@@ -519,9 +523,16 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
         // S is faded once lam^since leaves [1/2, 2]; until then what comes in is
         // scaled up instead.  A factor lam^32 for every chunk, rounded, would
         // take a state kept for 1024 chunks 7e-5 from its value.
-        const float after = decay_power(gl, static_cast<float>(since + L));
+        const float after = uniform(decay_power(gl, static_cast<float>(since + L)));
         const bool keep = after >= 0.5f && after <= 2.0f;
-        const float up = keep ? __builtin_amdgcn_rcpf(after) : 1.0f;
+        const float up = keep ? uniform(__builtin_amdgcn_rcpf(after)) : 1.0f;
+        // (of three parts without a branch, 152 us for 156 of a ragged float32
+        // batch; of one and two with it, 618 for 636 of a bfloat16 training pass)
+        auto fade_s = [&] {
+            if (NP == 3 || !keep)
+#pragma unroll
+                for (int t = 0; t < KT; ++t) S[t] *= keep ? 1.0f : after;
+        };
         auto weigh_v = [&](int t) {
             float v8[8];
             sum_parts<NP>(vf[t], v8);
@@ -601,16 +612,13 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
             }
             out += out_step;
         } else {
+            fade_s();
             load_kx(0);
             weigh_v(0);
         }
         // fade S = lam^L fade S + K^T (w V)
         load_kx(1);
-        // (of three parts without a branch, 152 us for 156 of a ragged float32
-        // batch; of one and two with it, 618 for 636 of a bfloat16 training pass)
-        if (NP == 3 || !keep)
-#pragma unroll
-            for (int t = 0; t < KT; ++t) S[t] *= keep ? 1.0f : after;
+        if (OUT) fade_s();
         fade = keep ? after : 1.0f;
         since = keep ? since + L : 0;
 #pragma unroll
