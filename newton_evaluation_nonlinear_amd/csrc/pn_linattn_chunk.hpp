@@ -526,8 +526,12 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
         const float after = uniform(decay_power(gl, static_cast<float>(since + L)));
         const bool keep = after >= 0.5f && after <= 2.0f;
         const float up = keep ? uniform(__builtin_amdgcn_rcpf(after)) : 1.0f;
-        // (of three parts without a branch, 152 us for 156 of a ragged float32
-        // batch; of one and two with it, 618 for 636 of a bfloat16 training pass)
+        // Of three parts without a branch (152 us, 156 with, for a ragged float32
+        // batch), of one and two with it (618 us, 636 without, for a bfloat16
+        // training pass).  Early, before the fragments, where registers are short
+        // (256 rows or single channels: 12 to 290 bytes of scratch otherwise),
+        // else under their loads (67 us, 78 early, for the states of 128 rows).
+        constexpr bool EARLY = !OUT && (DKP == 256 || !VEC);
         auto fade_s = [&] {
             if (NP == 3 || !keep)
 #pragma unroll
@@ -612,13 +616,13 @@ __global__ __launch_bounds__(64 * NW, (la_occupancy<T, DKP, OUT>())) void la_chu
             }
             out += out_step;
         } else {
-            fade_s();
+            if (EARLY) fade_s();
             load_kx(0);
             weigh_v(0);
         }
         // fade S = lam^L fade S + K^T (w V)
         load_kx(1);
-        if (OUT) fade_s();
+        if (!EARLY) fade_s();
         fade = keep ? after : 1.0f;
         since = keep ? since + L : 0;
 #pragma unroll
