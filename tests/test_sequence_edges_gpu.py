@@ -135,6 +135,31 @@ def test_segments_against_the_oracle(dtype, heads):
     _close(got[3], want[3].astype(np.float32).astype(np.float64), c32 * mag[3], "d initial state")
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("DK, DV", [(256, 256), (200, 130), (130, 20), (20, 132), (96, 100), (40, 128), (33, 7)])
+def test_segments_of_every_width(dtype, DK, DV):
+    """The pass for the segments' states at each number of rows and columns it is built for, read 16 bytes and one channel
+    at a time; bounds as in test_segments_against_the_oracle."""
+    B, T, H, HK, scale, lengths = 2, 530, 2, 1, 0.3, [530, 333]
+    n = _segments(dtype, B, T, H, HK, DK, DV)
+    assert n > 1
+    print(f"[segments] {dtype} {DK} x {DV}: {n}", flush=True)
+    a = _inputs(dtype, B, T, H, HK, DK, DV, True, seed=12)
+    kw = dict(initial_state=a["initial_state"], scale=scale, lengths=torch.tensor(lengths, dtype=torch.int32, device=DEV))
+    o, S = pn.linear_attention(a["q"], a["k"], a["v"], a["log_decay"], **kw)
+    c32 = (DK + DV + 12 * T / 32 + 64) * EPS
+    c, u, tiny = c32 + (0.0 if dtype == "f32" else 4 * 2.0 ** -16), ROUND[dtype], TINY[dtype]
+    (wo, wS), (Ao, AS) = _oracle(ref.linear_attention, a, ("q", "k", "v", "log_decay", "initial_state"), scale=scale, lengths=lengths)
+    _close(o, wo, u * np.abs(wo) + c * Ao + tiny, "o")
+    _close(S, wS, c32 * AS, "final state")
+    got = pn.linear_attention_backward(a["do"], a["q"], a["k"], a["v"], a["log_decay"], d_final_state=a["d_final_state"], **kw)
+    want, mag = _oracle(ref.linear_attention_backward, a, ("do", "q", "k", "v", "log_decay", "initial_state", "d_final_state"),
+                        scale=scale, lengths=lengths)
+    for name, x, w, A in zip(("dq", "dk", "dv"), got, want, mag):
+        _close(x, w, u * np.abs(w) + c * A + tiny, name)
+    _close(got[3], want[3], c32 * mag[3], "d initial state")
+
+
 # ---------------------------------------------------------------- non-finite values
 
 
