@@ -306,15 +306,23 @@ size_t pn_affine_scan_workspace_bytes(int64_t B, int64_t T, int64_t D, int32_t d
  *   - token tensors are [B, T, heads, channels] in one storage type (PN_F32,
  *     PN_BF16, PN_F16), channels adjacent, the other strides free and given
  *     in elements (0 broadcasts an input); outputs are C-contiguous;
- *   - states are C-contiguous float32 [B, H, dk, dv]; all arithmetic, sums
- *     and states are at least float32, one rounding at the end;
+ *   - states are C-contiguous float32 [B, H, dk, dv]; sums, norms and states
+ *     are held in at least float32, with one rounding of the result at the
+ *     end.  The matrix products of linear attention take their float32
+ *     operands as sums of bfloat16 parts: three, 24 bits, for float32 storage
+ *     and for states that are results; two, to 2^-16 of each operand, where
+ *     only outputs in 16-bit storage come of them (their error against 64 bits
+ *     is that of their last rounding either way).  float32 elements and states
+ *     beyond 3.389e38, the largest bfloat16, count as infinite there;
  *   - calls ENQUEUE their kernels on `stream` (hipStream_t, NULL = the null
  *     stream) and return without waiting, so they can be captured into a
  *     graph; nothing is allocated: a workspace is given by the caller,
  *     256-byte aligned (PN_EWORKSPACE otherwise), and is free for reuse by
  *     later work of the same stream;
  *   - sizes, strides, pointers and overlaps are checked on the host before
- *     any launch (PN_EINVAL, PN_EUNSUPPORTED); a size of 0 is an empty
+ *     any launch (PN_EINVAL, PN_EUNSUPPORTED, the latter also for more
+ *     sequences and heads than a launch holds: by their sizes, from 2.8 million
+ *     in the attention's gradients, 2^24 in steps); a size of 0 is an empty
  *     problem (PN_OK; what has elements left is still written, as a state);
  *   - indices held in device memory (positions, lengths, slots) are bounded
  *     in the kernels as each entry states: no value of theirs reads or
@@ -350,7 +358,9 @@ typedef struct pn_rotary_args {
     int64_t n_pos;
     const void* positions;
     int64_t pos64, pos_sb, pos_st, offset;
-    double eps;                 /* norm entries: x / sqrt(mean x^2 + eps)        */
+    double eps;                 /* norm entries: x / sqrt(mean x^2 + eps), the
+                                   mean in float32: rows of elements past 1e18
+                                   come out as 0                                */
     const float *qw, *kw;       /* norm weights, float32 [D] or [heads, D]; NULL = 1 */
     int64_t qw_sh, kw_sh;       /* 0: one [D] for all heads, D: one per head      */
     pn_tokens dq, dk;           /* backward: gradients of q_out and k_out         */
@@ -388,7 +398,8 @@ size_t pn_qk_norm_rotary_workspace_bytes(const pn_rotary_args* a);
  * and final_state is the state after lengths[b] tokens.  A NaN or infinity
  * in a token reaches the outputs from that token on, as NaN or infinity, and
  * may reach those of the up to 31 tokens before it (in the gradients of k and
- * v, which run backwards, after it). */
+ * v, which run backwards, after it).  An infinite element of a state stays
+ * infinite (lam > 0), and the outputs of its channel are NaN or infinite. */
 typedef struct pn_linattn_args {
     int64_t dtype, B, T, H, HK, dk, dv;
     double scale;

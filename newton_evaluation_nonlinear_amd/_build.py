@@ -3,7 +3,8 @@
     python -m newton_evaluation_nonlinear_amd._build
 
 Each source is compiled to an object in parallel (the device code of every
-file is self-contained), then the objects are linked into libpn.so; the
+file is self-contained) and its assembly is checked (lost_lanes), then the
+objects are linked into libpn.so; the
 ceiling microbenchmarks (pn_ceiling.hip) become libpn_ceiling.so.
 """
 

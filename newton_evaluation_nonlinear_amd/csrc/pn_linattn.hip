@@ -75,7 +75,8 @@ int carried(const LaArgs& a) { return a.n_ops == 3 ? 2 : a.n_ops; }
 // kStart before them, and runs alone in kAlone of the time; the pass for the
 // segments' states takes kStates of it, with half as many workgroups more at a
 // time.  Measured on one training pass (8 x 4096 tokens, 16 heads of 128,
-// bfloat16): outputs 5.1 us a chunk and pair of workgroups, 3.6 alone; states 2.5.
+// bfloat16): outputs 5.1 us a chunk and pair of workgroups, 3.6 alone; states 2.5
+// (2.1 since the state is faded late).
 constexpr int64_t kFillWaves = 2048;     // two on each of the 4 SIMDs of 256 compute units
 constexpr double kStart = 2.0, kAlone = 0.7, kStates = 0.5;
 constexpr double kClear = 0.85;          // more segments, with their traffic, only for a clear gain

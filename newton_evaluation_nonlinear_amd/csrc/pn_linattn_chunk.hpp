@@ -22,16 +22,24 @@
 // product of two the sum of the parts' products of order below `LIM`; a
 // storage type has NP parts (bfloat16 1, binary16 2, float32 3, all exact).
 // Outputs in 16 bits take LIM 2 (2^-16 per operand, far below their rounding);
-// the state, and float32 outputs, LIM 3 (2^-24).
+// the state, and float32 outputs, LIM 3 (2^-24).  With LIM 3 for all, the error
+// against 64 bits was the same to four digits in every output (1.66e-3 bfloat16,
+// 2.07e-4 binary16, of the norm) and the time more: 417 -> 466 us for 65536
+// tokens, 620 -> 760 for a training pass (16 heads of 128, bfloat16), 1013 -> 1236
+// for one in binary16.
+//
+// Decay.  Between chunks the state is faded late: it is held as S / lam^n, n
+// tokens after it was last faded, and faded when lam^n leaves [1/2, 2].  So a slow
+// memory is not rounded once a chunk.
 //
 // Bound and measurements (8 x 4096 tokens, 16 heads of 128 x 128, bfloat16).
 // Per wave and chunk of 32 tokens: 52 matrix instructions (8 scores, 16 with S,
-// 4 with V, 24 for the state in three parts) of 32 cycles, and 440 vector ones of
-// 4, most of them the 64 values of S cut into parts and faded.  Two waves per
+// 4 with V, 24 for the state in three parts) of 32 cycles, and 434 vector ones of
+// 4, most of them the 64 values of S cut into parts.  Two waves per
 // SIMD keep the matrix units busy for 45 % and the vector units for 48 % of the
 // time; sustained, the card lowers its clock from 2.0 to about 1.5 GHz.  Outputs
-// of 4 segments: 162 us (537 MB, 3.3 TB/s; 140 us with every load from cache),
-// the states of 3 of them 80 us.  With chunks of 64 tokens and K and V transposed
+// of 4 segments: 166 us (537 MB, 3.2 TB/s; 140 us with every load from cache),
+// the states of 3 of them 64 to 67 us.  With chunks of 64 tokens and K and V transposed
 // through registers on their way into LDS the same outputs took 257 us, and 206
 // with the loads ahead of the stores.
 #pragma once

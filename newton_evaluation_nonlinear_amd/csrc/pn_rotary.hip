@@ -16,8 +16,9 @@
 //
 // Measured (a large copy moves 4.7 TB/s): norm and rotation of 8 x 4096 tokens,
 // 16 + 4 heads of 128, bfloat16, 77 us, 4.4 TB/s; rotation of 32768 tokens, 16
-// heads of 64, float32, 55 us, 4.9 TB/s; gradients of 4 x 4095 tokens, 16 + 16
-// heads of 128, bfloat16, 116 us, 4.6 TB/s, and 9 us for the weights' sums.
+// heads of 64, float32, 63 us, 4.3 TB/s (55 to 57 over the same 268 MB again and
+// again, partly from cache); gradients of 4 x 4095 tokens, 16 + 16 heads of 128,
+// bfloat16, 117 us, 4.6 TB/s, and 9 us for the weights' sums.
 
 #include "pn_seq.hpp"
 #include "pn_seq_device.hpp"
