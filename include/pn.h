@@ -448,6 +448,152 @@ typedef struct pn_linattn_step_args {
 
 int pn_linear_attention_step(const pn_linattn_step_args* a);
 
+/* ------------------------------------------------------------------------
+ * State-space operators: the diagonal recurrence whose decay depends on the
+ * token (a selective scan), the short causal convolution in front of it, and
+ * the norms that join a block to its residual stream.  The conventions above
+ * hold; tokens here are [B, T, D] (pn_tokens' sh is not used) unless stated.
+ * lengths (int32 [B], NULL = T each; values are clamped to [0, T]): tokens at
+ * and after lengths[b] are padding: never read, their rows of the outputs 0,
+ * and final states those after lengths[b] tokens.  Sums over tokens or
+ * channels run in a fixed order: the same bits on every run. */
+
+/* Causal convolution of each channel with W (1 .. 8) taps,
+ *     y_t = act(bias + sum_{k < W} weight[d][k] x_{t - W + 1 + k}),
+ * act(v) = v / (1 + e^-v), or v if activation is 0.  Tokens before the first
+ * come from initial_state [B, W - 1, D] (the storage type; the last row is
+ * the newest), or are 0.  final_state holds the last W - 1 tokens, of the
+ * initial state where the sequence is shorter. */
+typedef struct pn_conv_args {
+    int64_t dtype, B, T, D, W, activation;
+    const float *weight, *bias; /* [D, W]; [D] or NULL                          */
+    const int32_t* lengths;
+    pn_tokens x;
+    const void* initial_state;  /* [B, W - 1, D] or NULL                         */
+    void *y, *final_state;      /* forward: [B, T, D]; [B, W - 1, D] or NULL      */
+    pn_tokens dy;               /* backward: gradient of y                       */
+    const void* d_final_state;  /* backward: [B, W - 1, D] or NULL                */
+    void* dx;                   /* backward: [B, T, D]                           */
+    float *dweight, *dbias;     /* backward: [D, W]; [D] or NULL                  */
+    void* d_initial_state;      /* backward: [B, W - 1, D] or NULL                */
+    void* workspace;
+    int64_t workspace_bytes;
+    void* stream;
+} pn_conv_args;
+
+int pn_short_conv(const pn_conv_args* a);
+int pn_short_conv_backward(const pn_conv_args* a);
+/* Workspace bytes of pn_short_conv_backward (the forward needs none), a
+ * function of dtype and sizes alone; 256 means that none is needed, 0 invalid
+ * arguments, with the error set.  Pointers are not looked at. */
+size_t pn_short_conv_workspace_bytes(const pn_conv_args* a);
+
+/* One token for each of B sequences: x and y [B, D]; state is a pool
+ * [n_slots, W - 1, D] in the storage type, which drops its oldest token for
+ * this one.  Slots as in pn_linear_attention_step. */
+typedef struct pn_conv_step_args {
+    int64_t dtype, B, D, W, activation;
+    const float *weight, *bias;
+    pn_tokens x;
+    void* state;
+    const int32_t* slots;       /* [B] or NULL                                  */
+    int64_t n_slots;
+    void* y;                    /* [B, D]                                       */
+    void* stream;
+} pn_conv_step_args;
+
+int pn_short_conv_step(const pn_conv_step_args* a);
+
+/* Selective scan.  For each channel d with N (1 .. 128) states,
+ *     delta_t = softplus(dt_t + dt_bias[d])   (without softplus: the sum),
+ *     h_t = exp(delta_t A[d]) h_{t-1} + delta_t x_t b_t,
+ *     y_t = (c_t . h_t + skip[d] x_t) * gate_t / (1 + e^-gate_t),
+ * h_0 = initial_state or 0; a NULL dt_bias is 0, a NULL skip leaves its term
+ * out, a NULL gate.p the gate.  x, dt, gate [B, T, D]; b and c [B, T, G, N],
+ * D a multiple of G: channel d reads group d / (D / G).  A is finite, < 0 in
+ * use; growth is allowed as far as the states are finite in float32.  Steps
+ * and decays are float32: exp(delta A) to (2 |delta A| + 2) 2^-24 of itself,
+ * 0 below 2^-126.  A NaN or infinity in a token reaches that token's outputs
+ * and those after it (in the gradients also those before it), as NaN or
+ * infinity. */
+typedef struct pn_ssm_args {
+    int64_t dtype, B, T, D, N, G, softplus;
+    const float *A, *skip, *dt_bias;    /* [D, N]; [D] or NULL; [D] or NULL       */
+    const int32_t* lengths;
+    pn_tokens x, dt, gate, b, c;
+    const float* initial_state;         /* [B, D, N] or NULL (zeros)              */
+    void* y;                            /* forward: [B, T, D]                    */
+    float* final_state;                 /* forward: [B, D, N] or NULL             */
+    pn_tokens dy;                       /* backward: gradient of y               */
+    const float* d_final_state;         /* backward: of final_state, or NULL      */
+    void *dx, *ddt, *dgate, *db, *dc;   /* backward: shaped as the inputs (dgate
+                                           written where the gate is given)      */
+    float *dA, *dskip, *ddt_bias;       /* backward: shaped as the inputs (the last
+                                           two written where their input is given) */
+    float* d_initial_state;             /* backward: [B, D, N] or NULL            */
+    void* workspace;
+    int64_t workspace_bytes;
+    void* stream;
+} pn_ssm_args;
+
+int pn_ssm_scan(const pn_ssm_args* a);
+int pn_ssm_scan_backward(const pn_ssm_args* a);
+/* Workspace bytes of the two, a function of dtype and sizes alone; 256 means
+ * that none is needed, 0 invalid arguments, with the error set.  Pointers are
+ * not looked at. */
+size_t pn_ssm_scan_workspace_bytes(const pn_ssm_args* a, int32_t backward);
+
+/* One token for each of B sequences: x, dt, gate, y [B, D], b and c
+ * [B, G, N]; state is a pool float32 [n_slots, D, N], updated in place.  Slots
+ * as in pn_linear_attention_step. */
+typedef struct pn_ssm_step_args {
+    int64_t dtype, B, D, N, G, softplus;
+    const float *A, *skip, *dt_bias;
+    pn_tokens x, dt, gate, b, c;
+    float* state;
+    const int32_t* slots;       /* [B] or NULL                                  */
+    int64_t n_slots;
+    void* y;                    /* [B, D]                                       */
+    void* stream;
+} pn_ssm_step_args;
+
+int pn_ssm_step(const pn_ssm_step_args* a);
+
+/* The norms around a block.  For each token of D (1 .. 16384) channels,
+ *     u = x * gate / (1 + e^-gate)                 (x without a gate),
+ *     p = post_weight * u / sqrt(mean u^2 + eps)   (u without post_weight),
+ *     s = residual + scale * p                     (scale NULL: 1; residual.p NULL: 0),
+ *     y = weight * s / sqrt(mean s^2 + eps)        (not computed without weight):
+ * x is what a block gives, s the residual stream after it and y what the next
+ * block takes.  x, gate, y and their gradients have the storage type, the
+ * residual, s and theirs residual_dtype: the storage type or PN_F32.  Means
+ * are float32 sums of squares: rows of elements past 1e18 come out as 0.
+ * The backward reads s as it was stored. */
+typedef struct pn_block_norm_args {
+    int64_t dtype, residual_dtype, B, T, D;
+    double eps;
+    const float *weight, *post_weight, *scale;   /* float32 [D] or NULL            */
+    pn_tokens x, gate, residual;                 /* [B, T, D]; p NULL: none         */
+    void *y, *s;                /* forward: contiguous [B, T, D]; y where weight is given */
+    pn_tokens dy, ds;           /* backward: gradients of y (where weight is given) and of
+                                   s (p NULL: 0)                                 */
+    pn_tokens s_in;             /* backward: the forward's s                     */
+    void *dx, *dgate, *dresidual;   /* backward: [B, T, D]; dgate where the gate is given,
+                                   dresidual or NULL                             */
+    float *dweight, *dpost_weight, *dscale;      /* backward, where the input is given */
+    void* workspace;
+    int64_t workspace_bytes;
+    void* stream;
+} pn_block_norm_args;
+
+int pn_block_norm(const pn_block_norm_args* a);
+int pn_block_norm_backward(const pn_block_norm_args* a);
+/* Workspace bytes of pn_block_norm_backward (the forward needs none), a
+ * function of types and sizes alone, and of which of weight, post_weight and
+ * scale are given; 256 means that none is needed, 0 invalid arguments, with
+ * the error set. */
+size_t pn_block_norm_workspace_bytes(const pn_block_norm_args* a);
+
 /* Message of the last error on this thread ("" if none).  The pointer stays
  * valid until the next library call on the same thread. */
 const char* pn_last_error(void);

@@ -25,7 +25,8 @@ CEILING_SOURCES = ["pn_ceiling.hip"]
 
 SOURCES = ["pn_api.cpp", "pn_diag.hip", "pn_cell.hip", "pn_dense.hip", "pn_scan.hip", "pn_static.hip", "pn_small.hip",
            "pn_seq_api.cpp", "pn_rotary.hip", "pn_linattn.hip", "pn_linattn_bf16.hip",
-           "pn_linattn_f16.hip", "pn_linattn_f32.hip"]
+           "pn_linattn_f16.hip", "pn_linattn_f32.hip", "pn_ssm_api.cpp", "pn_conv.hip", "pn_block_norm.hip", "pn_ssm.hip",
+           "pn_ssm_bf16.hip", "pn_ssm_f16.hip", "pn_ssm_f32.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

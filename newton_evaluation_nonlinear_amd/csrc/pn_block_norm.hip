@@ -1,0 +1,340 @@
+// The norms around a block, with its gate and the scaled residual,
+//     u = x silu(gate),  p = pw u ru,  s = residual + scale p,  y = w s rs,
+// ru = (mean u^2 + eps)^{-1/2} and rs likewise of s; and the gradients, with
+// n = u ru, m = s rs and t the gradient of s as a whole,
+//     e = w dy,  t = ds + rs (e - m mean(e m)),  dresidual = t,  dw = sum dy m,
+//     q = pw scale t,  du = ru (q - n mean(q n)),  dpw = sum scale t n,
+//     dscale = sum t p,  dx = du silu(gate),  dgate = du x silu'(gate).
+//
+// Bound: bytes.  A row stays in the registers of the lanes that hold it, NU
+// units of V channels each, so everything is read once and written once; sums
+// over a row go through the lanes and, in workgroups of several waves, LDS.
+// V: 16 bytes of the storage type where sizes, strides and alignment allow,
+// two channels or one otherwise.
+
+#include <algorithm>
+
+#include "pn_seq_device.hpp"
+#include "pn_ssm.hpp"
+
+namespace pn {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e)); }
+
+// Sums of two values over the workgroup, in every lane.
+template <int THREADS>
+__device__ __forceinline__ void row_sums(float& x, float& y, float* lds) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        x += __shfl_xor(x, m);
+        y += __shfl_xor(y, m);
+    }
+    if (THREADS == 64) return;
+    constexpr int WAVES = THREADS / 64;
+    __syncthreads();                                     // the last sums have been read
+    if (threadIdx.x % 64 == 0) {
+        lds[threadIdx.x / 64] = x;
+        lds[WAVES + threadIdx.x / 64] = y;
+    }
+    __syncthreads();
+    x = y = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+        x += lds[i];
+        y += lds[WAVES + i];
+    }
+}
+
+// The channels of one lane: unit u is V channels from at(u).
+template <int V, int NU, int THREADS>
+struct Row {
+    int D;
+    __device__ __forceinline__ int at(int u) const { return (static_cast<int>(threadIdx.x) + u * THREADS) * V; }
+    __device__ __forceinline__ bool on(int u) const { return at(u) < D; }     // V divides D
+    template <typename T>
+    __device__ __forceinline__ void load(const T* row, float (*v)[V]) const {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            Pack<T, V> q{};
+            if (on(u)) q = *reinterpret_cast<const Pack<T, V>*>(row + at(u));
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[u][i] = to_f32(q.v[i]);
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T* row, const float (*v)[V]) const {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            Pack<T, V> q;
+#pragma unroll
+            for (int i = 0; i < V; ++i) q.v[i] = from_f32<T>(v[u][i]);
+            if (on(u)) *reinterpret_cast<Pack<T, V>*>(row + at(u)) = q;
+        }
+    }
+    // f(u, i) for all values of the lane.
+    template <typename F>
+    __device__ __forceinline__ static void each(F f) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int i = 0; i < V; ++i) f(u, i);
+    }
+};
+
+__device__ __forceinline__ const char* row_of(const pn_tokens& x, int64_t b, int64_t t, int elem) {
+    return static_cast<const char*>(x.p) + (b * x.sb + t * x.st) * elem;
+}
+template <typename T>
+__device__ __forceinline__ const T* row_of(const pn_tokens& x, int64_t b, int64_t t) {
+    return reinterpret_cast<const T*>(row_of(x, b, t, sizeof(T)));
+}
+
+template <typename T, typename R, int V, int NU, int THREADS>
+__global__ __launch_bounds__(THREADS) void block_norm(pn_block_norm_args a) {
+    __shared__ float lds[2 * (THREADS / 64)];
+    const int64_t row = block_id();
+    if (row >= a.B * a.T) return;
+    const int64_t b = row / a.T, t = row - b * a.T;
+    const Row<V, NU, THREADS> r{static_cast<int>(a.D)};
+    const float eps = static_cast<float>(a.eps), inv = 1.0f / static_cast<float>(a.D);
+    float x[NU][V], s[NU][V];
+    r.load(row_of<T>(a.x, b, t), x);
+    if (a.residual.p) {
+        r.load(row_of<R>(a.residual, b, t), s);
+    } else {
+        r.each([&](int u, int i) { s[u][i] = 0.0f; });
+    }
+    if (a.gate.p) {
+        float g[NU][V];
+        r.load(row_of<T>(a.gate, b, t), g);
+        r.each([&](int u, int i) { x[u][i] *= g[u][i] * logistic(g[u][i]); });
+    }
+    float unused = 0.0f;
+    if (a.post_weight) {
+        float w[NU][V], ss = 0.0f;
+        r.load(a.post_weight, w);
+        r.each([&](int u, int i) { ss = fmaf(x[u][i], x[u][i], ss); });
+        row_sums<THREADS>(ss, unused, lds);
+        const float ru = 1.0f / sqrtf(fmaf(ss, inv, eps));
+        r.each([&](int u, int i) { x[u][i] = x[u][i] * ru * w[u][i]; });
+    }
+    if (a.scale) {
+        float w[NU][V];
+        r.load(a.scale, w);
+        r.each([&](int u, int i) { s[u][i] = fmaf(w[u][i], x[u][i], s[u][i]); });
+    } else {
+        r.each([&](int u, int i) { s[u][i] += x[u][i]; });
+    }
+    r.store(static_cast<R*>(a.s) + row * a.D, s);
+    if (!a.weight) return;
+    float w[NU][V], ss = 0.0f;
+    r.load(a.weight, w);
+    r.each([&](int u, int i) { ss = fmaf(s[u][i], s[u][i], ss); });
+    row_sums<THREADS>(ss, unused, lds);
+    const float rs = 1.0f / sqrtf(fmaf(ss, inv, eps));
+    r.each([&](int u, int i) { s[u][i] = s[u][i] * rs * w[u][i]; });
+    r.store(static_cast<T*>(a.y) + row * a.D, s);
+}
+
+// A workgroup takes `rows` rows one after the other; each lane keeps the sums
+// of its channels' weight gradients, which go to part[workgroup][3][D].
+template <typename T, typename R, int V, int NU, int THREADS>
+__global__ __launch_bounds__(THREADS) void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float* part) {
+    __shared__ float lds[2 * (THREADS / 64)];
+    const int64_t wg = block_id();
+    if (wg >= n_wg) return;
+    const Row<V, NU, THREADS> r{static_cast<int>(a.D)};
+    const float eps = static_cast<float>(a.eps), inv = 1.0f / static_cast<float>(a.D);
+    float dw[NU][V], dpw[NU][V], dsc[NU][V];
+    r.each([&](int u, int i) { dw[u][i] = dpw[u][i] = dsc[u][i] = 0.0f; });
+    const int64_t end = min((wg + 1) * rows, a.B * a.T);
+    for (int64_t row = wg * rows; row < end; ++row) {
+        const int64_t b = row / a.T, tok = row - b * a.T;
+        const bool need = a.gate.p || a.post_weight || a.scale;
+        float t[NU][V], x[NU][V], g[NU][V];
+        if (need) r.load(row_of<T>(a.x, b, tok), x);
+        if (a.gate.p) r.load(row_of<T>(a.gate, b, tok), g);
+        if (a.ds.p) {
+            r.load(row_of<R>(a.ds, b, tok), t);
+        } else {
+            r.each([&](int u, int i) { t[u][i] = 0.0f; });
+        }
+        if (a.weight) {
+            float s[NU][V], e[NU][V], w[NU][V], ss = 0.0f, es = 0.0f;
+            r.load(row_of<R>(a.s_in, b, tok), s);
+            r.load(row_of<T>(a.dy, b, tok), e);
+            r.load(a.weight, w);
+            r.each([&](int u, int i) {
+                ss = fmaf(s[u][i], s[u][i], ss);
+                es = fmaf(e[u][i] * w[u][i], s[u][i], es);
+            });
+            row_sums<THREADS>(ss, es, lds);
+            const float rs = 1.0f / sqrtf(fmaf(ss, inv, eps)), mean = es * rs * inv;
+            r.each([&](int u, int i) {
+                const float m = s[u][i] * rs;
+                dw[u][i] = fmaf(e[u][i], m, dw[u][i]);
+                t[u][i] = fmaf(rs, fmaf(-m, mean, e[u][i] * w[u][i]), t[u][i]);
+            });
+        }
+        if (a.dresidual) r.store(static_cast<R*>(a.dresidual) + row * a.D, t);
+        float act[NU][V];
+        r.each([&](int u, int i) { act[u][i] = a.gate.p ? logistic(g[u][i]) : 1.0f; });
+        auto silu = [&](int u, int i) { return a.gate.p ? g[u][i] * act[u][i] : 1.0f; };
+        if (a.post_weight) {
+            float w[NU][V], sc[NU][V], uu = 0.0f, qu = 0.0f;
+            r.load(a.post_weight, w);
+            if (a.scale) {
+                r.load(a.scale, sc);
+            } else {
+                r.each([&](int u, int i) { sc[u][i] = 1.0f; });
+            }
+            r.each([&](int u, int i) {
+                const float v = x[u][i] * silu(u, i);
+                uu = fmaf(v, v, uu);
+                qu = fmaf(w[u][i] * sc[u][i] * t[u][i], v, qu);
+            });
+            row_sums<THREADS>(uu, qu, lds);
+            const float ru = 1.0f / sqrtf(fmaf(uu, inv, eps)), mean = qu * ru * inv;
+            r.each([&](int u, int i) {
+                const float n = x[u][i] * silu(u, i) * ru, tn = t[u][i] * n;
+                dpw[u][i] = fmaf(sc[u][i], tn, dpw[u][i]);
+                dsc[u][i] = fmaf(w[u][i], tn, dsc[u][i]);
+                t[u][i] = ru * fmaf(-n, mean, w[u][i] * sc[u][i] * t[u][i]);
+            });
+        } else if (a.scale) {
+            float sc[NU][V];
+            r.load(a.scale, sc);
+            r.each([&](int u, int i) {
+                dsc[u][i] = fmaf(t[u][i], x[u][i] * silu(u, i), dsc[u][i]);
+                t[u][i] *= sc[u][i];
+            });
+        }
+        if (a.gate.p) {
+            r.each([&](int u, int i) {                   // x: dgate, t: dx
+                const float du = t[u][i], s = act[u][i];
+                x[u][i] = du * x[u][i] * s * fmaf(g[u][i], 1.0f - s, 1.0f);
+                t[u][i] = du * g[u][i] * s;
+            });
+            r.store(static_cast<T*>(a.dgate) + row * a.D, x);
+        }
+        r.store(static_cast<T*>(a.dx) + row * a.D, t);
+    }
+    float* q = part + wg * 3 * a.D;
+    if (a.weight) r.store(q, dw);
+    if (a.post_weight) r.store(q + a.D, dpw);
+    if (a.scale) r.store(q + 2 * a.D, dsc);
+}
+
+// ---------------------------------------------------------------- choice of the form
+
+template <int V_, int NU_, int THREADS_>
+struct Form {
+    static constexpr int V = V_, NU = NU_, THREADS = THREADS_;
+};
+
+// The widest access that every row of the call allows.
+template <typename T, typename R>
+int widest(const pn_block_norm_args& a, bool backward) {
+    auto bits = [&](const pn_tokens& x, int64_t elem) {
+        return x.p ? reinterpret_cast<intptr_t>(x.p) | (a.B > 1 ? x.sb * elem : 0) | (a.T > 1 ? x.st * elem : 0) : 0;
+    };
+    auto ptr = [](const void* p) { return reinterpret_cast<intptr_t>(p); };
+    int64_t t = bits(a.x, sizeof(T)) | bits(a.gate, sizeof(T)), r = 0;
+    if (backward) {
+        t |= (a.weight ? bits(a.dy, sizeof(T)) : 0) | ptr(a.dx) | (a.gate.p ? ptr(a.dgate) : 0);
+        r |= bits(a.ds, sizeof(R)) | (a.weight ? bits(a.s_in, sizeof(R)) : 0) | ptr(a.dresidual);
+    } else {
+        t |= a.weight ? ptr(a.y) : 0;
+        r |= bits(a.residual, sizeof(R)) | ptr(a.s);
+    }
+    const int64_t f = ptr(a.weight) | ptr(a.post_weight) | ptr(a.scale);
+    for (int V : {static_cast<int>(16 / sizeof(T)), 2}) {
+        // (a pack of more than 16 bytes is aligned to its size here, and moved in pieces)
+        if (a.D % V == 0 && t % (V * static_cast<int64_t>(sizeof(T))) == 0 && r % (V * static_cast<int64_t>(sizeof(R))) == 0 &&
+            f % (V * 4) == 0)
+            return V;
+    }
+    return 1;
+}
+
+// f(form) for rows of D channels, V at a time: the fewest waves that hold a
+// row in up to `most` values a lane; four waves a row where `spread` (few
+// rows: latency).
+template <int V, int MOST, typename F>
+hipError_t with_threads(int64_t D, bool spread, F f) {
+    constexpr int NU = MOST / V, ALL = 16384 / (1024 * V);
+    if (!spread && D <= 64 * V) return f(Form<V, 1, 64>{});
+    if (!spread && D <= 64 * V * NU) return f(Form<V, NU, 64>{});
+    if (D <= 256 * V) return f(Form<V, 1, 256>{});
+    if (D <= 256 * V * NU) return f(Form<V, NU, 256>{});
+    if (D <= 1024 * V * (ALL / 2)) return f(Form<V, ALL / 2, 1024>{});
+    return f(Form<V, ALL, 1024>{});
+}
+
+template <typename T, typename R, typename F>
+hipError_t with_form(const pn_block_norm_args& a, int V, bool spread, F f) {
+    constexpr int W = 16 / sizeof(T);
+    if (V == W) return with_threads<W, 16>(a.D, spread, f);
+    if (V == 2) return with_threads<2, 16>(a.D, spread, f);
+    return with_threads<1, 8>(a.D, spread, f);
+}
+
+template <typename T, typename R>
+hipError_t forward_typed(const pn_block_norm_args& a, hipStream_t st) {
+    const int64_t rows = a.B * a.T;
+    return with_form<T, R>(a, widest<T, R>(a, false), rows < 1024, [&](auto form) {
+        using Fm = decltype(form);
+        block_norm<T, R, Fm::V, Fm::NU, Fm::THREADS><<<grid_of(rows, Fm::THREADS), Fm::THREADS, 0, st>>>(a);
+        return hipGetLastError();
+    });
+}
+
+// Rows of a workgroup of the gradients.
+void backward_split(const pn_block_norm_args& a, int64_t* rows, int64_t* n_wg) {
+    const int64_t n = a.B * a.T;
+    *rows = std::max<int64_t>(1, (n + 2047) / 2048);
+    *n_wg = (n + *rows - 1) / *rows;
+}
+
+template <typename T, typename R>
+hipError_t backward_typed(const pn_block_norm_args& a, hipStream_t st) {
+    int64_t rows, n_wg;
+    backward_split(a, &rows, &n_wg);
+    float* part = static_cast<float*>(a.workspace);
+    const hipError_t e = with_form<T, R>(a, widest<T, R>(a, true), a.B * a.T < 1024, [&](auto form) {
+        using Fm = decltype(form);
+        block_norm_backward<T, R, Fm::V, Fm::NU, Fm::THREADS><<<grid_of(n_wg, Fm::THREADS), Fm::THREADS, 0, st>>>(a, rows, n_wg, part);
+        return hipGetLastError();
+    });
+    float *dw = a.weight ? a.dweight : nullptr, *dpw = a.post_weight ? a.dpost_weight : nullptr, *dsc = a.scale ? a.dscale : nullptr;
+    if (e != hipSuccess || (!dw && !dpw && !dsc)) return e;
+    return launch_column_sum(ColumnSum{part, n_wg, 3 * a.D, 3, {0, a.D, 2 * a.D}, {dw, dpw, dsc}}, st);
+}
+
+}  // namespace
+
+hipError_t launch_block_norm(const pn_block_norm_args& a, hipStream_t st) {
+    if (a.dtype == PN_F32) return forward_typed<float, float>(a, st);
+    if (a.dtype == PN_BF16)
+        return a.residual_dtype == PN_F32 ? forward_typed<bf16, float>(a, st) : forward_typed<bf16, bf16>(a, st);
+    return a.residual_dtype == PN_F32 ? forward_typed<f16, float>(a, st) : forward_typed<f16, f16>(a, st);
+}
+
+size_t block_norm_workspace(const pn_block_norm_args& a) {
+    if (!a.weight && !a.post_weight && !a.scale) return 0;
+    int64_t rows, n_wg;
+    backward_split(a, &rows, &n_wg);
+    return sizeof(float) * static_cast<size_t>(n_wg) * 3 * static_cast<size_t>(a.D);
+}
+
+hipError_t launch_block_norm_backward(const pn_block_norm_args& a, hipStream_t st) {
+    if (a.dtype == PN_F32) return backward_typed<float, float>(a, st);
+    if (a.dtype == PN_BF16)
+        return a.residual_dtype == PN_F32 ? backward_typed<bf16, float>(a, st) : backward_typed<bf16, bf16>(a, st);
+    return a.residual_dtype == PN_F32 ? backward_typed<f16, float>(a, st) : backward_typed<f16, f16>(a, st);
+}
+
+}  // namespace pn

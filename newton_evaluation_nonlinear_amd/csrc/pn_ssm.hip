@@ -1,0 +1,231 @@
+// The selective scan's plan, launches and sums, and its single-token form.
+//
+// Single tokens: bound by the states' bytes, 8 N per channel.  A group of lanes
+// holds a channel, V adjacent states a lane.
+
+#include <algorithm>
+
+#include "pn_seq_device.hpp"
+#include "pn_ssm.hpp"
+
+namespace pn {
+namespace {
+
+// 16 rows of lanes per 64 columns, added in order in float64.
+__global__ __launch_bounds__(1024) void column_sum(ColumnSum a) {
+    __shared__ double red[16][65];
+    const int col = threadIdx.x % 64, lane = threadIdx.x / 64;
+    const int64_t c = static_cast<int64_t>(block_id()) * 64 + col;
+    double s = 0.0;
+    if (c < a.cols)
+        for (int64_t r0 = lane; r0 < a.rows; r0 += 16 * 16) {
+            float x[16];                                 // 16 loads in flight, added in order
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = a.in[min(r0 + 16 * i, a.rows - 1) * a.cols + c];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s += r0 + 16 * i < a.rows ? x[i] : 0.0f;
+        }
+    red[lane][col] = s;
+    __syncthreads();
+    if (lane != 0 || c >= a.cols) return;
+    double v = 0.0;
+    for (int i = 0; i < 16; ++i) v += red[i][col];
+    int part = 0;
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        if (i < a.n_parts && c >= a.from[i]) part = i;
+    float* out = a.out[part];
+    if (out) out[c - a.from[part]] = static_cast<float>(v);
+}
+
+// db and dc: the sums of the channel blocks' shares [block][b, t][2][NP].
+template <typename T>
+__global__ __launch_bounds__(256) void bc_sum(pn_ssm_args a, SsmPlan p, const float* part) {
+    const int64_t N = a.N, GN = a.G * N, rows = a.B * a.T, NP = static_cast<int64_t>(p.blocks) * p.states;
+    const int64_t i = static_cast<int64_t>(block_id()) * 256 + threadIdx.x;
+    if (i >= rows * 2 * GN) return;
+    const int64_t row = i / (2 * GN), o = i - row * 2 * GN, which = o / GN, gn = o - which * GN, g = gn / N;
+    const int64_t b = row / a.T;
+    float v = 0.0f;
+    if (!a.lengths || row - b * a.T < a.lengths[b]) {
+        const float* q = part + ((g * p.per_group * rows + row) * 2 + which) * NP + (gn - g * N);
+        for (int k = 0; k < p.per_group; ++k) v += q[k * rows * 2 * NP];
+    }
+    static_cast<T*>(which ? a.dc : a.db)[row * GN + gn] = from_f32<T>(v);
+}
+
+// L lanes per channel, NU units of V states each.
+template <typename T, int V, int NU>
+__global__ __launch_bounds__(256) void ssm_step(pn_ssm_step_args a, int L) {
+    const int64_t g = static_cast<int64_t>(block_id()) * (256 / L) + threadIdx.x / L;
+    const int lane = threadIdx.x & (L - 1);
+    if (g >= a.B * a.D) return;
+    const int64_t b = g / a.D;
+    const int d = static_cast<int>(g - b * a.D), N = static_cast<int>(a.N);
+    const int64_t slot = a.slots ? a.slots[b] : b;
+    T* y = static_cast<T*>(a.y) + g;
+    if (slot < 0 || slot >= a.n_slots) {
+        if (lane == 0) *y = from_f32<T>(0.0f);
+        return;
+    }
+    float* hp = a.state + (slot * a.D + d) * N;
+    const float* Ap = a.A + static_cast<int64_t>(d) * N;
+    Pack<float, V> h[NU], A[NU];
+    Pack<T, V> bv[NU], cv[NU];
+    const int group = d / static_cast<int>(a.D / a.G);
+    const T* bp = static_cast<const T*>(a.b.p) + b * a.b.sb + group * a.b.sh;
+    const T* cp = static_cast<const T*>(a.c.p) + b * a.c.sb + group * a.c.sh;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+        const int n = (lane + u * L) * V;                // V divides N
+        h[u] = A[u] = Pack<float, V>{};
+        bv[u] = cv[u] = Pack<T, V>{};
+        if (n < N) {
+            h[u] = *reinterpret_cast<const Pack<float, V>*>(hp + n);
+            A[u] = *reinterpret_cast<const Pack<float, V>*>(Ap + n);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                bv[u].v[i] = bp[n + i];
+                cv[u].v[i] = cp[n + i];
+            }
+        }
+    }
+    const float x = to_f32(static_cast<const T*>(a.x.p)[b * a.x.sb + d]);
+    const float raw = to_f32(static_cast<const T*>(a.dt.p)[b * a.dt.sb + d]) + (a.dt_bias ? a.dt_bias[d] : 0.0f);
+    float delta = raw;
+    if (a.softplus) delta = fmaxf(raw, 0.0f) + log1pf(expf(-fabsf(raw)));
+    const float ux = delta * x;
+    float acc = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+        const int n = (lane + u * L) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            h[u].v[i] = fmaf(expf(delta * A[u].v[i]), h[u].v[i], ux * to_f32(bv[u].v[i]));
+            acc = fmaf(to_f32(cv[u].v[i]), h[u].v[i], acc);
+        }
+        if (n < N) *reinterpret_cast<Pack<float, V>*>(hp + n) = h[u];
+    }
+    for (int m = 1; m < L; m <<= 1) acc += __shfl_xor(acc, m);
+    if (lane != 0) return;
+    if (a.skip) acc = fmaf(a.skip[d], x, acc);
+    if (a.gate.p) {
+        const float z = to_f32(static_cast<const T*>(a.gate.p)[b * a.gate.sb + d]);
+        acc *= z / (1.0f + expf(-z));
+    }
+    *y = from_f32<T>(acc);
+}
+
+template <typename T>
+hipError_t step_typed(const pn_ssm_step_args& a, hipStream_t st) {
+    const bool wide = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) | reinterpret_cast<uintptr_t>(a.A)) % 16 == 0;
+    const int units = static_cast<int>(wide ? a.N / 4 : a.N);
+    int L = 1;
+    while (L < units && L < 64) L *= 2;
+    const int64_t per = 256 / L;
+    const dim3 grid = grid_of((a.B * a.D + per - 1) / per, 256);
+    if (wide) ssm_step<T, 4, 1><<<grid, 256, 0, st>>>(a, L);
+    else if (units <= 64) ssm_step<T, 1, 1><<<grid, 256, 0, st>>>(a, L);
+    else ssm_step<T, 1, 2><<<grid, 256, 0, st>>>(a, L);
+    return hipGetLastError();
+}
+
+hipError_t pass(const pn_ssm_args& a, const SsmPlan& p, SsmPass which, hipStream_t st) {
+    switch (a.dtype) {
+        case PN_F32: return launch_ssm_pass<float>(a, p, which, st);
+        case PN_BF16: return launch_ssm_pass<bf16>(a, p, which, st);
+        default: return launch_ssm_pass<f16>(a, p, which, st);
+    }
+}
+
+}  // namespace
+
+// Segments: as many waves as fill the device, no segment below 32 tokens.
+// Two sweeps of a segment then take the place of one of the sequence, so that
+// two segments gain nothing.
+SsmPlan plan_ssm(const pn_ssm_args& a, bool backward) {
+    SsmPlan p{};
+    p.states = a.N <= 4 ? 4 : a.N <= 8 ? 8 : 16;
+    p.blocks = static_cast<int32_t>((a.N + 15) / 16);
+    p.per_group = static_cast<int32_t>((a.D / a.G + 63) / 64);
+    p.chans = static_cast<int32_t>(a.G) * p.per_group;
+    const int64_t rows = a.B * p.chans, waves = rows * p.blocks;
+    p.tiles = (a.T + kSsmTile - 1) / kSsmTile;
+    int64_t n = std::min<int64_t>((2048 + waves - 1) / waves, a.T / 32);
+    if (n < 3) n = 1;
+    const int64_t per = std::max<int64_t>(1, (p.tiles + n - 1) / n);
+    p.seg = per * kSsmTile;
+    p.n_seg = static_cast<int32_t>(std::max<int64_t>(1, (p.tiles + per - 1) / per));
+    const int64_t state = rows * p.blocks * p.states * 64;
+    int64_t at = 0;
+    auto take = [&](int64_t floats) {
+        const int64_t from = at;
+        at += (floats + 63) / 64 * 64;
+        return from;
+    };
+    if (p.n_seg > 1) {
+        p.ends = take(p.n_seg * state);
+        p.decay = take(p.n_seg * rows * 64);
+        if (backward) p.rends = take(p.n_seg * state);
+    }
+    if (backward) {
+        p.marks = take(p.tiles * state);
+        p.since = take(p.tiles * rows * 64);
+        p.part_bc = take(p.chans * a.B * a.T * 2 * p.blocks * p.states);
+        p.part_A = take(a.B * p.n_seg * a.D * a.N);
+        p.part_vec = take(a.B * p.n_seg * p.blocks * 2 * a.D);
+    }
+    p.total = at;
+    return p;
+}
+
+bool ssm_fits(const pn_ssm_args& a, const SsmPlan& p) {
+    const int64_t limit = (int64_t(1) << 31) - 1, rows = a.B * p.chans * p.n_seg;
+    return rows <= limit && a.B * a.T <= limit * 64 / (a.G * a.N);
+}
+
+hipError_t launch_column_sum(const ColumnSum& s, hipStream_t st) {
+    if (s.cols <= 0) return hipSuccess;
+    column_sum<<<grid_of((s.cols + 63) / 64, 1024), 1024, 0, st>>>(s);
+    return hipGetLastError();
+}
+
+hipError_t launch_ssm(const pn_ssm_args& a, const SsmPlan& p, hipStream_t st) {
+    if (p.n_seg > 1) {
+        const hipError_t e = pass(a, p, kSsmEnds, st);
+        if (e != hipSuccess) return e;
+    }
+    return pass(a, p, kSsmOutputs, st);
+}
+
+hipError_t launch_ssm_backward(const pn_ssm_args& a, const SsmPlan& p, hipStream_t st) {
+    hipError_t e = a.T > 0 ? pass(a, p, p.n_seg > 1 ? kSsmMarksBoth : kSsmMarks, st) : hipSuccess;
+    if (e == hipSuccess) e = pass(a, p, kSsmGradients, st);
+    if (e != hipSuccess) return e;
+    float* ws = static_cast<float*>(a.workspace);
+    if (a.T > 0) {
+        const dim3 grid = grid_of((a.B * a.T * 2 * a.G * a.N + 255) / 256, 256);
+        switch (a.dtype) {
+            case PN_F32: bc_sum<float><<<grid, 256, 0, st>>>(a, p, ws + p.part_bc); break;
+            case PN_BF16: bc_sum<bf16><<<grid, 256, 0, st>>>(a, p, ws + p.part_bc); break;
+            default: bc_sum<f16><<<grid, 256, 0, st>>>(a, p, ws + p.part_bc); break;
+        }
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    e = launch_column_sum(ColumnSum{ws + p.part_A, a.B * p.n_seg, a.D * a.N, 1, {0}, {a.dA}}, st);
+    if (e != hipSuccess) return e;
+    float *dskip = a.skip ? a.dskip : nullptr, *dbias = a.dt_bias ? a.ddt_bias : nullptr;
+    if (!dskip && !dbias) return hipSuccess;
+    return launch_column_sum(ColumnSum{ws + p.part_vec, a.B * p.n_seg * p.blocks, 2 * a.D, 2, {0, a.D}, {dskip, dbias}}, st);
+}
+
+hipError_t launch_ssm_step(const pn_ssm_step_args& a, hipStream_t st) {
+    switch (a.dtype) {
+        case PN_F32: return step_typed<float>(a, st);
+        case PN_BF16: return step_typed<bf16>(a, st);
+        default: return step_typed<f16>(a, st);
+    }
+}
+
+}  // namespace pn
