@@ -38,7 +38,7 @@ __global__ __launch_bounds__(1024) void column_sum(ColumnSum a) {
     if (out) out[c - a.from[part]] = static_cast<float>(v);
 }
 
-// db and dc: the sums of the channel blocks' shares [block][b, t][2][NP].
+// db and dc: the sums of the workgroups' shares [workgroup][b, t][2][NP].
 template <typename T>
 __global__ __launch_bounds__(256) void bc_sum(pn_ssm_args a, SsmPlan p, const float* part) {
     const int64_t N = a.N, GN = a.G * N, rows = a.B * a.T, NP = static_cast<int64_t>(p.blocks) * p.states;
@@ -48,8 +48,9 @@ __global__ __launch_bounds__(256) void bc_sum(pn_ssm_args a, SsmPlan p, const fl
     const int64_t b = row / a.T;
     float v = 0.0f;
     if (!a.lengths || row - b * a.T < a.lengths[b]) {
-        const float* q = part + ((g * p.per_group * rows + row) * 2 + which) * NP + (gn - g * N);
-        for (int k = 0; k < p.per_group; ++k) v += q[k * rows * 2 * NP];
+        const int per = p.per_group / p.wide;
+        const float* q = part + ((g * per * rows + row) * 2 + which) * NP + (gn - g * N);
+        for (int k = 0; k < per; ++k) v += q[k * rows * 2 * NP];
     }
     static_cast<T*>(which ? a.dc : a.db)[row * GN + gn] = from_f32<T>(v);
 }
@@ -147,16 +148,18 @@ SsmPlan plan_ssm(const pn_ssm_args& a, bool backward) {
     SsmPlan p{};
     p.states = a.N <= 4 ? 4 : a.N <= 8 ? 8 : 16;
     p.blocks = static_cast<int32_t>((a.N + 15) / 16);
-    p.per_group = static_cast<int32_t>((a.D / a.G + 63) / 64);
+    const int64_t per_group = (a.D / a.G + 31) / 32;
+    p.wide = p.blocks > 1 || per_group == 1 ? 1 : per_group == 2 ? 2 : 4;
+    p.per_group = static_cast<int32_t>((per_group + p.wide - 1) / p.wide * p.wide);
     p.chans = static_cast<int32_t>(a.G) * p.per_group;
     const int64_t rows = a.B * p.chans, waves = rows * p.blocks;
     p.tiles = (a.T + kSsmTile - 1) / kSsmTile;
-    int64_t n = std::min<int64_t>((2048 + waves - 1) / waves, a.T / 32);
+    int64_t n = std::min<int64_t>((6144 + waves - 1) / waves, a.T / 32);
     if (n < 3) n = 1;
     const int64_t per = std::max<int64_t>(1, (p.tiles + n - 1) / n);
     p.seg = per * kSsmTile;
     p.n_seg = static_cast<int32_t>(std::max<int64_t>(1, (p.tiles + per - 1) / per));
-    const int64_t state = rows * p.blocks * p.states * 64;
+    const int64_t state = rows * p.blocks * p.states * 32;
     int64_t at = 0;
     auto take = [&](int64_t floats) {
         const int64_t from = at;
@@ -165,13 +168,13 @@ SsmPlan plan_ssm(const pn_ssm_args& a, bool backward) {
     };
     if (p.n_seg > 1) {
         p.ends = take(p.n_seg * state);
-        p.decay = take(p.n_seg * rows * 64);
+        p.decay = take(p.n_seg * rows * 32);
         if (backward) p.rends = take(p.n_seg * state);
     }
     if (backward) {
         p.marks = take(p.tiles * state);
-        p.since = take(p.tiles * rows * 64);
-        p.part_bc = take(p.chans * a.B * a.T * 2 * p.blocks * p.states);
+        p.since = take(p.tiles * rows * 32);
+        p.part_bc = take(p.chans / p.wide * a.B * a.T * 2 * p.blocks * p.states);
         p.part_A = take(a.B * p.n_seg * a.D * a.N);
         p.part_vec = take(a.B * p.n_seg * p.blocks * 2 * a.D);
     }

@@ -36,7 +36,8 @@ constexpr int kSsmTile = 8;      // tokens that a wave holds at a time
 struct SsmPlan {
     int32_t states;              // padded states of a wave: 4, 8 or 16
     int32_t blocks;              // waves that share the states of a channel
-    int32_t per_group;           // blocks of 64 channels in a group of b and c
+    int32_t wide;                // channel blocks of a workgroup of the gradients
+    int32_t per_group;           // blocks of 32 channels in a group of b and c (whole workgroups)
     int32_t chans;               // channel blocks in all
     int32_t n_seg;               // segments of the time axis
     int64_t seg, tiles;          // tokens per segment, tiles of a sequence

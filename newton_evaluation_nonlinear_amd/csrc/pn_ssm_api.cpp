@@ -102,6 +102,7 @@ int check_conv(const pn_conv_args* p, bool backward) {
 
 int check_ssm_sizes(int64_t dtype, int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, int64_t softplus) {
     PN_TRY(check_types(dtype, B, T, D));
+    if (D > int64_t(1) << 26) return fail(PN_EUNSUPPORTED, "size too large");
     if (N < 1 || N > 128) return fail(PN_EUNSUPPORTED, "1 .. 128 states per channel are supported");
     if (G < 1 || (D > 0 && (G > D || D % G))) return fail(PN_EINVAL, "D must be a multiple of G >= 1");
     if (softplus < 0 || softplus > 1) return fail(PN_EINVAL, "softplus must be 0 or 1");
@@ -110,6 +111,9 @@ int check_ssm_sizes(int64_t dtype, int64_t B, int64_t T, int64_t D, int64_t N, i
         return fail(PN_EUNSUPPORTED, "size too large");
     return PN_OK;
 }
+
+// Offsets within a tile of the scan are 32 bits wide.
+constexpr int64_t kMaxScanStride = int64_t(1) << 26;
 
 int check_ssm(const pn_ssm_args* p, bool backward) {
     clear_error();
@@ -134,6 +138,10 @@ int check_ssm(const pn_ssm_args* p, bool backward) {
         if (backward ? !a.dx || !a.ddt || !a.db || !a.dc || (a.gate.p && !a.dgate) : !a.y)
             return fail(PN_EINVAL, "an output is NULL");
     }
+    if (a.T > 1)
+        for (const pn_tokens* t : {&a.x, &a.dt, &a.gate, &a.b, &a.c, &a.dy})
+            if (t->p && (backward || t != &a.dy) && t->st > kMaxScanStride)
+                return fail(PN_EUNSUPPORTED, "token strides of up to 2^26 elements are supported");
     const Range none{0, 0};
     const Range x = range3(a.x, a.B, a.T, a.D, e), dt = range3(a.dt, a.B, a.T, a.D, e), z = range3(a.gate, a.B, a.T, a.D, e);
     const Range b = range(a.b, a.B, a.T, a.G, a.N, e), c = range(a.c, a.B, a.T, a.G, a.N, e);
@@ -154,6 +162,13 @@ int check_ssm(const pn_ssm_args* p, bool backward) {
                            range(a.skip ? a.dskip : nullptr, 4 * a.D), range(a.dt_bias ? a.ddt_bias : nullptr, 4 * a.D),
                            range(a.d_initial_state, state), ws},
                           {x, dt, z, b, c, A, skip, bias, n, s0, range3(a.dy, a.B, a.T, a.D, e), range(a.d_final_state, state)});
+}
+
+// The token stride of one token is any number, and is left out.
+pn_ssm_args one_token(pn_ssm_args a) {
+    if (a.T <= 1)
+        for (pn_tokens* t : {&a.x, &a.dt, &a.gate, &a.b, &a.c, &a.dy}) t->st = 0;
+    return a;
 }
 
 // ---------------------------------------------------------------- norms around a block
@@ -279,22 +294,24 @@ size_t pn_ssm_scan_workspace_bytes(const pn_ssm_args* a, int32_t backward) {
     return p.total > 0 ? padded(sizeof(float) * static_cast<size_t>(p.total)) : kAlign;
 }
 
-int pn_ssm_scan(const pn_ssm_args* a) {
-    PN_TRY(check_ssm(a, false));
-    if (a->B == 0 || a->D == 0) return PN_OK;
-    return launched(launch_ssm(*a, plan_ssm(*a, false), static_cast<hipStream_t>(a->stream)));
+int pn_ssm_scan(const pn_ssm_args* p) {
+    PN_TRY(check_ssm(p, false));
+    if (p->B == 0 || p->D == 0) return PN_OK;
+    const pn_ssm_args a = one_token(*p);
+    return launched(launch_ssm(a, plan_ssm(a, false), static_cast<hipStream_t>(a.stream)));
 }
 
-int pn_ssm_scan_backward(const pn_ssm_args* a) {
-    PN_TRY(check_ssm(a, true));
-    if (a->D == 0) return PN_OK;
-    hipStream_t st = static_cast<hipStream_t>(a->stream);
-    if (a->B == 0) {                                     // sums over nothing
-        PN_TRY(zeros(a->dA, a->D * a->N, st));
-        PN_TRY(zeros(a->skip ? a->dskip : nullptr, a->D, st));
-        return zeros(a->dt_bias ? a->ddt_bias : nullptr, a->D, st);
+int pn_ssm_scan_backward(const pn_ssm_args* p) {
+    PN_TRY(check_ssm(p, true));
+    if (p->D == 0) return PN_OK;
+    const pn_ssm_args a = one_token(*p);
+    hipStream_t st = static_cast<hipStream_t>(a.stream);
+    if (a.B == 0) {                                      // sums over nothing
+        PN_TRY(zeros(a.dA, a.D * a.N, st));
+        PN_TRY(zeros(a.skip ? a.dskip : nullptr, a.D, st));
+        return zeros(a.dt_bias ? a.ddt_bias : nullptr, a.D, st);
     }
-    return launched(launch_ssm_backward(*a, plan_ssm(*a, true), st));
+    return launched(launch_ssm_backward(a, plan_ssm(a, true), st));
 }
 
 int pn_ssm_step(const pn_ssm_step_args* p) {

@@ -6,16 +6,20 @@
 //     du = r . b,   ddelta = x du + sum_n r e A,   dA = sum r e delta,
 //     db = sum over channels of r u,   dc = sum over channels of g h.
 //
-// Layout.  A wave (a workgroup of its own up to 16 states) holds 64 channels.
-// In a quad of lanes each lane holds S of the 4 S states of the quad's four
-// channels, in registers over all tokens: b and c are read from LDS once for
-// four channels, and the sums over channels in db and dc are a fourth the
-// work of lanes that hold whole channels.  What belongs to a channel and not
-// to a state (step, gate, products with x) is computed by the one lane whose
-// number is the channel's, so tokens move 64 adjacent elements at a time; the
-// quad passes these values on by DPP, and sums of its four lanes go back to
-// the channel's own lane.  More than 16 states are blocks of 16 in as many
-// waves, which add their shares of such sums through LDS.
+// Layout.  A wave holds 32 channels.  In a quad of lanes each lane holds S of
+// the 4 S states of the quad's two channels, in registers over all tokens.
+// What belongs to a channel and not to a state (step, gate, products with x)
+// is computed once, by the lane of the channel (bit 0 of its number in the
+// quad) and of the token's parity (bit 1); the quad passes such values on by
+// DPP, and sums over its four lanes go back to the lane they belong to.  More
+// than 16 states are blocks of 16 in as many waves, which add their shares of
+// such sums through LDS.
+//
+// Bound: instructions.  A state and token take an exponential (9 cycles of a
+// SIMD, which does nothing else meanwhile) and 3 to 4 products and sums (2.5
+// each, from two waves on).  So waves are kept small: four channels a quad
+// need a fourth fewer instructions for the sums over channels, but twice the
+// registers, and then the SIMD waits.
 //
 // Time.  Where channels do not fill the device the tokens are cut into
 // segments: a first pass takes the state that a segment leaves alone
@@ -26,6 +30,8 @@
 // decay since the segment's start); the second walks the tiles backwards,
 // each once forward from its mark with e kept in registers, once back.
 #pragma once
+
+#include <type_traits>
 
 #include "pn_seq_device.hpp"
 #include "pn_ssm.hpp"
@@ -41,12 +47,6 @@ __device__ __forceinline__ float quad_lane(float v) {
     int r = __builtin_amdgcn_mov_dpp(__float_as_int(v), K * 0x55, 0xf, 0xf, true);
     asm("" : "+v"(r));           // kept apart: one move and plain products take less than DPP in every product
     return __int_as_float(r);
-}
-__device__ __forceinline__ void quad_lanes(float v, float* k) {
-    k[0] = quad_lane<0>(v);
-    k[1] = quad_lane<1>(v);
-    k[2] = quad_lane<2>(v);
-    k[3] = quad_lane<3>(v);
 }
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
@@ -78,71 +78,80 @@ __device__ __forceinline__ float softplus(float v, float* slope) {
 }
 __device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e)); }
 
-// Where a wave works.
-template <typename T, int S, bool MULTI>
+constexpr int kChans = 32;               // channels of a wave
+constexpr int kOwn = kSsmTile / 2;       // tokens of a tile that belong to a lane: 2 m + its parity
+
+// Where a wave works.  WIDE: the waves of a workgroup are adjacent channel
+// blocks, otherwise the blocks of states of one.
+template <typename T, int S, bool WIDE>
 struct SsmWave {
-    static constexpr int E = 4 * S;                      // states of a quad's channel, and values of a lane
-    static constexpr int M = kSsmTile * E / 64 > 0 ? kSsmTile * E / 64 : 1;
+    static constexpr int E = 4 * S;                      // states of a wave
+    static constexpr int M = (kSsmTile * E + 63) / 64;   // values of b that a lane loads for a tile
     const pn_ssm_args& a;
     const SsmPlan& p;
-    int lane, j, blk, seg, cb, ch, first, n0, behind;    // n0: the lane's first state; behind: the channel after the group
+    int lane, j, odd, blk, seg, cb, ch, first, n0, behind;    // n0: the lane's first state; behind: the channel after the group
     int64_t b, row, begin, stop, end;                    // row: (b, channel block); stop: of the segment, end: of its tokens
-    bool own;                                            // whether the lane's channel exists
-    const T *xp, *dp, *zp, *bp, *cp;
+    bool own, full;                                      // whether the lane's channel exists, and all of the wave's
+    const T *bp, *cp;
 
     __device__ __forceinline__ SsmWave(const pn_ssm_args& a_, const SsmPlan& p_) : a(a_), p(p_) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         lane = threadIdx.x & 63;
         j = lane & 3;
-        blk = MULTI ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
-        const uint32_t id = block_id(), B = static_cast<uint32_t>(a.B), chans = static_cast<uint32_t>(p.chans);
+        odd = j >> 1;
+        blk = WIDE ? 0 : wave;
+        const uint32_t id = block_id(), B = static_cast<uint32_t>(a.B);
+        const uint32_t chans = static_cast<uint32_t>(WIDE ? p.chans / p.wide : p.chans);
         cb = static_cast<int>(id % chans);
+        if (WIDE) cb = cb * p.wide + wave;
         b = id / chans % B;
         seg = static_cast<int>(id / chans / B);
-        row = b * chans + cb;
-        const int group = cb / p.per_group, DG = static_cast<int>(a.D / a.G), in = cb % p.per_group * 64;
+        row = b * p.chans + cb;
+        const int group = cb / p.per_group, DG = static_cast<int>(a.D / a.G), in = cb % p.per_group * kChans;
+        const int mine = in + (lane >> 2) * 2 + (j & 1);
         first = group * DG + in;
         behind = (group + 1) * DG;
-        own = in + lane < DG;
-        ch = group * DG + min(in + lane, DG - 1);
+        own = mine < DG;
+        full = in + kChans <= DG;
+        ch = group * DG + min(mine, DG - 1);
         n0 = blk * E + j * S;
         begin = seg * p.seg;
         stop = min(begin + p.seg, a.T);
         int64_t len = a.T;
         if (a.lengths) len = max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.lengths[b]), a.T));
         end = min(stop, len);
-        xp = static_cast<const T*>(a.x.p) + b * a.x.sb;
-        dp = static_cast<const T*>(a.dt.p) + b * a.dt.sb;
-        zp = a.gate.p ? static_cast<const T*>(a.gate.p) + b * a.gate.sb : nullptr;
         bp = static_cast<const T*>(a.b.p) + b * a.b.sb + group * a.b.sh;
         cp = static_cast<const T*>(a.c.p) + b * a.c.sb + group * a.c.sh;
     }
     // Channel k of the lane's quad, and whether it exists.
-    __device__ __forceinline__ int chan(int k) const { return first + (lane & ~3) + k; }
+    __device__ __forceinline__ int chan(int k) const { return first + (lane >> 2) * 2 + k; }
     __device__ __forceinline__ bool has(int k) const { return chan(k) < behind; }
+    // Token m of the lane's in the tile at t0.
+    __device__ __forceinline__ int64_t tok(int64_t t0, int m) const { return t0 + 2 * m + odd; }
 
     // f(k, s, index in [D, N]) for the states that exist.
     template <typename F>
     __device__ __forceinline__ void states(F f) const {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int s = 0; s < S; ++s)
                 if (has(k) && n0 + s < a.N) f(k, s, static_cast<int64_t>(chan(k)) * a.N + n0 + s);
     }
     __device__ __forceinline__ void decays(float (*A2)[S]) const {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int s = 0; s < S; ++s) A2[k][s] = 0.0f;
         states([&](int k, int s, int64_t i) { A2[k][s] = a.A[i] * kLog2e; });
     }
     // A state array of the workspace: [.., row, block, k, lane, s].
     __device__ __forceinline__ float* at(float* base, int64_t n) const {
-        return base + (((n * a.B * p.chans + row) * p.blocks + blk) * 256 + lane) * S;
+        return base + (((n * a.B * p.chans + row) * p.blocks + blk) * 128 + lane) * S;
     }
     __device__ __forceinline__ void put(float* q, const float (*h)[S]) const {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             Pack<float, S> v;
 #pragma unroll
             for (int s = 0; s < S; ++s) v.v[s] = h[k][s];
@@ -151,46 +160,50 @@ struct SsmWave {
     }
     __device__ __forceinline__ void get(const float* q, float (*h)[S]) const {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             const Pack<float, S> v = *reinterpret_cast<const Pack<float, S>*>(q + k * 64 * S);
 #pragma unroll
             for (int s = 0; s < S; ++s) h[k][s] = v.v[s];
         }
     }
-    // h = exp(sum of steps * A) h + more
+    // h = exp(sum of steps * A) h + more; steps: of the lane's channel, in its lanes of both parities
     __device__ __forceinline__ void fade(float (*h)[S], float steps, const float (*A2)[S], const float (*more)[S]) const {
-        float d[4];
-        quad_lanes(steps, d);
+        const float d[2] = {quad_lane<0>(steps), quad_lane<1>(steps)};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int s = 0; s < S; ++s) h[k][s] = fmaf(__builtin_amdgcn_exp2f(d[k] * A2[k][s]), h[k][s], more[k][s]);
     }
-    __device__ __forceinline__ int64_t own_at(int64_t n) const { return (n * a.B * p.chans + row) * 64 + lane; }
+    // A number of each channel of the workspace.
+    __device__ __forceinline__ int64_t own_at(int64_t n) const {
+        return (n * a.B * p.chans + row) * kChans + (lane >> 2) * 2 + (j & 1);
+    }
     // The state before segment seg > 0 from the ends of those before it.
     __device__ __forceinline__ void carried(float* ws, const float (*A2)[S], float (*h)[S]) const {
         get(at(ws + p.ends, 0), h);
         for (int i = 1; i < seg; ++i) {
-            float more[4][S];
+            float more[2][S];
             get(at(ws + p.ends, i), more);
             fade(h, ws[p.decay + own_at(i)], A2, more);
         }
     }
 
-    // The b and c of a tile, to LDS as [token][b | c][E].
-    __device__ __forceinline__ void load_bc(const T* src, int64_t st, int64_t t0, float* v) const {
+    // The b and c of a tile, to LDS as [token][b | c][E]; 0 for states and tokens that do not exist.
+    __device__ __forceinline__ void load_bc(const T* src, int64_t st, int64_t t0, T* v) const {
+        const int left = static_cast<int>(min(end - t0, static_cast<int64_t>(kSsmTile))), N = static_cast<int>(a.N);
+        const T* q = src + t0 * st;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            const int i = lane + 64 * m, tok = i / E, n = blk * E + i % E;
-            const bool on = i < kSsmTile * E && t0 + tok < end && n < a.N;
-            v[m] = on ? to_f32(src[(t0 + tok) * st + n]) : 0.0f;
+            const int i = lane + 64 * m, tok = min(i / E, left - 1), n = min(blk * E + i % E, N - 1);
+            const T x = element(q, (tok * static_cast<uint32_t>(st) + n) * sizeof(T));
+            v[m] = i / E < left && blk * E + i % E < N ? x : from_f32<T>(0.0f);
         }
     }
-    __device__ __forceinline__ void store_bc(float* lds, int which, const float* v) const {
+    __device__ __forceinline__ void store_bc(float* lds, int which, const T* v) const {
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             const int i = lane + 64 * m;
-            if (i < kSsmTile * E) lds[(i / E * 2 + which) * E + i % E] = v[m];
+            if (i < kSsmTile * E) lds[(i / E * 2 + which) * E + i % E] = to_f32(v[m]);
         }
     }
     __device__ __forceinline__ void read_bc(const float* lds, int i, int which, float* v) const {
@@ -198,44 +211,67 @@ struct SsmWave {
 #pragma unroll
         for (int s = 0; s < S; ++s) v[s] = q.v[s];
     }
-    // The lane's channel of a token row; rows at and after `end` are not read.
-    __device__ __forceinline__ void load_rows(const T* src, int64_t st, int64_t t0, T* v) const {
+    // The lane's tokens and channel of x; rows at and after `end` are not read.
+    // A wave's offsets within a tile are 32 bits (strides are checked).
+    __device__ __forceinline__ void load_rows(const pn_tokens& x, int64_t t0, T* v) const {
+        const T* src = static_cast<const T*>(x.p) + b * x.sb + t0 * x.st;
+        const uint32_t st = static_cast<uint32_t>(x.st);
+        if (t0 + kSsmTile <= end) {
+            const uint32_t at = (odd * st + ch) * sizeof(T);
 #pragma unroll
-        for (int i = 0; i < kSsmTile; ++i) {
-            const int64_t t = min(t0 + i, end - 1);
-            v[i] = (src + t * st)[ch];
+            for (int m = 0; m < kOwn; ++m) v[m] = element(src + 2 * m * x.st, at);
+        } else {
+            const int left = static_cast<int>(end - t0) - 1;
+#pragma unroll
+            for (int m = 0; m < kOwn; ++m) v[m] = element(src, (min(2 * m + odd, left) * st + ch) * sizeof(T));
         }
+    }
+    __device__ __forceinline__ static T element(const T* base, uint32_t bytes) {
+        return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + bytes);
+    }
+    // Writes the lane's token m and channel of an output [B, T, D].
+    __device__ __forceinline__ void put_row(void* out, int64_t t0, int m, float v) const {
+        T* base = static_cast<T*>(out) + (b * a.T + t0 + 2 * m) * a.D;
+        const uint32_t at = (odd * static_cast<uint32_t>(a.D) + ch) * sizeof(T);
+        *reinterpret_cast<T*>(reinterpret_cast<char*>(base) + at) = from_f32<T>(v);
     }
 };
 
-// Sums over the waves of a workgroup: wave w gets its tokens w, w + blocks, ..
-template <int S, bool MULTI>
-__device__ __forceinline__ float joined(const float* ex, int blocks, int i, int lane) {
+// The step's value and a token's other value at channel k of the quad, token 2 m + P of the tile.
+template <int P>
+__device__ __forceinline__ void pair(float v, float* k) {
+    k[0] = quad_lane<2 * P>(v);
+    k[1] = quad_lane<2 * P + 1>(v);
+}
+
+// The sum over the waves of a workgroup of their values for a lane's token m.
+__device__ __forceinline__ float joined(const float* ex, int blocks, int m, int lane) {
     float v = 0.0f;
-    for (int w = 0; w < blocks; ++w) v += ex[(w * kSsmTile + i) * 64 + lane];
+    for (int w = 0; w < blocks; ++w) v += ex[(w * kOwn + m) * 64 + lane];
     return v;
 }
 
 template <typename T, int S, bool MULTI, int PASS>
-__global__ __launch_bounds__(MULTI ? 512 : 64) void ssm_pass(pn_ssm_args a, SsmPlan p) {
+__global__ __launch_bounds__(MULTI ? 512 : 64) __attribute__((amdgpu_waves_per_eu(MULTI ? 2 : PASS == kSsmMarksBoth ? 3 : 4)))
+void ssm_pass(pn_ssm_args a, SsmPlan p) {
     constexpr int E = 4 * S, WAVES = MULTI ? 8 : 1;
     constexpr bool OUT = PASS == kSsmOutputs, MARKS = PASS == kSsmMarks || PASS == kSsmMarksBoth, BACK = PASS == kSsmMarksBoth;
     __shared__ __align__(16) float bc_lds[WAVES][kSsmTile * 2 * E];
-    __shared__ float ex[MULTI && OUT ? WAVES * kSsmTile * 64 : 1];
-    const SsmWave<T, S, MULTI> w(a, p);
+    __shared__ float ex[MULTI && OUT ? WAVES * kOwn * 64 : 1];
+    const SsmWave<T, S, false> w(a, p);
     if (w.seg >= (PASS == kSsmEnds ? p.n_seg - 1 : p.n_seg)) return;
     float* ws = static_cast<float*>(a.workspace);
     float* lds = bc_lds[MULTI ? w.blk : 0];
     const float bias = a.dt_bias ? a.dt_bias[w.ch] : 0.0f, skip = a.skip ? a.skip[w.ch] : 0.0f;
-    const T* gp = BACK ? static_cast<const T*>(a.dy.p) + w.b * a.dy.sb : nullptr;
+    const bool gated = a.gate.p != nullptr;
     T* yp = static_cast<T*>(a.y);
-    float A2[4][S], h[4][S], R[BACK ? 4 : 1][S], P[BACK ? 4 : 1][S];
+    float A2[2][S], h[2][S], R[BACK ? 2 : 1][S], P[BACK ? 2 : 1][S];
     w.decays(A2);
     if (OUT && w.seg > 0) {
         w.carried(ws, A2, h);
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int s = 0; s < S; ++s) h[k][s] = 0.0f;
         if (w.seg == 0 && a.initial_state)
@@ -243,39 +279,41 @@ __global__ __launch_bounds__(MULTI ? 512 : 64) void ssm_pass(pn_ssm_args a, SsmP
     }
     if (BACK) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 R[k][s] = 0.0f;
                 P[k][s] = 1.0f;
             }
     }
-    float since = 0.0f;                                  // sum of the lane's steps
-    constexpr bool C = OUT || BACK, Z = OUT || BACK;
-    T x[kSsmTile], dt[kSsmTile], z[kSsmTile], gy[kSsmTile];
-    float bv[w.M], cv[w.M];
+    float since = 0.0f;                                  // sum of the channel's steps
+    constexpr bool C = OUT || BACK;
+    T x[kOwn], dt[kOwn], z[kOwn], gy[kOwn];
+    T bv[w.M], cv[w.M];
     auto load = [&](int64_t t0) {
-        w.load_rows(w.xp, a.x.st, t0, x);
-        w.load_rows(w.dp, a.dt.st, t0, dt);
-        if (Z && w.zp) w.load_rows(w.zp, a.gate.st, t0, z);
-        if (BACK) w.load_rows(gp, a.dy.st, t0, gy);
+        w.load_rows(a.x, t0, x);
+        w.load_rows(a.dt, t0, dt);
+        if (C && gated) w.load_rows(a.gate, t0, z);
+        if (BACK) w.load_rows(a.dy, t0, gy);
         w.load_bc(w.bp, a.b.st, t0, bv);
         if (C) w.load_bc(w.cp, a.c.st, t0, cv);
     };
-    if (w.begin < w.end) load(w.begin);
-    for (int64_t t0 = w.begin; t0 < w.end; t0 += kSsmTile) {
-        float dl[kSsmTile], xs[kSsmTile], g[kSsmTile];
+    // One tile.  WHOLE: all its tokens and channels exist.
+    auto tile = [&](int64_t t0, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        float dl[kOwn], xs[kOwn], g[kOwn], steps = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kSsmTile; ++i) {
-            const bool on = t0 + i < w.end;
-            const float raw = to_f32(dt[i]) + bias;
+        for (int m = 0; m < kOwn; ++m) {
+            const bool on = WHOLE || w.tok(t0, m) < w.end;
+            const float raw = to_f32(dt[m]) + bias;
             float slope;
-            dl[i] = on ? (a.softplus ? softplus(raw, &slope) : raw) : 0.0f;
-            xs[i] = on ? to_f32(x[i]) : 0.0f;
-            if (Z) {
-                const float zf = w.zp ? to_f32(z[i]) : 0.0f;
-                g[i] = w.zp ? zf * logistic(zf) : 1.0f;
-                if (BACK) g[i] = on ? g[i] * to_f32(gy[i]) : 0.0f;
+            dl[m] = on ? (a.softplus ? softplus(raw, &slope) : raw) : 0.0f;
+            xs[m] = on ? to_f32(x[m]) : 0.0f;
+            steps += dl[m];
+            if (C) {
+                const float zf = gated ? to_f32(z[m]) : 0.0f;
+                g[m] = gated ? zf * logistic(zf) : 1.0f;
+                if (BACK) g[m] = on ? g[m] * to_f32(gy[m]) : 0.0f;
             }
         }
         wave_sync();
@@ -287,52 +325,62 @@ __global__ __launch_bounds__(MULTI ? 512 : 64) void ssm_pass(pn_ssm_args a, SsmP
             w.put(w.at(ws + p.marks, t0 / kSsmTile), h);
             if (!MULTI || w.blk == 0) ws[p.since + w.own_at(t0 / kSsmTile)] = since;
         }
+        since += steps + dpp<0x4E>(steps);               // and of the other parity
 #pragma unroll
-        for (int i = 0; i < kSsmTile; ++i) {
-            float bi[S], ci[S], d[4], u[4], gk[4], part[4];
-            w.read_bc(lds, i, 0, bi);
-            if (C) w.read_bc(lds, i, 1, ci);
-            quad_lanes(dl[i], d);
-            quad_lanes(dl[i] * xs[i], u);
-            if (BACK) quad_lanes(g[i], gk);
+        for (int m = 0; m < kOwn; ++m) {
+            float part[4];
+            const float um = dl[m] * xs[m];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                part[k] = 0.0f;
+            for (int par = 0; par < 2; ++par) {
+                float bi[S], ci[S], d[2], u[2], gk[2];
+                w.read_bc(lds, 2 * m + par, 0, bi);
+                if (C) w.read_bc(lds, 2 * m + par, 1, ci);
+                if (par == 0) {
+                    pair<0>(dl[m], d);
+                    pair<0>(um, u);
+                    if (BACK) pair<0>(g[m], gk);
+                } else {
+                    pair<1>(dl[m], d);
+                    pair<1>(um, u);
+                    if (BACK) pair<1>(g[m], gk);
+                }
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    const float f = __builtin_amdgcn_exp2f(d[k] * A2[k][s]);
-                    h[k][s] = fmaf(u[k], bi[s], f * h[k][s]);
-                    if (OUT) part[k] = fmaf(ci[s], h[k][s], part[k]);
-                    if (BACK) {
-                        P[k][s] *= f;
-                        R[k][s] = fmaf(P[k][s], ci[s] * gk[k], R[k][s]);
+                for (int k = 0; k < 2; ++k) {
+                    float y = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        const float f = __builtin_amdgcn_exp2f(d[k] * A2[k][s]);
+                        h[k][s] = fmaf(u[k], bi[s], f * h[k][s]);
+                        if (OUT) y = fmaf(ci[s], h[k][s], y);
+                        if (BACK) {
+                            P[k][s] *= f;
+                            R[k][s] = fmaf(P[k][s], ci[s] * gk[k], R[k][s]);
+                        }
                     }
+                    part[2 * par + k] = y;
                 }
             }
-            since += dl[i];
             if (OUT) {
-                float y = quad_sum(part, w.j);
-                if (MULTI) {
-                    ex[(w.blk * kSsmTile + i) * 64 + w.lane] = y;
-                } else if (t0 + i < w.end && w.own) {
-                    y = (y + skip * xs[i]) * g[i];
-                    yp[(w.b * a.T + t0 + i) * a.D + w.ch] = from_f32<T>(y);
-                }
+                const float y = quad_sum(part, w.j);
+                if (MULTI) ex[(w.blk * kOwn + m) * 64 + w.lane] = y;
+                else if (WHOLE || (w.tok(t0, m) < w.end && w.own)) w.put_row(yp, t0, m, fmaf(skip, xs[m], y) * g[m]);
             }
         }
         if (OUT && MULTI) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kSsmTile; ++i)
-                if (i % p.blocks == w.blk && t0 + i < w.end && w.own) {
-                    const float y = joined<S, MULTI>(ex, p.blocks, i, w.lane);
-                    yp[(w.b * a.T + t0 + i) * a.D + w.ch] = from_f32<T>((y + skip * xs[i]) * g[i]);
-                }
+            for (int m = 0; m < kOwn; ++m)
+                if (m % p.blocks == w.blk && (WHOLE || (w.tok(t0, m) < w.end && w.own)))
+                    w.put_row(yp, t0, m, fmaf(skip, xs[m], joined(ex, p.blocks, m, w.lane)) * g[m]);
             __syncthreads();
         }
-    }
+    };
+    if (w.begin < w.end) load(w.begin);
+    const int64_t whole = w.full ? w.begin + max(w.end - w.begin, static_cast<int64_t>(0)) / kSsmTile * kSsmTile : w.begin;
+    for (int64_t t0 = w.begin; t0 < whole; t0 += kSsmTile) tile(t0, std::true_type{});
+    for (int64_t t0 = whole; t0 < w.end; t0 += kSsmTile) tile(t0, std::false_type{});
     if (OUT) {
-        for (int64_t t = max(w.end, w.begin) + w.blk; t < w.stop; t += p.blocks)
+        for (int64_t t = max(w.end, w.begin) + 2 * w.blk + w.odd; t < w.stop; t += 2 * p.blocks)
             if (w.own) yp[(w.b * a.T + t) * a.D + w.ch] = from_f32<T>(0.0f);
         if (w.seg == p.n_seg - 1 && a.final_state)
             w.states([&](int k, int s, int64_t i) { a.final_state[w.b * a.D * a.N + i] = h[k][s]; });
@@ -388,175 +436,226 @@ struct ChannelSum {
     }
 };
 
+// The waves of a workgroup: blocks of states (MULTI), or adjacent channel
+// blocks, whose shares of db and dc are added in LDS before they are written.
 template <typename T, int S, bool MULTI>
-__global__ __launch_bounds__(MULTI ? 512 : 64) __attribute__((amdgpu_waves_per_eu(2)))
+__global__ __launch_bounds__(MULTI ? 512 : 256) __attribute__((amdgpu_waves_per_eu(2)))
 void ssm_gradients(pn_ssm_args a, SsmPlan p) {
-    constexpr int E = 4 * S, WAVES = MULTI ? 8 : 1;
+    constexpr int E = 4 * S, WAVES = MULTI ? 8 : 4;
     __shared__ __align__(16) float bc_lds[WAVES][kSsmTile * 2 * E];
-    __shared__ float ex[3][MULTI ? WAVES * kSsmTile * 64 : 1];
-    const SsmWave<T, S, MULTI> w(a, p);
+    __shared__ float ex[3][MULTI ? WAVES * kOwn * 64 : 1];
+    __shared__ float shares[2][MULTI ? 1 : WAVES][MULTI ? 1 : kSsmTile * 2 * E];
+    const SsmWave<T, S, !MULTI> w(a, p);
     if (w.seg >= p.n_seg) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float* ws = static_cast<float*>(a.workspace);
-    float* lds = bc_lds[MULTI ? w.blk : 0];
+    float* lds = bc_lds[wave];
     const float bias = a.dt_bias ? a.dt_bias[w.ch] : 0.0f, skip = a.skip ? a.skip[w.ch] : 0.0f;
-    const T* gp = static_cast<const T*>(a.dy.p) + w.b * a.dy.sb;
+    const bool gated = a.gate.p != nullptr;
     T *dxp = static_cast<T*>(a.dx), *ddp = static_cast<T*>(a.ddt), *dzp = static_cast<T*>(a.dgate);
-    float A2[4][S], in[4][S], r[4][S], dA[4][S];
+    float A2[2][S], in[2][S], r[2][S], dA[2][S];
     w.decays(A2);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int s = 0; s < S; ++s) in[k][s] = r[k][s] = dA[k][s] = 0.0f;
     if (w.seg > 0) w.carried(ws, A2, in);
     if (a.d_final_state)
         w.states([&](int k, int s, int64_t i) { r[k][s] = a.d_final_state[w.b * a.D * a.N + i]; });
     for (int i = p.n_seg - 1; i > w.seg; --i) {          // what the segments behind give
-        float more[4][S];
+        float more[2][S];
         w.get(w.at(ws + p.rends, i), more);
         w.fade(r, ws[p.decay + w.own_at(i)], A2, more);
     }
     float dskip = 0.0f, dbias = 0.0f;
-    const int64_t rows = w.b * a.T;
     const int NP = p.blocks * E;
-    float* bc_out = ws + p.part_bc + (static_cast<int64_t>(w.cb) * a.B * a.T + rows) * 2 * NP;
+    float* bc_out = ws + p.part_bc + (static_cast<int64_t>(MULTI ? w.cb : w.cb / p.wide) * a.B + w.b) * a.T * 2 * NP;
     const int value = ChannelSum<S>::of(w.lane);
     const int bc_at = (value / S) * NP + w.n0 + value % S;
     const bool bc_on = ChannelSum<S>::writes(w.lane);
-    for (int64_t t = max(w.end, w.begin) + w.blk; t < w.stop; t += p.blocks)
+    for (int64_t t = max(w.end, w.begin) + 2 * w.blk + w.odd; t < w.stop; t += 2 * p.blocks)
         if (w.own) {
-            const int64_t o = (rows + t) * a.D + w.ch;
+            const int64_t o = (w.b * a.T + t) * a.D + w.ch;
             dxp[o] = from_f32<T>(0.0f);
             ddp[o] = from_f32<T>(0.0f);
-            if (w.zp) dzp[o] = from_f32<T>(0.0f);
+            if (gated) dzp[o] = from_f32<T>(0.0f);
         }
-    for (int64_t t0 = w.begin + (w.end - 1 - w.begin) / kSsmTile * kSsmTile; w.begin < w.end && t0 >= w.begin; t0 -= kSsmTile) {
-        float dl[kSsmTile], xs[kSsmTile], g[kSsmTile], slope[kSsmTile], dz[kSsmTile], e[kSsmTile][4][S], h[4][S];
-        {
-            T x[kSsmTile], dt[kSsmTile], z[kSsmTile], gy[kSsmTile];
-            float bv[w.M], cv[w.M];
-            w.load_rows(w.xp, a.x.st, t0, x);
-            w.load_rows(w.dp, a.dt.st, t0, dt);
-            if (w.zp) w.load_rows(w.zp, a.gate.st, t0, z);
-            w.load_rows(gp, a.dy.st, t0, gy);
-            w.load_bc(w.bp, a.b.st, t0, bv);
-            w.load_bc(w.cp, a.c.st, t0, cv);
-            w.get(w.at(ws + p.marks, t0 / kSsmTile), h);
-            if (w.seg > 0) {
-                float mark[4][S];
+    int turn = 0;
+    T x[kOwn], dt[kOwn], z[kOwn], gy[kOwn], bv[w.M], cv[w.M];
+    float mark[2][S], since = 0.0f;
+    auto load = [&](int64_t t0) {
+        w.load_rows(a.x, t0, x);
+        w.load_rows(a.dt, t0, dt);
+        if (gated) w.load_rows(a.gate, t0, z);
+        w.load_rows(a.dy, t0, gy);
+        w.load_bc(w.bp, a.b.st, t0, bv);
+        w.load_bc(w.cp, a.c.st, t0, cv);
+        w.get(w.at(ws + p.marks, t0 / kSsmTile), mark);
+        if (w.seg > 0) since = ws[p.since + w.own_at(t0 / kSsmTile)];
+    };
+    // One tile.  WHOLE: all its tokens and channels exist.
+    auto tile = [&](int64_t t0, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        float dl[kOwn], xs[kOwn], g[kOwn], slope[kOwn], dz[kOwn], e[kSsmTile][2][S], h[2][S];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+        for (int m = 0; m < kOwn; ++m) {
+            const bool on = WHOLE || w.tok(t0, m) < w.end, mine = WHOLE || (on && w.own);
+            const float raw = to_f32(dt[m]) + bias, dy = to_f32(gy[m]);
+            float sl = 1.0f;
+            const float v = a.softplus ? softplus(raw, &sl) : raw;
+            dl[m] = on ? v : 0.0f;
+            slope[m] = sl;
+            xs[m] = mine ? to_f32(x[m]) : 0.0f;
+            const float zf = gated ? to_f32(z[m]) : 0.0f, sg = logistic(zf);
+            g[m] = mine ? (gated ? dy * zf * sg : dy) : 0.0f;
+            dz[m] = dy * sg * fmaf(zf, 1.0f - sg, 1.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int s = 0; s < S; ++s) h[k][s] = w.seg > 0 ? in[k][s] : mark[k][s];
+        if (w.seg > 0) w.fade(h, since, A2, mark);
+        wave_sync();
+        w.store_bc(lds, 0, bv);
+        w.store_bc(lds, 1, cv);
+        wave_sync();
+        if (t0 > w.begin) load(t0 - kSsmTile);
+#pragma unroll
+        for (int m = 0; m < kOwn; ++m) {
+            __builtin_amdgcn_sched_barrier(0);               // a pair of tokens at a time: registers
+            float part[4];
+            const float um = dl[m] * xs[m];
+#pragma unroll
+            for (int par = 0; par < 2; ++par) {
+                const int i = 2 * m + par;
+                float bi[S], ci[S], d[2], u[2];
+                w.read_bc(lds, i, 0, bi);
+                w.read_bc(lds, i, 1, ci);
+                if (par == 0) {
+                    pair<0>(dl[m], d);
+                    pair<0>(um, u);
+                } else {
+                    pair<1>(dl[m], d);
+                    pair<1>(um, u);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float y = 0.0f;
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
-                        mark[k][s] = h[k][s];
-                        h[k][s] = in[k][s];
+                        e[i][k][s] = __builtin_amdgcn_exp2f(d[k] * A2[k][s]) * h[k][s];
+                        h[k][s] = fmaf(u[k], bi[s], e[i][k][s]);
+                        y = fmaf(ci[s], h[k][s], y);
                     }
-                w.fade(h, ws[p.since + w.own_at(t0 / kSsmTile)], A2, mark);
-            }
-#pragma unroll
-            for (int i = 0; i < kSsmTile; ++i) {
-                const bool on = t0 + i < w.end;
-                const float raw = to_f32(dt[i]) + bias, dy = to_f32(gy[i]);
-                float sl = 1.0f;
-                const float v = a.softplus ? softplus(raw, &sl) : raw;
-                dl[i] = on ? v : 0.0f;
-                slope[i] = sl;
-                xs[i] = on && w.own ? to_f32(x[i]) : 0.0f;
-                const float zf = w.zp ? to_f32(z[i]) : 0.0f, sg = logistic(zf);
-                g[i] = on && w.own ? (w.zp ? dy * zf * sg : dy) : 0.0f;
-                dz[i] = dy * sg * fmaf(zf, 1.0f - sg, 1.0f);
-            }
-            wave_sync();
-            w.store_bc(lds, 0, bv);
-            w.store_bc(lds, 1, cv);
-            wave_sync();
-        }
-#pragma unroll
-        for (int i = 0; i < kSsmTile; ++i) {
-            float bi[S], ci[S], d[4], u[4], part[4];
-            w.read_bc(lds, i, 0, bi);
-            w.read_bc(lds, i, 1, ci);
-            quad_lanes(dl[i], d);
-            quad_lanes(dl[i] * xs[i], u);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                part[k] = 0.0f;
-#pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    e[i][k][s] = __builtin_amdgcn_exp2f(d[k] * A2[k][s]) * h[k][s];
-                    h[k][s] = fmaf(u[k], bi[s], e[i][k][s]);
-                    part[k] = fmaf(ci[s], h[k][s], part[k]);
+                    part[2 * par + k] = y;
                 }
             }
-            if (w.zp) {
+            if (gated) {
                 const float y = quad_sum(part, w.j);
-                if (MULTI) ex[0][(w.blk * kSsmTile + i) * 64 + w.lane] = y;
-                else if (t0 + i < w.end && w.own) dzp[(rows + t0 + i) * a.D + w.ch] = from_f32<T>(dz[i] * fmaf(skip, xs[i], y));
+                if (MULTI) ex[0][(w.blk * kOwn + m) * 64 + w.lane] = y;
+                else if (WHOLE || (w.tok(t0, m) < w.end && w.own)) w.put_row(dzp, t0, m, dz[m] * fmaf(skip, xs[m], y));
             }
         }
 #pragma unroll
-        for (int i = kSsmTile - 1; i >= 0; --i) {
-            float bi[S], ci[S], d[4], u[4], gk[4], s1[4], s2[4], db[S], dc[S], gu = 0.0f;
-            w.read_bc(lds, i, 0, bi);
-            w.read_bc(lds, i, 1, ci);
-            quad_lanes(dl[i], d);
-            quad_lanes(dl[i] * xs[i], u);
-            quad_lanes(g[i], gk);
+        for (int m = kOwn - 1; m >= 0; --m) {
+            __builtin_amdgcn_sched_barrier(0);
+            float s1[4], s2[4];
+            const float um = dl[m] * xs[m];
 #pragma unroll
-            for (int s = 0; s < S; ++s) db[s] = dc[s] = 0.0f;
+            for (int par = 1; par >= 0; --par) {
+                const int i = 2 * m + par;
+                float bi[S], ci[S], d[2], u[2], gk[2], db[S], dc[S], gu = 0.0f;
+                w.read_bc(lds, i, 0, bi);
+                w.read_bc(lds, i, 1, ci);
+                if (par == 0) {
+                    pair<0>(dl[m], d);
+                    pair<0>(um, u);
+                    pair<0>(g[m], gk);
+                } else {
+                    pair<1>(dl[m], d);
+                    pair<1>(um, u);
+                    pair<1>(g[m], gk);
+                }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                s1[k] = s2[k] = 0.0f;
-                gu = fmaf(gk[k], u[k], gu);
+                for (int s = 0; s < S; ++s) db[s] = dc[s] = 0.0f;
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    r[k][s] = fmaf(gk[k], ci[s], r[k][s]);
-                    db[s] = fmaf(r[k][s], u[k], db[s]);
-                    dc[s] = fmaf(gk[k], e[i][k][s], dc[s]);
-                    s1[k] = fmaf(r[k][s], bi[s], s1[k]);
-                    const float x = r[k][s] * e[i][k][s];
-                    s2[k] = fmaf(x, A2[k][s], s2[k]);
-                    dA[k][s] = fmaf(x, d[k], dA[k][s]);
-                    r[k][s] *= __builtin_amdgcn_exp2f(d[k] * A2[k][s]);
+                for (int k = 0; k < 2; ++k) {
+                    float du = 0.0f, dd = 0.0f;
+                    gu = fmaf(gk[k], u[k], gu);
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        r[k][s] = fmaf(gk[k], ci[s], r[k][s]);
+                        db[s] = fmaf(r[k][s], u[k], db[s]);
+                        dc[s] = fmaf(gk[k], e[i][k][s], dc[s]);
+                        du = fmaf(r[k][s], bi[s], du);
+                        const float x = r[k][s] * e[i][k][s];
+                        dd = fmaf(x, A2[k][s], dd);
+                        dA[k][s] = fmaf(x, d[k], dA[k][s]);
+                        r[k][s] *= __builtin_amdgcn_exp2f(d[k] * A2[k][s]);
+                    }
+                    s1[2 * par + k] = du;
+                    s2[2 * par + k] = dd;
+                }
+#pragma unroll
+                for (int s = 0; s < S; ++s) dc[s] = fmaf(gu, bi[s], dc[s]);  // h = e + u b
+                const float sum = ChannelSum<S>::sum(db, dc, w.lane);
+                if (MULTI) {
+                    if (bc_on && (WHOLE || t0 + i < w.end)) bc_out[(t0 + i) * 2 * NP + bc_at] = sum;
+                } else if (bc_on) {
+                    shares[turn][wave][i * 2 * E + bc_at] = sum;
                 }
             }
-#pragma unroll
-            for (int s = 0; s < S; ++s) dc[s] = fmaf(gu, bi[s], dc[s]);      // h = e + u b
-            const float sum = ChannelSum<S>::sum(db, dc, w.lane);
-            if (bc_on && t0 + i < w.end) bc_out[(t0 + i) * 2 * NP + bc_at] = sum;
             const float du = quad_sum(s1, w.j), dd = quad_sum(s2, w.j) * kLn2;
             if (MULTI) {
-                ex[1][(w.blk * kSsmTile + i) * 64 + w.lane] = du;
-                ex[2][(w.blk * kSsmTile + i) * 64 + w.lane] = dd;
-            } else if (t0 + i < w.end && w.own) {
-                const int64_t o = (rows + t0 + i) * a.D + w.ch;
-                const float ddt = fmaf(xs[i], du, dd) * slope[i];
-                dxp[o] = from_f32<T>(fmaf(dl[i], du, skip * g[i]));
-                ddp[o] = from_f32<T>(ddt);
-                dskip = fmaf(g[i], xs[i], dskip);
+                ex[1][(w.blk * kOwn + m) * 64 + w.lane] = du;
+                ex[2][(w.blk * kOwn + m) * 64 + w.lane] = dd;
+            } else if (WHOLE || (w.tok(t0, m) < w.end && w.own)) {
+                const float ddt = fmaf(xs[m], du, dd) * slope[m];
+                w.put_row(dxp, t0, m, fmaf(dl[m], du, skip * g[m]));
+                w.put_row(ddp, t0, m, ddt);
+                dskip = fmaf(g[m], xs[m], dskip);
                 dbias += ddt;
             }
         }
         if (MULTI) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kSsmTile; ++i)
-                if (i % p.blocks == w.blk && t0 + i < w.end && w.own) {
-                    const int64_t o = (rows + t0 + i) * a.D + w.ch;
-                    const float du = joined<S, MULTI>(ex[1], p.blocks, i, w.lane);
-                    const float dd = joined<S, MULTI>(ex[2], p.blocks, i, w.lane);
-                    const float ddt = fmaf(xs[i], du, dd) * slope[i];
-                    dxp[o] = from_f32<T>(fmaf(dl[i], du, skip * g[i]));
-                    ddp[o] = from_f32<T>(ddt);
-                    if (w.zp) dzp[o] = from_f32<T>(dz[i] * fmaf(skip, xs[i], joined<S, MULTI>(ex[0], p.blocks, i, w.lane)));
-                    dskip = fmaf(g[i], xs[i], dskip);
+            for (int m = 0; m < kOwn; ++m)
+                if (m % p.blocks == w.blk && (WHOLE || (w.tok(t0, m) < w.end && w.own))) {
+                    const float du = joined(ex[1], p.blocks, m, w.lane), dd = joined(ex[2], p.blocks, m, w.lane);
+                    const float ddt = fmaf(xs[m], du, dd) * slope[m];
+                    w.put_row(dxp, t0, m, fmaf(dl[m], du, skip * g[m]));
+                    w.put_row(ddp, t0, m, ddt);
+                    if (gated) w.put_row(dzp, t0, m, dz[m] * fmaf(skip, xs[m], joined(ex[0], p.blocks, m, w.lane)));
+                    dskip = fmaf(g[m], xs[m], dskip);
                     dbias += ddt;
                 }
             __syncthreads();
+        } else {
+            __syncthreads();                             // one a tile: the other half of shares is free since the last
+            const int64_t rest = (w.end - t0) * 2 * E;
+            for (int i = threadIdx.x; i < kSsmTile * 2 * E; i += 64 * p.wide) {
+                float v = 0.0f;
+                for (int q = 0; q < p.wide; ++q) v += shares[turn][q][i];
+                if (i < rest) bc_out[t0 * 2 * E + i] = v;
+            }
+            turn ^= 1;
+        }
+    };
+    if (w.begin < w.end) {
+        const int64_t last = w.begin + (w.end - 1 - w.begin) / kSsmTile * kSsmTile;
+        load(last);
+        for (int64_t t0 = last; t0 >= w.begin; t0 -= kSsmTile) {
+            if (w.full && t0 + kSsmTile <= w.end) tile(t0, std::true_type{});
+            else tile(t0, std::false_type{});
         }
     }
+    // the two parities of a channel
+    dskip += dpp<0x4E>(dskip);
+    dbias += dpp<0x4E>(dbias);
     const int64_t part = w.b * p.n_seg + w.seg;
     w.states([&](int k, int s, int64_t i) { ws[p.part_A + part * a.D * a.N + i] = dA[k][s]; });
-    if (w.own) {
+    if (w.own && w.odd == 0) {
         float* v = ws + p.part_vec + (part * p.blocks + w.blk) * 2 * a.D + w.ch;
         v[0] = dskip;
         v[a.D] = dbias;
@@ -567,9 +666,9 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
 
 template <typename T, int S, bool MULTI>
 hipError_t ssm_launch(const pn_ssm_args& a, const SsmPlan& p, SsmPass pass, hipStream_t st) {
-    const int threads = MULTI ? 64 * p.blocks : 64;
+    const int threads = MULTI ? 64 * p.blocks : pass == kSsmGradients ? 64 * p.wide : 64;
     const int64_t segs = pass == kSsmEnds ? p.n_seg - 1 : p.n_seg;
-    const dim3 grid = grid_of(segs * a.B * p.chans, threads);
+    const dim3 grid = grid_of(segs * a.B * (pass == kSsmGradients && !MULTI ? p.chans / p.wide : p.chans), threads);
     switch (pass) {
         case kSsmEnds: ssm_pass<T, S, MULTI, kSsmEnds><<<grid, threads, 0, st>>>(a, p); break;
         case kSsmOutputs: ssm_pass<T, S, MULTI, kSsmOutputs><<<grid, threads, 0, st>>>(a, p); break;
