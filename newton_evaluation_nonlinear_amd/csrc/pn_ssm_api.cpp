@@ -102,7 +102,7 @@ int check_conv(const pn_conv_args* p, bool backward) {
 
 int check_ssm_sizes(int64_t dtype, int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, int64_t softplus) {
     PN_TRY(check_types(dtype, B, T, D));
-    if (D > int64_t(1) << 26) return fail(PN_EUNSUPPORTED, "size too large");
+    if (D > int64_t(1) << 24) return fail(PN_EUNSUPPORTED, "size too large");
     if (N < 1 || N > 128) return fail(PN_EUNSUPPORTED, "1 .. 128 states per channel are supported");
     if (G < 1 || (D > 0 && (G > D || D % G))) return fail(PN_EINVAL, "D must be a multiple of G >= 1");
     if (softplus < 0 || softplus > 1) return fail(PN_EINVAL, "softplus must be 0 or 1");

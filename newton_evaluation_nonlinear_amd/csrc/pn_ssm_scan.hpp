@@ -10,8 +10,8 @@
 // the 4 S states of the quad's two channels, in registers over all tokens.
 // What belongs to a channel and not to a state (step, gate, products with x)
 // is computed once, by the lane of the channel (bit 0 of its number in the
-// quad) and of the token's parity (bit 1); the quad passes such values on by
-// DPP, and sums over its four lanes go back to the lane they belong to.  More
+// quad) and of the token's parity (bit 1); such values pass on through
+// LDS, and sums over its four lanes go back by DPP to the lane they belong to.  More
 // than 16 states are blocks of 16 in as many waves, which add their shares of
 // such sums through LDS.
 //
@@ -30,8 +30,6 @@
 // decay since the segment's start); the second walks the tiles backwards,
 // each once forward from its mark with e kept in registers, once back.
 #pragma once
-
-#include <type_traits>
 
 #include "pn_seq_device.hpp"
 #include "pn_ssm.hpp"
@@ -68,13 +66,18 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// log(1 + e^v) = max(v, 0) + log(1 + t), t = e^-|v|; log(1 + t) as
-// log(w) t / (w - 1) with w = 1 + t rounded: the error of w cancels.
+// Keeps a value's computation where it stands: before a select, not in a branch made of it.
+__device__ __forceinline__ float pinned(float v) {
+    asm("" : "+v"(v));
+    return v;
+}
+
+// log(1 + e^v) = max(v, 0) + log(1 + t), t = e^-|v|; log(1 + t) as log(w) +
+// (t - (w - 1)) / w, w = 1 + t as rounded, which leaves 2^-48 of its rounding.
 __device__ __forceinline__ float softplus(float v, float* slope) {
-    const float t = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e), w = 1.0f + t;
-    const float l = w == 1.0f ? t : __builtin_amdgcn_logf(w) * kLn2 * t * __builtin_amdgcn_rcpf(w - 1.0f);
-    *slope = (v >= 0.0f ? 1.0f : t) * __builtin_amdgcn_rcpf(w);
-    return fmaxf(v, 0.0f) + l;
+    const float t = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e), w = 1.0f + t, r = __builtin_amdgcn_rcpf(w);
+    *slope = (v >= 0.0f ? 1.0f : t) * r;
+    return fmaxf(v, 0.0f) + fmaf(__builtin_amdgcn_logf(w), kLn2, (t - (w - 1.0f)) * r);
 }
 __device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e)); }
 
@@ -90,8 +93,8 @@ struct SsmWave {
     const pn_ssm_args& a;
     const SsmPlan& p;
     int lane, j, odd, blk, seg, cb, ch, first, n0, behind;    // n0: the lane's first state; behind: the channel after the group
-    int64_t b, row, begin, stop, end;                    // row: (b, channel block); stop: of the segment, end: of its tokens
-    bool own, full;                                      // whether the lane's channel exists, and all of the wave's
+    int64_t b, row, begin, stop, end, behind_tiles;      // row: (b, channel block); stop: of the segment, end: of its tokens
+    bool own;                                            // whether the lane's channel exists
     const T *bp, *cp;
 
     __device__ __forceinline__ SsmWave(const pn_ssm_args& a_, const SsmPlan& p_) : a(a_), p(p_) {
@@ -112,22 +115,20 @@ struct SsmWave {
         first = group * DG + in;
         behind = (group + 1) * DG;
         own = mine < DG;
-        full = in + kChans <= DG;
         ch = group * DG + min(mine, DG - 1);
         n0 = blk * E + j * S;
         begin = seg * p.seg;
         stop = min(begin + p.seg, a.T);
         int64_t len = a.T;
-        if (a.lengths) len = max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.lengths[b]), a.T));
+        if (a.lengths) len = max(static_cast<int64_t>(0), min(static_cast<int64_t>(__builtin_amdgcn_readfirstlane(a.lengths[b])), a.T));
         end = min(stop, len);
+        behind_tiles = end > begin ? min(stop, begin + (end - begin + kSsmTile - 1) / kSsmTile * kSsmTile) : begin;
         bp = static_cast<const T*>(a.b.p) + b * a.b.sb + group * a.b.sh;
         cp = static_cast<const T*>(a.c.p) + b * a.c.sb + group * a.c.sh;
     }
     // Channel k of the lane's quad, and whether it exists.
     __device__ __forceinline__ int chan(int k) const { return first + (lane >> 2) * 2 + k; }
     __device__ __forceinline__ bool has(int k) const { return chan(k) < behind; }
-    // Token m of the lane's in the tile at t0.
-    __device__ __forceinline__ int64_t tok(int64_t t0, int m) const { return t0 + 2 * m + odd; }
 
     // f(k, s, index in [D, N]) for the states that exist.
     template <typename F>
@@ -188,15 +189,67 @@ struct SsmWave {
         }
     }
 
+    // Step and u of the lane's tokens, to LDS as [token][channel][2], and those of the quad's two channels from there.
+    __device__ __forceinline__ void store_du(float* lds, int m, float d, float u) const {
+        *reinterpret_cast<Pack<float, 2>*>(lds + ((2 * m + odd) * kChans + (lane >> 2) * 2 + (j & 1)) * 2) = {d, u};
+    }
+    __device__ __forceinline__ void read_du(const float* lds, int i, float* d, float* u) const {
+        const Pack<float, 4> q = *reinterpret_cast<const Pack<float, 4>*>(lds + (i * kChans + (lane >> 2) * 2) * 2);
+        d[0] = q.v[0];
+        u[0] = q.v[1];
+        d[1] = q.v[2];
+        u[1] = q.v[3];
+    }
+    // Likewise g, as [token][channel].
+    __device__ __forceinline__ void store_g(float* lds, int m, float g) const {
+        lds[(2 * m + odd) * kChans + (lane >> 2) * 2 + (j & 1)] = g;
+    }
+    __device__ __forceinline__ void read_g(const float* lds, int i, float* g) const {
+        const Pack<float, 2> q = *reinterpret_cast<const Pack<float, 2>*>(lds + i * kChans + (lane >> 2) * 2);
+        g[0] = q.v[0];
+        g[1] = q.v[1];
+    }
+    // Tokens of the tile at t0 that exist.
+    __device__ __forceinline__ int left(int64_t t0) const { return static_cast<int>(min(end - t0, static_cast<int64_t>(kSsmTile))); }
+    // `rows` rows from p, `width` elements of each: accesses behind the last
+    // read 0 and write nothing (offsets within a tile are 32 bits: sizes and
+    // strides are checked).
+    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rows_at(const T* p, int64_t st, int rows, int width) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), static_cast<short>(0),
+                                                 static_cast<int>(((rows - 1) * static_cast<uint32_t>(st) + width) * sizeof(T)), 0x00020000);
+    }
+    __device__ __forceinline__ static T read(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+        if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+        else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+    }
+    __device__ __forceinline__ static void write(__amdgpu_buffer_rsrc_t r, uint32_t at, float v) {
+        if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, at, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, from_f32<T>(v)), r, at, 0, 0);
+    }
+    static constexpr uint32_t kNowhere = 0x80000000u;    // behind every tile
+    // The lane's tokens and channel of x.
+    __device__ __forceinline__ void load_rows(const pn_tokens& x, int64_t t0, T* v) const {
+        const __amdgpu_buffer_rsrc_t r = rows_at(static_cast<const T*>(x.p) + b * x.sb + t0 * x.st, x.st, left(t0), static_cast<int>(a.D));
+        const uint32_t st = static_cast<uint32_t>(x.st) * sizeof(T), at = odd * st + ch * sizeof(T);
+#pragma unroll
+        for (int m = 0; m < kOwn; ++m) v[m] = read(r, at + 2 * m * st);
+    }
+    // Rows of an output [B, T, D] from t0 on, and where the lane writes.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(void* out, int64_t t0) const {
+        return rows_at(static_cast<const T*>(out) + (b * a.T + t0) * a.D, a.D,
+                       static_cast<int>(min(a.T - t0, static_cast<int64_t>(kSsmTile))), static_cast<int>(a.D));
+    }
+    __device__ __forceinline__ uint32_t row_at(int m) const {
+        const uint32_t st = static_cast<uint32_t>(a.D) * sizeof(T);
+        return (own ? odd * st + ch * sizeof(T) : kNowhere) + 2 * m * st;
+    }
     // The b and c of a tile, to LDS as [token][b | c][E]; 0 for states and tokens that do not exist.
     __device__ __forceinline__ void load_bc(const T* src, int64_t st, int64_t t0, T* v) const {
-        const int left = static_cast<int>(min(end - t0, static_cast<int64_t>(kSsmTile))), N = static_cast<int>(a.N);
-        const T* q = src + t0 * st;
+        const __amdgpu_buffer_rsrc_t r = rows_at(src + t0 * st, st, left(t0), static_cast<int>(a.N));
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            const int i = lane + 64 * m, tok = min(i / E, left - 1), n = min(blk * E + i % E, N - 1);
-            const T x = element(q, (tok * static_cast<uint32_t>(st) + n) * sizeof(T));
-            v[m] = i / E < left && blk * E + i % E < N ? x : from_f32<T>(0.0f);
+            const int i = lane + 64 * m, n = blk * E + i % E;
+            v[m] = read(r, n < a.N && i < kSsmTile * E ? (i / E * static_cast<uint32_t>(st) + n) * sizeof(T) : kNowhere);
         }
     }
     __device__ __forceinline__ void store_bc(float* lds, int which, const T* v) const {
@@ -211,38 +264,7 @@ struct SsmWave {
 #pragma unroll
         for (int s = 0; s < S; ++s) v[s] = q.v[s];
     }
-    // The lane's tokens and channel of x; rows at and after `end` are not read.
-    // A wave's offsets within a tile are 32 bits (strides are checked).
-    __device__ __forceinline__ void load_rows(const pn_tokens& x, int64_t t0, T* v) const {
-        const T* src = static_cast<const T*>(x.p) + b * x.sb + t0 * x.st;
-        const uint32_t st = static_cast<uint32_t>(x.st);
-        if (t0 + kSsmTile <= end) {
-            const uint32_t at = (odd * st + ch) * sizeof(T);
-#pragma unroll
-            for (int m = 0; m < kOwn; ++m) v[m] = element(src + 2 * m * x.st, at);
-        } else {
-            const int left = static_cast<int>(end - t0) - 1;
-#pragma unroll
-            for (int m = 0; m < kOwn; ++m) v[m] = element(src, (min(2 * m + odd, left) * st + ch) * sizeof(T));
-        }
-    }
-    __device__ __forceinline__ static T element(const T* base, uint32_t bytes) {
-        return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + bytes);
-    }
-    // Writes the lane's token m and channel of an output [B, T, D].
-    __device__ __forceinline__ void put_row(void* out, int64_t t0, int m, float v) const {
-        T* base = static_cast<T*>(out) + (b * a.T + t0 + 2 * m) * a.D;
-        const uint32_t at = (odd * static_cast<uint32_t>(a.D) + ch) * sizeof(T);
-        *reinterpret_cast<T*>(reinterpret_cast<char*>(base) + at) = from_f32<T>(v);
-    }
 };
-
-// The step's value and a token's other value at channel k of the quad, token 2 m + P of the tile.
-template <int P>
-__device__ __forceinline__ void pair(float v, float* k) {
-    k[0] = quad_lane<2 * P>(v);
-    k[1] = quad_lane<2 * P + 1>(v);
-}
 
 // The sum over the waves of a workgroup of their values for a lane's token m.
 __device__ __forceinline__ float joined(const float* ex, int blocks, int m, int lane) {
@@ -257,11 +279,12 @@ void ssm_pass(pn_ssm_args a, SsmPlan p) {
     constexpr int E = 4 * S, WAVES = MULTI ? 8 : 1;
     constexpr bool OUT = PASS == kSsmOutputs, MARKS = PASS == kSsmMarks || PASS == kSsmMarksBoth, BACK = PASS == kSsmMarksBoth;
     __shared__ __align__(16) float bc_lds[WAVES][kSsmTile * 2 * E];
+    __shared__ __align__(16) float du_lds[WAVES][kSsmTile * kChans * 2], g_lds[BACK ? WAVES : 1][BACK ? kSsmTile * kChans : 2];
     __shared__ float ex[MULTI && OUT ? WAVES * kOwn * 64 : 1];
     const SsmWave<T, S, false> w(a, p);
     if (w.seg >= (PASS == kSsmEnds ? p.n_seg - 1 : p.n_seg)) return;
     float* ws = static_cast<float*>(a.workspace);
-    float* lds = bc_lds[MULTI ? w.blk : 0];
+    float *lds = bc_lds[MULTI ? w.blk : 0], *du_of = du_lds[MULTI ? w.blk : 0], *g_of = g_lds[MULTI && BACK ? w.blk : 0];
     const float bias = a.dt_bias ? a.dt_bias[w.ch] : 0.0f, skip = a.skip ? a.skip[w.ch] : 0.0f;
     const bool gated = a.gate.p != nullptr;
     T* yp = static_cast<T*>(a.y);
@@ -298,25 +321,31 @@ void ssm_pass(pn_ssm_args a, SsmPlan p) {
         w.load_bc(w.bp, a.b.st, t0, bv);
         if (C) w.load_bc(w.cp, a.c.st, t0, cv);
     };
-    // One tile.  WHOLE: all its tokens and channels exist.
-    auto tile = [&](int64_t t0, auto whole) {
-        constexpr bool WHOLE = decltype(whole)::value;
+    if (w.begin < w.end) load(w.begin);
+    for (int64_t t0 = w.begin; t0 < w.end; t0 += kSsmTile) {
+        const int left = w.left(t0) - w.odd;             // the lane's token m exists if 2 m < left
         float dl[kOwn], xs[kOwn], g[kOwn], steps = 0.0f;
 #pragma unroll
         for (int m = 0; m < kOwn; ++m) {
-            const bool on = WHOLE || w.tok(t0, m) < w.end;
+            const bool on = 2 * m < left;
             const float raw = to_f32(dt[m]) + bias;
             float slope;
-            dl[m] = on ? (a.softplus ? softplus(raw, &slope) : raw) : 0.0f;
+            const float soft = pinned(softplus(raw, &slope));
+            dl[m] = on ? (a.softplus ? soft : raw) : 0.0f;
             xs[m] = on ? to_f32(x[m]) : 0.0f;
             steps += dl[m];
             if (C) {
-                const float zf = gated ? to_f32(z[m]) : 0.0f;
-                g[m] = gated ? zf * logistic(zf) : 1.0f;
+                const float zf = gated ? to_f32(z[m]) : 0.0f, act = pinned(zf * logistic(zf));
+                g[m] = gated ? act : 1.0f;
                 if (BACK) g[m] = on ? g[m] * to_f32(gy[m]) : 0.0f;
             }
         }
         wave_sync();
+#pragma unroll
+        for (int m = 0; m < kOwn; ++m) {
+            w.store_du(du_of, m, dl[m], dl[m] * xs[m]);
+            if (BACK) w.store_g(g_of, m, g[m]);
+        }
         w.store_bc(lds, 0, bv);
         if (C) w.store_bc(lds, 1, cv);
         wave_sync();
@@ -326,24 +355,17 @@ void ssm_pass(pn_ssm_args a, SsmPlan p) {
             if (!MULTI || w.blk == 0) ws[p.since + w.own_at(t0 / kSsmTile)] = since;
         }
         since += steps + dpp<0x4E>(steps);               // and of the other parity
+        [[maybe_unused]] const __amdgpu_buffer_rsrc_t y_rows = w.rows_of(a.y, t0);
 #pragma unroll
         for (int m = 0; m < kOwn; ++m) {
             float part[4];
-            const float um = dl[m] * xs[m];
 #pragma unroll
             for (int par = 0; par < 2; ++par) {
                 float bi[S], ci[S], d[2], u[2], gk[2];
                 w.read_bc(lds, 2 * m + par, 0, bi);
                 if (C) w.read_bc(lds, 2 * m + par, 1, ci);
-                if (par == 0) {
-                    pair<0>(dl[m], d);
-                    pair<0>(um, u);
-                    if (BACK) pair<0>(g[m], gk);
-                } else {
-                    pair<1>(dl[m], d);
-                    pair<1>(um, u);
-                    if (BACK) pair<1>(g[m], gk);
-                }
+                w.read_du(du_of, 2 * m + par, d, u);
+                if (BACK) w.read_g(g_of, 2 * m + par, gk);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float y = 0.0f;
@@ -363,24 +385,20 @@ void ssm_pass(pn_ssm_args a, SsmPlan p) {
             if (OUT) {
                 const float y = quad_sum(part, w.j);
                 if (MULTI) ex[(w.blk * kOwn + m) * 64 + w.lane] = y;
-                else if (WHOLE || (w.tok(t0, m) < w.end && w.own)) w.put_row(yp, t0, m, fmaf(skip, xs[m], y) * g[m]);
+                else w.write(y_rows, w.row_at(m), 2 * m < left ? pinned(fmaf(skip, xs[m], y) * g[m]) : 0.0f);
             }
         }
         if (OUT && MULTI) {
             __syncthreads();
 #pragma unroll
             for (int m = 0; m < kOwn; ++m)
-                if (m % p.blocks == w.blk && (WHOLE || (w.tok(t0, m) < w.end && w.own)))
-                    w.put_row(yp, t0, m, fmaf(skip, xs[m], joined(ex, p.blocks, m, w.lane)) * g[m]);
+                if (m % p.blocks == w.blk)
+                    w.write(y_rows, w.row_at(m), 2 * m < left ? fmaf(skip, xs[m], joined(ex, p.blocks, m, w.lane)) * g[m] : 0.0f);
             __syncthreads();
         }
-    };
-    if (w.begin < w.end) load(w.begin);
-    const int64_t whole = w.full ? w.begin + max(w.end - w.begin, static_cast<int64_t>(0)) / kSsmTile * kSsmTile : w.begin;
-    for (int64_t t0 = w.begin; t0 < whole; t0 += kSsmTile) tile(t0, std::true_type{});
-    for (int64_t t0 = whole; t0 < w.end; t0 += kSsmTile) tile(t0, std::false_type{});
+    }
     if (OUT) {
-        for (int64_t t = max(w.end, w.begin) + 2 * w.blk + w.odd; t < w.stop; t += 2 * p.blocks)
+        for (int64_t t = w.behind_tiles + 2 * w.blk + w.odd; t < w.stop; t += 2 * p.blocks)
             if (w.own) yp[(w.b * a.T + t) * a.D + w.ch] = from_f32<T>(0.0f);
         if (w.seg == p.n_seg - 1 && a.final_state)
             w.states([&](int k, int s, int64_t i) { a.final_state[w.b * a.D * a.N + i] = h[k][s]; });
@@ -436,30 +454,40 @@ struct ChannelSum {
     }
 };
 
+constexpr int kTurn = 4;                 // tiles whose shares of db and dc wait in LDS
+
 // The waves of a workgroup: blocks of states (MULTI), or adjacent channel
-// blocks, whose shares of db and dc are added in LDS before they are written.
+// blocks, whose shares of db and dc are added in LDS before they are written,
+// every kTurn tiles so that the waves need not keep step.
 template <typename T, int S, bool MULTI>
 __global__ __launch_bounds__(MULTI ? 512 : 256) __attribute__((amdgpu_waves_per_eu(2)))
 void ssm_gradients(pn_ssm_args a, SsmPlan p) {
     constexpr int E = 4 * S, WAVES = MULTI ? 8 : 4;
     __shared__ __align__(16) float bc_lds[WAVES][kSsmTile * 2 * E];
+    __shared__ __align__(16) float du_lds[WAVES][kSsmTile * kChans * 2], g_lds[WAVES][kSsmTile * kChans];
     __shared__ float ex[3][MULTI ? WAVES * kOwn * 64 : 1];
-    __shared__ float shares[2][MULTI ? 1 : WAVES][MULTI ? 1 : kSsmTile * 2 * E];
+    __shared__ float shares[2][MULTI ? 1 : kTurn][MULTI ? 1 : WAVES][MULTI ? 1 : kSsmTile * 2 * E];
+    __shared__ __align__(16) float in_lds[WAVES][128 * S];
     const SsmWave<T, S, !MULTI> w(a, p);
     if (w.seg >= p.n_seg) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float* ws = static_cast<float*>(a.workspace);
-    float* lds = bc_lds[wave];
+    float *lds = bc_lds[wave], *du_of = du_lds[wave], *g_of = g_lds[wave];
     const float bias = a.dt_bias ? a.dt_bias[w.ch] : 0.0f, skip = a.skip ? a.skip[w.ch] : 0.0f;
     const bool gated = a.gate.p != nullptr;
     T *dxp = static_cast<T*>(a.dx), *ddp = static_cast<T*>(a.ddt), *dzp = static_cast<T*>(a.dgate);
-    float A2[2][S], in[2][S], r[2][S], dA[2][S];
+    float A2[2][S], r[2][S], dA[2][S];
     w.decays(A2);
+    float* in = in_lds[wave] + w.lane * S;               // the segment's first state: the lane's own, in put()'s order
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int s = 0; s < S; ++s) in[k][s] = r[k][s] = dA[k][s] = 0.0f;
-    if (w.seg > 0) w.carried(ws, A2, in);
+        for (int s = 0; s < S; ++s) r[k][s] = dA[k][s] = 0.0f;
+    if (w.seg > 0) {
+        float h[2][S];
+        w.carried(ws, A2, h);
+        w.put(in, h);
+    }
     if (a.d_final_state)
         w.states([&](int k, int s, int64_t i) { r[k][s] = a.d_final_state[w.b * a.D * a.N + i]; });
     for (int i = p.n_seg - 1; i > w.seg; --i) {          // what the segments behind give
@@ -473,16 +501,15 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
     const int value = ChannelSum<S>::of(w.lane);
     const int bc_at = (value / S) * NP + w.n0 + value % S;
     const bool bc_on = ChannelSum<S>::writes(w.lane);
-    for (int64_t t = max(w.end, w.begin) + 2 * w.blk + w.odd; t < w.stop; t += 2 * p.blocks)
+    for (int64_t t = w.behind_tiles + 2 * w.blk + w.odd; t < w.stop; t += 2 * p.blocks)
         if (w.own) {
             const int64_t o = (w.b * a.T + t) * a.D + w.ch;
             dxp[o] = from_f32<T>(0.0f);
             ddp[o] = from_f32<T>(0.0f);
             if (gated) dzp[o] = from_f32<T>(0.0f);
         }
-    int turn = 0;
+    int turn = 0;                                        // tiles done
     T x[kOwn], dt[kOwn], z[kOwn], gy[kOwn], bv[w.M], cv[w.M];
-    float mark[2][S], since = 0.0f;
     auto load = [&](int64_t t0) {
         w.load_rows(a.x, t0, x);
         w.load_rows(a.dt, t0, dt);
@@ -490,54 +517,56 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
         w.load_rows(a.dy, t0, gy);
         w.load_bc(w.bp, a.b.st, t0, bv);
         w.load_bc(w.cp, a.c.st, t0, cv);
-        w.get(w.at(ws + p.marks, t0 / kSsmTile), mark);
-        if (w.seg > 0) since = ws[p.since + w.own_at(t0 / kSsmTile)];
     };
-    // One tile.  WHOLE: all its tokens and channels exist.
-    auto tile = [&](int64_t t0, auto whole) {
-        constexpr bool WHOLE = decltype(whole)::value;
-        float dl[kOwn], xs[kOwn], g[kOwn], slope[kOwn], dz[kOwn], e[kSsmTile][2][S], h[2][S];
+    const int64_t last = w.begin + (w.end - 1 - w.begin) / kSsmTile * kSsmTile;
+    if (w.begin < w.end) load(last);
+    for (int64_t t0 = last; w.begin < w.end && t0 >= w.begin; t0 -= kSsmTile) {
+        const int left = w.left(t0) - w.odd;             // the lane's token m exists if 2 m < left
+        float dl[kOwn], xs[kOwn], g[kOwn], slope[kOwn], dz[kOwn], e[kSsmTile][2][S], h[2][S], mark[2][S];
+        w.get(w.at(ws + p.marks, t0 / kSsmTile), mark);
+        wave_sync();                                     // the last tile's have been read
+        const float since = w.seg > 0 ? ws[p.since + w.own_at(t0 / kSsmTile)] : 0.0f;
 #pragma unroll
         for (int m = 0; m < kOwn; ++m) {
-            const bool on = WHOLE || w.tok(t0, m) < w.end, mine = WHOLE || (on && w.own);
+            const bool on = 2 * m < left, mine = on && w.own;
             const float raw = to_f32(dt[m]) + bias, dy = to_f32(gy[m]);
             float sl = 1.0f;
-            const float v = a.softplus ? softplus(raw, &sl) : raw;
-            dl[m] = on ? v : 0.0f;
-            slope[m] = sl;
+            const float soft = pinned(softplus(raw, &sl));
+            dl[m] = on ? (a.softplus ? soft : raw) : 0.0f;
+            slope[m] = a.softplus ? pinned(sl) : 1.0f;
             xs[m] = mine ? to_f32(x[m]) : 0.0f;
-            const float zf = gated ? to_f32(z[m]) : 0.0f, sg = logistic(zf);
-            g[m] = mine ? (gated ? dy * zf * sg : dy) : 0.0f;
+            const float zf = gated ? to_f32(z[m]) : 0.0f, sg = logistic(zf), act = pinned(zf * sg);
+            g[m] = mine ? (gated ? dy * act : dy) : 0.0f;
             dz[m] = dy * sg * fmaf(zf, 1.0f - sg, 1.0f);
+            w.store_du(du_of, m, dl[m], dl[m] * xs[m]);
+            w.store_g(g_of, m, g[m]);
         }
+        if (w.seg > 0) {
+            w.get(in, h);
+            w.fade(h, since, A2, mark);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int s = 0; s < S; ++s) h[k][s] = w.seg > 0 ? in[k][s] : mark[k][s];
-        if (w.seg > 0) w.fade(h, since, A2, mark);
-        wave_sync();
+                for (int s = 0; s < S; ++s) h[k][s] = mark[k][s];
+        }
         w.store_bc(lds, 0, bv);
         w.store_bc(lds, 1, cv);
         wave_sync();
         if (t0 > w.begin) load(t0 - kSsmTile);
+        const __amdgpu_buffer_rsrc_t dx_rows = w.rows_of(a.dx, t0), dd_rows = w.rows_of(a.ddt, t0);
+        const __amdgpu_buffer_rsrc_t dz_rows = w.rows_of(a.dgate, t0);
 #pragma unroll
         for (int m = 0; m < kOwn; ++m) {
             __builtin_amdgcn_sched_barrier(0);               // a pair of tokens at a time: registers
             float part[4];
-            const float um = dl[m] * xs[m];
 #pragma unroll
             for (int par = 0; par < 2; ++par) {
                 const int i = 2 * m + par;
                 float bi[S], ci[S], d[2], u[2];
                 w.read_bc(lds, i, 0, bi);
                 w.read_bc(lds, i, 1, ci);
-                if (par == 0) {
-                    pair<0>(dl[m], d);
-                    pair<0>(um, u);
-                } else {
-                    pair<1>(dl[m], d);
-                    pair<1>(um, u);
-                }
+                w.read_du(du_of, i, d, u);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float y = 0.0f;
@@ -553,29 +582,21 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
             if (gated) {
                 const float y = quad_sum(part, w.j);
                 if (MULTI) ex[0][(w.blk * kOwn + m) * 64 + w.lane] = y;
-                else if (WHOLE || (w.tok(t0, m) < w.end && w.own)) w.put_row(dzp, t0, m, dz[m] * fmaf(skip, xs[m], y));
+                else w.write(dz_rows, w.row_at(m), 2 * m < left ? pinned(dz[m] * fmaf(skip, xs[m], y)) : 0.0f);
             }
         }
 #pragma unroll
         for (int m = kOwn - 1; m >= 0; --m) {
             __builtin_amdgcn_sched_barrier(0);
             float s1[4], s2[4];
-            const float um = dl[m] * xs[m];
 #pragma unroll
             for (int par = 1; par >= 0; --par) {
                 const int i = 2 * m + par;
                 float bi[S], ci[S], d[2], u[2], gk[2], db[S], dc[S], gu = 0.0f;
                 w.read_bc(lds, i, 0, bi);
                 w.read_bc(lds, i, 1, ci);
-                if (par == 0) {
-                    pair<0>(dl[m], d);
-                    pair<0>(um, u);
-                    pair<0>(g[m], gk);
-                } else {
-                    pair<1>(dl[m], d);
-                    pair<1>(um, u);
-                    pair<1>(g[m], gk);
-                }
+                w.read_du(du_of, i, d, u);
+                w.read_g(g_of, i, gk);
 #pragma unroll
                 for (int s = 0; s < S; ++s) db[s] = dc[s] = 0.0f;
 #pragma unroll
@@ -600,19 +621,19 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
                 for (int s = 0; s < S; ++s) dc[s] = fmaf(gu, bi[s], dc[s]);  // h = e + u b
                 const float sum = ChannelSum<S>::sum(db, dc, w.lane);
                 if (MULTI) {
-                    if (bc_on && (WHOLE || t0 + i < w.end)) bc_out[(t0 + i) * 2 * NP + bc_at] = sum;
+                    if (bc_on && t0 + i < w.end) bc_out[(t0 + i) * 2 * NP + bc_at] = sum;
                 } else if (bc_on) {
-                    shares[turn][wave][i * 2 * E + bc_at] = sum;
+                    shares[turn / kTurn & 1][turn % kTurn][wave][i * 2 * E + bc_at] = sum;
                 }
             }
             const float du = quad_sum(s1, w.j), dd = quad_sum(s2, w.j) * kLn2;
             if (MULTI) {
                 ex[1][(w.blk * kOwn + m) * 64 + w.lane] = du;
                 ex[2][(w.blk * kOwn + m) * 64 + w.lane] = dd;
-            } else if (WHOLE || (w.tok(t0, m) < w.end && w.own)) {
-                const float ddt = fmaf(xs[m], du, dd) * slope[m];
-                w.put_row(dxp, t0, m, fmaf(dl[m], du, skip * g[m]));
-                w.put_row(ddp, t0, m, ddt);
+            } else {
+                const float ddt = 2 * m < left ? pinned(fmaf(xs[m], du, dd) * slope[m]) : 0.0f;
+                w.write(dx_rows, w.row_at(m), 2 * m < left ? pinned(fmaf(dl[m], du, skip * g[m])) : 0.0f);
+                w.write(dd_rows, w.row_at(m), ddt);
                 dskip = fmaf(g[m], xs[m], dskip);
                 dbias += ddt;
             }
@@ -621,33 +642,30 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
             __syncthreads();
 #pragma unroll
             for (int m = 0; m < kOwn; ++m)
-                if (m % p.blocks == w.blk && (WHOLE || (w.tok(t0, m) < w.end && w.own))) {
+                if (m % p.blocks == w.blk) {
                     const float du = joined(ex[1], p.blocks, m, w.lane), dd = joined(ex[2], p.blocks, m, w.lane);
-                    const float ddt = fmaf(xs[m], du, dd) * slope[m];
-                    w.put_row(dxp, t0, m, fmaf(dl[m], du, skip * g[m]));
-                    w.put_row(ddp, t0, m, ddt);
-                    if (gated) w.put_row(dzp, t0, m, dz[m] * fmaf(skip, xs[m], joined(ex[0], p.blocks, m, w.lane)));
+                    const float ddt = 2 * m < left ? pinned(fmaf(xs[m], du, dd) * slope[m]) : 0.0f;
+                    w.write(dx_rows, w.row_at(m), 2 * m < left ? pinned(fmaf(dl[m], du, skip * g[m])) : 0.0f);
+                    w.write(dd_rows, w.row_at(m), ddt);
+                    if (gated)
+                        w.write(dz_rows, w.row_at(m), 2 * m < left ? dz[m] * fmaf(skip, xs[m], joined(ex[0], p.blocks, m, w.lane)) : 0.0f);
                     dskip = fmaf(g[m], xs[m], dskip);
                     dbias += ddt;
                 }
             __syncthreads();
         } else {
-            __syncthreads();                             // one a tile: the other half of shares is free since the last
-            const int64_t rest = (w.end - t0) * 2 * E;
-            for (int i = threadIdx.x; i < kSsmTile * 2 * E; i += 64 * p.wide) {
-                float v = 0.0f;
-                for (int q = 0; q < p.wide; ++q) v += shares[turn][q][i];
-                if (i < rest) bc_out[t0 * 2 * E + i] = v;
+            if (turn % kTurn == kTurn - 1 || t0 == w.begin) {
+                __syncthreads();                         // the other half of shares is free since the last
+                const int tiles = turn % kTurn + 1;
+                for (int i = threadIdx.x; i < tiles * kSsmTile * 2 * E; i += 64 * p.wide) {
+                    const int n = i / (kSsmTile * 2 * E), at = i % (kSsmTile * 2 * E);
+                    float v = 0.0f;
+                    for (int q = 0; q < p.wide; ++q) v += shares[turn / kTurn & 1][n][q][at];
+                    const int64_t from = t0 + (tiles - 1 - n) * kSsmTile;
+                    if (at < (w.end - from) * 2 * E) bc_out[from * 2 * E + at] = v;
+                }
             }
-            turn ^= 1;
-        }
-    };
-    if (w.begin < w.end) {
-        const int64_t last = w.begin + (w.end - 1 - w.begin) / kSsmTile * kSsmTile;
-        load(last);
-        for (int64_t t0 = last; t0 >= w.begin; t0 -= kSsmTile) {
-            if (w.full && t0 + kSsmTile <= w.end) tile(t0, std::true_type{});
-            else tile(t0, std::false_type{});
+            ++turn;
         }
     }
     // the two parities of a channel
