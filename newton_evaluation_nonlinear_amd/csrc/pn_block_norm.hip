@@ -14,15 +14,12 @@
 
 #include <algorithm>
 
-#include "pn_seq_device.hpp"
 #include "pn_ssm.hpp"
+#include "pn_ssm_device.hpp"
 
 namespace pn {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e)); }
 
 // Sums of two values over the workgroup, in every lane.
 template <int THREADS>
@@ -142,14 +139,21 @@ __global__ __launch_bounds__(THREADS) void block_norm(pn_block_norm_args a) {
 // A workgroup takes `rows` rows one after the other; each lane keeps the sums
 // of its channels' weight gradients, which go to part[workgroup][3][D].
 template <typename T, typename R, int V, int NU, int THREADS>
-__global__ __launch_bounds__(THREADS) void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float* part) {
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(4)))
+void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float* part) {
     __shared__ float lds[2 * (THREADS / 64)];
     const int64_t wg = block_id();
     if (wg >= n_wg) return;
     const Row<V, NU, THREADS> r{static_cast<int>(a.D)};
     const float eps = static_cast<float>(a.eps), inv = 1.0f / static_cast<float>(a.D);
-    float dw[NU][V], dpw[NU][V], dsc[NU][V];
-    r.each([&](int u, int i) { dw[u][i] = dpw[u][i] = dsc[u][i] = 0.0f; });
+    float w[NU][V], pw[NU][V], sc[NU][V], dw[NU][V], dpw[NU][V], dsc[NU][V];
+    r.each([&](int u, int i) {
+        dw[u][i] = dpw[u][i] = dsc[u][i] = 0.0f;
+        w[u][i] = pw[u][i] = sc[u][i] = 1.0f;
+    });
+    if (a.weight) r.load(a.weight, w);
+    if (a.post_weight) r.load(a.post_weight, pw);
+    if (a.scale) r.load(a.scale, sc);
     const int64_t end = min((wg + 1) * rows, a.B * a.T);
     for (int64_t row = wg * rows; row < end; ++row) {
         const int64_t b = row / a.T, tok = row - b * a.T;
@@ -163,10 +167,9 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward(pn_block_norm_arg
             r.each([&](int u, int i) { t[u][i] = 0.0f; });
         }
         if (a.weight) {
-            float s[NU][V], e[NU][V], w[NU][V], ss = 0.0f, es = 0.0f;
+            float s[NU][V], e[NU][V], ss = 0.0f, es = 0.0f;
             r.load(row_of<R>(a.s_in, b, tok), s);
             r.load(row_of<T>(a.dy, b, tok), e);
-            r.load(a.weight, w);
             r.each([&](int u, int i) {
                 ss = fmaf(s[u][i], s[u][i], ss);
                 es = fmaf(e[u][i] * w[u][i], s[u][i], es);
@@ -184,29 +187,21 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward(pn_block_norm_arg
         r.each([&](int u, int i) { act[u][i] = a.gate.p ? logistic(g[u][i]) : 1.0f; });
         auto silu = [&](int u, int i) { return a.gate.p ? g[u][i] * act[u][i] : 1.0f; };
         if (a.post_weight) {
-            float w[NU][V], sc[NU][V], uu = 0.0f, qu = 0.0f;
-            r.load(a.post_weight, w);
-            if (a.scale) {
-                r.load(a.scale, sc);
-            } else {
-                r.each([&](int u, int i) { sc[u][i] = 1.0f; });
-            }
+            float uu = 0.0f, qu = 0.0f;
             r.each([&](int u, int i) {
                 const float v = x[u][i] * silu(u, i);
                 uu = fmaf(v, v, uu);
-                qu = fmaf(w[u][i] * sc[u][i] * t[u][i], v, qu);
+                qu = fmaf(pw[u][i] * sc[u][i] * t[u][i], v, qu);
             });
             row_sums<THREADS>(uu, qu, lds);
             const float ru = 1.0f / sqrtf(fmaf(uu, inv, eps)), mean = qu * ru * inv;
             r.each([&](int u, int i) {
                 const float n = x[u][i] * silu(u, i) * ru, tn = t[u][i] * n;
                 dpw[u][i] = fmaf(sc[u][i], tn, dpw[u][i]);
-                dsc[u][i] = fmaf(w[u][i], tn, dsc[u][i]);
-                t[u][i] = ru * fmaf(-n, mean, w[u][i] * sc[u][i] * t[u][i]);
+                dsc[u][i] = fmaf(pw[u][i], tn, dsc[u][i]);
+                t[u][i] = ru * fmaf(-n, mean, pw[u][i] * sc[u][i] * t[u][i]);
             });
         } else if (a.scale) {
-            float sc[NU][V];
-            r.load(a.scale, sc);
             r.each([&](int u, int i) {
                 dsc[u][i] = fmaf(t[u][i], x[u][i] * silu(u, i), dsc[u][i]);
                 t[u][i] *= sc[u][i];
@@ -261,41 +256,43 @@ int widest(const pn_block_norm_args& a, bool backward) {
 }
 
 // f(form) for rows of D channels, V at a time: the fewest waves that hold a
-// row in up to `most` values a lane; four waves a row where `spread` (few
-// rows: latency).
-template <int V, int MOST, typename F>
-hipError_t with_threads(int64_t D, bool spread, F f) {
-    constexpr int NU = MOST / V, ALL = 16384 / (1024 * V);
-    if (!spread && D <= 64 * V) return f(Form<V, 1, 64>{});
-    if (!spread && D <= 64 * V * NU) return f(Form<V, NU, 64>{});
-    if (D <= 256 * V) return f(Form<V, 1, 256>{});
-    if (D <= 256 * V * NU) return f(Form<V, NU, 256>{});
-    if (D <= 1024 * V * (ALL / 2)) return f(Form<V, ALL / 2, 1024>{});
-    return f(Form<V, ALL, 1024>{});
+// row in 8 values a lane (16 past 8192).  More values would take the registers
+// of the waves that hide each other's waits: 2050 channels in pairs, float32
+// residual, gradients of 8188 rows: 217 us with 16, see the head for 8.
+template <int V, typename F>
+hipError_t with_threads(int64_t D, F f) {
+    constexpr int NU = 8 / V;
+    if (D <= 512) return f(Form<V, NU, 64>{});
+    if (D <= 1024) return f(Form<V, NU, 128>{});
+    if (D <= 2048) return f(Form<V, NU, 256>{});
+    if (D <= 4096) return f(Form<V, NU, 512>{});
+    if (D <= 8192) return f(Form<V, NU, 1024>{});
+    return f(Form<V, 2 * NU, 1024>{});
 }
 
 template <typename T, typename R, typename F>
-hipError_t with_form(const pn_block_norm_args& a, int V, bool spread, F f) {
+hipError_t with_form(const pn_block_norm_args& a, int V, F f) {
     constexpr int W = 16 / sizeof(T);
-    if (V == W) return with_threads<W, 16>(a.D, spread, f);
-    if (V == 2) return with_threads<2, 16>(a.D, spread, f);
-    return with_threads<1, 8>(a.D, spread, f);
+    if (V == W) return with_threads<W>(a.D, f);
+    if (V == 2) return with_threads<2>(a.D, f);
+    return with_threads<1>(a.D, f);
 }
 
 template <typename T, typename R>
 hipError_t forward_typed(const pn_block_norm_args& a, hipStream_t st) {
     const int64_t rows = a.B * a.T;
-    return with_form<T, R>(a, widest<T, R>(a, false), rows < 1024, [&](auto form) {
+    return with_form<T, R>(a, widest<T, R>(a, false), [&](auto form) {
         using Fm = decltype(form);
         block_norm<T, R, Fm::V, Fm::NU, Fm::THREADS><<<grid_of(rows, Fm::THREADS), Fm::THREADS, 0, st>>>(a);
         return hipGetLastError();
     });
 }
 
-// Rows of a workgroup of the gradients.
+// Rows of a workgroup of the gradients: four workgroups of four waves for
+// every unit, whose shares of the weights' gradients are then few.
 void backward_split(const pn_block_norm_args& a, int64_t* rows, int64_t* n_wg) {
     const int64_t n = a.B * a.T;
-    *rows = std::max<int64_t>(1, (n + 2047) / 2048);
+    *rows = std::max<int64_t>(1, (n + 1023) / 1024);
     *n_wg = (n + *rows - 1) / *rows;
 }
 
@@ -304,7 +301,7 @@ hipError_t backward_typed(const pn_block_norm_args& a, hipStream_t st) {
     int64_t rows, n_wg;
     backward_split(a, &rows, &n_wg);
     float* part = static_cast<float*>(a.workspace);
-    const hipError_t e = with_form<T, R>(a, widest<T, R>(a, true), a.B * a.T < 1024, [&](auto form) {
+    const hipError_t e = with_form<T, R>(a, widest<T, R>(a, true), [&](auto form) {
         using Fm = decltype(form);
         block_norm_backward<T, R, Fm::V, Fm::NU, Fm::THREADS><<<grid_of(n_wg, Fm::THREADS), Fm::THREADS, 0, st>>>(a, rows, n_wg, part);
         return hipGetLastError();

@@ -4,30 +4,28 @@
 //     dx_t = sum_k w_k d_{t+W-1-k},   dw_k = sum_t d_t x_{t-W+1+k},   dbias = sum_t d_t,
 // and its single-token form.
 //
-// Bound: bytes.  A thread takes V adjacent channels (16 bytes where sizes,
+// Bound: bytes.  A thread takes V adjacent channels (8 bytes where sizes,
 // strides and alignment allow, one channel otherwise) and walks `run` tokens
 // with the last W - 1 in registers, so that a token is read once and, at the
-// ends of runs, W - 1 times more.
+// ends of runs, W - 1 times more.  (16 bytes at a time take twice the
+// registers and leave too few waves: 62 us where 8 take 50, 8 x 4096 tokens of
+// 2048 channels in bfloat16.)
 
 #include <algorithm>
 
-#include "pn_seq_device.hpp"
 #include "pn_ssm.hpp"
+#include "pn_ssm_device.hpp"
 
 namespace pn {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct ConvCut {
     int64_t run;             // tokens of a thread
     int64_t runs;            // of a sequence
     int vecs;                // threads across the channels
 };
-
-// e^-v past float32 is infinite and its reciprocal 0: -0 for v far below 0.
-__device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e)); }
 
 template <typename T, int V>
 __device__ __forceinline__ void load(const T* p, float* v) {
@@ -57,14 +55,13 @@ __device__ __forceinline__ void token(const pn_conv_args& a, int64_t b, int64_t 
     }
 }
 
-// The taps of V channels, in the last W of K places.
-template <int V, int K>
-__device__ __forceinline__ void taps(const pn_conv_args& a, int d, float (*w)[V]) {
-    const int W = static_cast<int>(a.W);
+// The taps of V channels in their places (P: see Taps below), 0 in the others.
+template <int V, typename P>
+__device__ __forceinline__ void weights(const pn_conv_args& a, const P& taps, int d, float (*w)[V]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < P::K; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) w[k][i] = k >= K - W ? a.weight[static_cast<int64_t>(d + i) * W + k - (K - W)] : 0.0f;
+        for (int i = 0; i < V; ++i) w[k][i] = taps.at(k) ? a.weight[(d + i) * a.W + k - taps.first] : 0.0f;
 }
 
 struct Place {
@@ -87,12 +84,25 @@ __device__ __forceinline__ int64_t length(const pn_conv_args& a, int64_t b) {
     return a.lengths ? max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.lengths[b]), a.T)) : a.T;
 }
 
-// K: 4 or 8 places for taps.  Four tokens at a time, their loads together.
-template <typename T, int V, int K>
+// Places for taps: K of them hold W, or exactly W taps (known then, without a
+// branch a tap).  Four tokens at a time; the next four are loaded before the
+// products of these.
+template <int K_, bool EXACT_>
+struct Taps {
+    static constexpr int K = K_;
+    static constexpr bool EXACT = EXACT_;
+    int first;               // place of the first tap
+    __host__ __device__ __forceinline__ explicit Taps(int64_t W) : first(EXACT ? 0 : K - static_cast<int>(W)) {}
+    __device__ __forceinline__ bool at(int k) const { return EXACT || k >= first; }
+};
+
+template <typename T, int V, typename P>
 __global__ __launch_bounds__(kBlock) void conv(pn_conv_args a, ConvCut c) {
+    constexpr int K = P::K;
     const Place p = place<V>(a, c);
     if (!p.on) return;
-    const int W = static_cast<int>(a.W);
+    const P taps(a.W);
+    const int W = P::EXACT ? K : static_cast<int>(a.W);
     const int64_t n = length(a, p.b), t0 = p.run * c.run, t1 = min(t0 + c.run, a.T), end = min(t1, n);
     T* y = static_cast<T*>(a.y) + p.b * a.T * a.D + p.d;
     if (p.run == 0 && a.final_state)
@@ -101,35 +111,47 @@ __global__ __launch_bounds__(kBlock) void conv(pn_conv_args a, ConvCut c) {
             token<T, V>(a, p.b, n - (W - 1) + r, n, p.d, v);
             store<T, V>(static_cast<T*>(a.final_state) + (p.b * (W - 1) + r) * a.D + p.d, v);
         }
-    float w[K][V], bias[V], x[K - 1 + 4][V];
-    taps<V, K>(a, p.d, w);
+    if (t0 < end) {
+        float w[K][V], bias[V], x[K - 1 + 4][V];
+        weights<V>(a, taps, p.d, w);
 #pragma unroll
-    for (int i = 0; i < V; ++i) bias[i] = a.bias ? a.bias[p.d + i] : 0.0f;
-#pragma unroll
-    for (int k = 0; k < K - 1; ++k)
-        if (k >= K - W) token<T, V>(a, p.b, t0 - (K - 1) + k, n, p.d, x[k]);
-    for (int64_t t = t0; t < end; t += 4) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) token<T, V>(a, p.b, t + j, end, p.d, x[K - 1 + j]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float v[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = bias[i];
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (k >= K - W)                          // taps that are not there touch no token
-#pragma unroll
-                    for (int i = 0; i < V; ++i) v[i] = fmaf(w[k][i], x[j + k][i], v[i]);
-            if (a.activation)
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[i] *= logistic(v[i]);
-            if (t + j < end) store<T, V>(y + (t + j) * a.D, v);
-        }
+        for (int i = 0; i < V; ++i) bias[i] = a.bias ? a.bias[p.d + i] : 0.0f;
 #pragma unroll
         for (int k = 0; k < K - 1; ++k)
+            if (taps.at(k)) token<T, V>(a, p.b, t0 - (K - 1) + k, n, p.d, x[k]);
+        const T* row = static_cast<const T*>(a.x.p) + p.b * a.x.sb + p.d;
+        Pack<T, V> next[4];
+        auto fetch = [&](int64_t t) {                    // rows behind the last are the last again: not stored
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[k][i] = x[k + 4][i];
+            for (int j = 0; j < 4; ++j) next[j] = *reinterpret_cast<const Pack<T, V>*>(row + min(t + j, end - 1) * a.x.st);
+        };
+        fetch(t0);
+        for (int64_t t = t0; t < end; t += 4) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[K - 1 + j][i] = to_f32(next[j].v[i]);
+            if (t + 4 < end) fetch(t + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float v[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = bias[i];
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (taps.at(k))                      // taps that are not there touch no token
+#pragma unroll
+                        for (int i = 0; i < V; ++i) v[i] = fmaf(w[k][i], x[j + k][i], v[i]);
+                if (a.activation)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] *= logistic(v[i]);
+                if (t + j < end) store<T, V>(y + (t + j) * a.D, v);
+            }
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[k][i] = x[k + 4][i];
+        }
     }
     const float zero[V] = {};
     for (int64_t t = max(end, t0); t < t1; ++t) store<T, V>(y + t * a.D, zero);
@@ -137,14 +159,16 @@ __global__ __launch_bounds__(kBlock) void conv(pn_conv_args a, ConvCut c) {
 
 // Gradients.  The walk goes over tokens t0 .. t1 + W - 2: each gives d_t from
 // its W tokens, and with it dx of the token W - 1 before.
-template <typename T, int V, int K>
+template <typename T, int V, typename P>
 __global__ __launch_bounds__(kBlock) void conv_backward(pn_conv_args a, ConvCut c, float* part) {
+    constexpr int K = P::K;
     const Place p = place<V>(a, c);
     if (!p.on) return;
-    const int W = static_cast<int>(a.W), past = W - 1;
+    const P taps(a.W);
+    const int W = P::EXACT ? K : static_cast<int>(a.W), past = W - 1;
     const int64_t n = length(a, p.b), t0 = p.run * c.run, t1 = min(t0 + c.run, a.T);
     float w[K][V], bias[V], x[K][V], d[K][V], dw[K][V], db[V];
-    taps<V, K>(a, p.d, w);
+    weights<V>(a, taps, p.d, w);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         bias[i] = a.bias ? a.bias[p.d + i] : 0.0f;
@@ -154,79 +178,79 @@ __global__ __launch_bounds__(kBlock) void conv_backward(pn_conv_args a, ConvCut 
     }
 #pragma unroll
     for (int k = 0; k < K - 1; ++k)
-        if (k >= K - W) token<T, V>(a, p.b, t0 - (K - 1) + k, n, p.d, x[k + 1]);
+        if (taps.at(k)) token<T, V>(a, p.b, t0 - (K - 1) + k, n, p.d, x[k + 1]);
+    const T* xrow = static_cast<const T*>(a.x.p) + p.b * a.x.sb + p.d;
+    const T* grow = static_cast<const T*>(a.dy.p) + p.b * a.dy.sb + p.d;
+    constexpr int AHEAD = 4;                             // tokens loaded at a time
+    Pack<T, V> nx[AHEAD], ng[AHEAD];
     // x[k] and d[k]: of token t - (K - 1) + k
-    for (int64_t t = t0; t < t1 + past; ++t) {
+    for (int64_t s = t0; s < t1 + past; s += AHEAD) {
+        if (n > 0)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k) {
-                d[k][i] = d[k + 1][i];
+            for (int j = 0; j < AHEAD; ++j) {            // rows behind the last are the last again: not used
+                const int64_t t = min(s + j, n - 1);
+                nx[j] = *reinterpret_cast<const Pack<T, V>*>(xrow + t * a.x.st);
+                ng[j] = *reinterpret_cast<const Pack<T, V>*>(grow + t * a.dy.st);
             }
-            d[K - 1][i] = 0.0f;
-        }
-        token<T, V>(a, p.b, t, n, p.d, x[0]);
-        {
-            float fresh[V];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int64_t t = s + j;
+            if (t >= t1 + past) break;
+            const bool on = t < n;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                fresh[i] = x[0][i];
 #pragma unroll
-                for (int k = 0; k < K - 1; ++k) x[k][i] = x[k + 1][i];
-                x[K - 1][i] = fresh[i];
-            }
-        }
-        if (t < n) {
-            float dy[V];
-            load<T, V>(static_cast<const T*>(a.dy.p) + p.b * a.dy.sb + t * a.dy.st + p.d, dy);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float pre = bias[i];
+                for (int k = 0; k < K - 1; ++k) {
+                    d[k][i] = d[k + 1][i];
+                    x[k][i] = x[k + 1][i];
+                }
+                x[K - 1][i] = on ? to_f32(nx[j].v[i]) : 0.0f;
+                float pre = bias[i], g = on ? to_f32(ng[j].v[i]) : 0.0f;
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (k >= K - W) pre = fmaf(w[k][i], x[k][i], pre);
-                float g = dy[i];
+                    if (taps.at(k)) pre = fmaf(w[k][i], x[k][i], pre);
                 if (a.activation) {
-                    const float s = logistic(pre);
-                    g *= s * fmaf(pre, 1.0f - s, 1.0f);
+                    const float q = logistic(pre);
+                    g = on ? g * q * fmaf(pre, 1.0f - q, 1.0f) : 0.0f;
                 }
                 d[K - 1][i] = g;
-                if (t < t1) {
-                    db[i] += g;
+            }
+            if (t < t1)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    db[i] += d[K - 1][i];
 #pragma unroll
                     for (int k = 0; k < K; ++k)
-                        if (k >= K - W) dw[k][i] = fmaf(g, x[k][i], dw[k][i]);
+                        if (taps.at(k)) dw[k][i] = fmaf(d[K - 1][i], x[k][i], dw[k][i]);
                 }
+            const int64_t at = t - past;                 // W - 1 tokens back: d[K - W + q] is that of token at + q
+            if (at < t0 && !(p.run == 0 && a.d_initial_state)) continue;
+            float v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[i] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (taps.at(k)) v[i] = fmaf(w[k][i], d[K - 1 - (k - taps.first)][i], v[i]);
+                if (at >= n) v[i] = 0.0f;
             }
-        }
-        const int64_t at = t - past;                     // W - 1 tokens back: d[K - W + j] is that of token at + j
-        if (at < t0 && !(p.run == 0 && a.d_initial_state)) continue;
-        float v[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.0f;
-        if (at < n) {
-#pragma unroll
-            for (int j = 0; j < K; ++j)
-                if (j >= K - W)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) v[i] = fmaf(w[K - 1 - (j - (K - W))][i], d[j][i], v[i]);
-            if (a.d_final_state && at >= n - past) {
+            if (a.d_final_state && at < n && at >= n - past) {
                 float f[V];
                 load<T, V>(static_cast<const T*>(a.d_final_state) + (p.b * past + at - (n - past)) * a.D + p.d, f);
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[i] += f[i];
             }
+            if (at >= 0) store<T, V>(static_cast<T*>(a.dx) + (p.b * a.T + at) * a.D + p.d, v);
+            else store<T, V>(static_cast<T*>(a.d_initial_state) + (p.b * past + past + at) * a.D + p.d, v);
         }
-        if (at >= 0) store<T, V>(static_cast<T*>(a.dx) + (p.b * a.T + at) * a.D + p.d, v);
-        else store<T, V>(static_cast<T*>(a.d_initial_state) + (p.b * past + past + at) * a.D + p.d, v);
     }
-    float* q = part + (p.b * c.runs + p.run) * (W + 1) * a.D + p.d;
+    float* q = part + (p.b * c.runs + p.run) * (W + 1) * a.D;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (k >= K - W) q[static_cast<int64_t>(p.d + i) * (W - 1) + i + k - (K - W)] = dw[k][i];
-        q[static_cast<int64_t>(W) * a.D + i] = db[i];
+            if (taps.at(k)) q[(p.d + i) * a.W + k - taps.first] = dw[k][i];
+        q[a.W * a.D + p.d + i] = db[i];
     }
 }
 
@@ -280,28 +304,37 @@ bool aligned(int64_t D, int64_t elem, int V, int64_t strides, P... p) {
 }
 int64_t strides(const pn_tokens& x, int64_t B, int64_t T) { return (B > 1 ? x.sb : 0) | (T > 1 ? x.st : 0); }
 
-// Tokens of a thread: 64, or fewer while 2^18 threads (four waves for every
-// SIMD) are not reached.
-ConvCut cut(const pn_conv_args& a, int V) {
+// Tokens of a thread: 64, or down to `least` while 2^18 threads (four waves for
+// every SIMD) are not reached.
+ConvCut cut(const pn_conv_args& a, int V, int least) {
     ConvCut c;
     c.vecs = static_cast<int>(a.D / V);
     c.run = 64;
-    while (c.run > 8 && a.B * c.vecs * ((a.T + c.run - 1) / c.run) < (1 << 18)) c.run /= 2;
+    while (c.run > least && a.B * c.vecs * ((a.T + c.run - 1) / c.run) < (1 << 18)) c.run /= 2;
     c.runs = std::max<int64_t>(1, (a.T + c.run - 1) / c.run);
     return c;
 }
 
+// f(places for W taps): exact for 4, the usual number.
+template <typename F>
+hipError_t with_taps(int64_t W, F f) {
+    if (W == 4) return f(Taps<4, true>(W));
+    if (W < 4) return f(Taps<4, false>(W));
+    return f(Taps<8, false>(W));
+}
+
 template <typename T>
 hipError_t conv_typed(const pn_conv_args& a, hipStream_t st) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 8 / sizeof(T);
     const bool wide = aligned(a.D, sizeof(T), V, strides(a.x, a.B, a.T), a.x.p, a.initial_state, a.y, a.final_state);
-    const ConvCut c = cut(a, wide ? V : 1);
+    const ConvCut c = cut(a, wide ? V : 1, 8);
     const dim3 grid = grid_of((a.B * c.runs * c.vecs + kBlock - 1) / kBlock, kBlock);
-    if (wide && a.W <= 4) conv<T, V, 4><<<grid, kBlock, 0, st>>>(a, c);
-    else if (wide) conv<T, V, 8><<<grid, kBlock, 0, st>>>(a, c);
-    else if (a.W <= 4) conv<T, 1, 4><<<grid, kBlock, 0, st>>>(a, c);
-    else conv<T, 1, 8><<<grid, kBlock, 0, st>>>(a, c);
-    return hipGetLastError();
+    return with_taps(a.W, [&](auto taps) {
+        using P = decltype(taps);
+        if (wide) conv<T, V, P><<<grid, kBlock, 0, st>>>(a, c);
+        else conv<T, 1, P><<<grid, kBlock, 0, st>>>(a, c);
+        return hipGetLastError();
+    });
 }
 
 // The gradients' runs are those of single channels, so that the workspace
@@ -311,15 +344,16 @@ hipError_t backward_typed(const pn_conv_args& a, hipStream_t st) {
     constexpr int V = 8 / sizeof(T);
     const bool wide = aligned(a.D, sizeof(T), V, strides(a.x, a.B, a.T) | strides(a.dy, a.B, a.T), a.x.p, a.dy.p,
                               a.initial_state, a.d_final_state, a.dx, a.d_initial_state);
-    ConvCut c = cut(a, 1);
+    ConvCut c = cut(a, 1, 16);
     if (wide) c.vecs = static_cast<int>(a.D / V);
     const dim3 grid = grid_of((a.B * c.runs * c.vecs + kBlock - 1) / kBlock, kBlock);
     float* part = static_cast<float*>(a.workspace);
-    if (wide && a.W <= 4) conv_backward<T, V, 4><<<grid, kBlock, 0, st>>>(a, c, part);
-    else if (wide) conv_backward<T, V, 8><<<grid, kBlock, 0, st>>>(a, c, part);
-    else if (a.W <= 4) conv_backward<T, 1, 4><<<grid, kBlock, 0, st>>>(a, c, part);
-    else conv_backward<T, 1, 8><<<grid, kBlock, 0, st>>>(a, c, part);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = with_taps(a.W, [&](auto taps) {
+        using P = decltype(taps);
+        if (wide) conv_backward<T, V, P><<<grid, kBlock, 0, st>>>(a, c, part);
+        else conv_backward<T, 1, P><<<grid, kBlock, 0, st>>>(a, c, part);
+        return hipGetLastError();
+    });
     if (e != hipSuccess) return e;
     return launch_column_sum(ColumnSum{part, a.B * c.runs, (a.W + 1) * a.D, 2, {0, a.W * a.D}, {a.dweight, a.bias ? a.dbias : nullptr}}, st);
 }
@@ -346,7 +380,7 @@ hipError_t launch_conv(const pn_conv_args& a, hipStream_t st) {
 }
 
 size_t conv_workspace(const pn_conv_args& a) {
-    return sizeof(float) * static_cast<size_t>(a.B * cut(a, 1).runs) * static_cast<size_t>((a.W + 1) * a.D);
+    return sizeof(float) * static_cast<size_t>(a.B * cut(a, 1, 16).runs) * static_cast<size_t>((a.W + 1) * a.D);
 }
 
 hipError_t launch_conv_backward(const pn_conv_args& a, hipStream_t st) {

@@ -5,8 +5,8 @@
 
 #include <algorithm>
 
-#include "pn_seq_device.hpp"
 #include "pn_ssm.hpp"
+#include "pn_ssm_device.hpp"
 
 namespace pn {
 namespace {
@@ -55,8 +55,8 @@ __global__ __launch_bounds__(256) void bc_sum(pn_ssm_args a, SsmPlan p, const fl
     static_cast<T*>(which ? a.dc : a.db)[row * GN + gn] = from_f32<T>(v);
 }
 
-// L lanes per channel, NU units of V states each.
-template <typename T, int V, int NU>
+// L lanes per channel, NU units of V states each; b and c are read W at a time.
+template <typename T, int V, int NU, int W>
 __global__ __launch_bounds__(256) void ssm_step(pn_ssm_step_args a, int L) {
     const int64_t g = static_cast<int64_t>(block_id()) * (256 / L) + threadIdx.x / L;
     const int lane = threadIdx.x & (L - 1);
@@ -85,16 +85,16 @@ __global__ __launch_bounds__(256) void ssm_step(pn_ssm_step_args a, int L) {
             h[u] = *reinterpret_cast<const Pack<float, V>*>(hp + n);
             A[u] = *reinterpret_cast<const Pack<float, V>*>(Ap + n);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                bv[u].v[i] = bp[n + i];
-                cv[u].v[i] = cp[n + i];
+            for (int i = 0; i < V / W; ++i) {
+                *reinterpret_cast<Pack<T, W>*>(bv[u].v + i * W) = *reinterpret_cast<const Pack<T, W>*>(bp + n + i * W);
+                *reinterpret_cast<Pack<T, W>*>(cv[u].v + i * W) = *reinterpret_cast<const Pack<T, W>*>(cp + n + i * W);
             }
         }
     }
     const float x = to_f32(static_cast<const T*>(a.x.p)[b * a.x.sb + d]);
     const float raw = to_f32(static_cast<const T*>(a.dt.p)[b * a.dt.sb + d]) + (a.dt_bias ? a.dt_bias[d] : 0.0f);
-    float delta = raw;
-    if (a.softplus) delta = fmaxf(raw, 0.0f) + log1pf(expf(-fabsf(raw)));
+    float slope;
+    const float delta = a.softplus ? softplus(raw, &slope) : raw;
     const float ux = delta * x;
     float acc = 0.0f;
 #pragma unroll
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256) void ssm_step(pn_ssm_step_args a, int L) {
         const int n = (lane + u * L) * V;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            h[u].v[i] = fmaf(expf(delta * A[u].v[i]), h[u].v[i], ux * to_f32(bv[u].v[i]));
+            h[u].v[i] = fmaf(__builtin_amdgcn_exp2f(delta * kLog2e * A[u].v[i]), h[u].v[i], ux * to_f32(bv[u].v[i]));
             acc = fmaf(to_f32(cv[u].v[i]), h[u].v[i], acc);
         }
         if (n < N) *reinterpret_cast<Pack<float, V>*>(hp + n) = h[u];
@@ -112,7 +112,7 @@ __global__ __launch_bounds__(256) void ssm_step(pn_ssm_step_args a, int L) {
     if (a.skip) acc = fmaf(a.skip[d], x, acc);
     if (a.gate.p) {
         const float z = to_f32(static_cast<const T*>(a.gate.p)[b * a.gate.sb + d]);
-        acc *= z / (1.0f + expf(-z));
+        acc *= z * logistic(z);
     }
     *y = from_f32<T>(acc);
 }
@@ -125,9 +125,12 @@ hipError_t step_typed(const pn_ssm_step_args& a, hipStream_t st) {
     while (L < units && L < 64) L *= 2;
     const int64_t per = 256 / L;
     const dim3 grid = grid_of((a.B * a.D + per - 1) / per, 256);
-    if (wide) ssm_step<T, 4, 1><<<grid, 256, 0, st>>>(a, L);
-    else if (units <= 64) ssm_step<T, 1, 1><<<grid, 256, 0, st>>>(a, L);
-    else ssm_step<T, 1, 2><<<grid, 256, 0, st>>>(a, L);
+    const int64_t bc = reinterpret_cast<intptr_t>(a.b.p) | reinterpret_cast<intptr_t>(a.c.p) |
+                       ((a.B > 1 ? a.b.sb | a.c.sb : 0) | (a.G > 1 ? a.b.sh | a.c.sh : 0)) * static_cast<int64_t>(sizeof(T));
+    if (wide && bc % (4 * sizeof(T)) == 0) ssm_step<T, 4, 1, 4><<<grid, 256, 0, st>>>(a, L);
+    else if (wide) ssm_step<T, 4, 1, 1><<<grid, 256, 0, st>>>(a, L);
+    else if (units <= 64) ssm_step<T, 1, 1, 1><<<grid, 256, 0, st>>>(a, L);
+    else ssm_step<T, 1, 2, 1><<<grid, 256, 0, st>>>(a, L);
     return hipGetLastError();
 }
 

@@ -10,10 +10,10 @@
 // the 4 S states of the quad's two channels, in registers over all tokens.
 // What belongs to a channel and not to a state (step, gate, products with x)
 // is computed once, by the lane of the channel (bit 0 of its number in the
-// quad) and of the token's parity (bit 1); such values pass on through
-// LDS, and sums over its four lanes go back by DPP to the lane they belong to.  More
-// than 16 states are blocks of 16 in as many waves, which add their shares of
-// such sums through LDS.
+// quad) and of the token's parity (bit 1); such values pass to the quad
+// through LDS, and sums over its four lanes go back by DPP to the lane they
+// belong to.  More than 16 states are blocks of 16 in as many waves, which add
+// their shares of such sums through LDS.
 //
 // Bound: instructions.  A state and token take an exponential (9 cycles of a
 // SIMD, which does nothing else meanwhile) and 3 to 4 products and sums (2.5
@@ -31,13 +31,11 @@
 // each once forward from its mark with e kept in registers, once back.
 #pragma once
 
-#include "pn_seq_device.hpp"
 #include "pn_ssm.hpp"
+#include "pn_ssm_device.hpp"
 
 namespace pn {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A value of the quad's lane K in all four lanes.
 template <int K>
@@ -65,21 +63,6 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
-
-// Keeps a value's computation where it stands: before a select, not in a branch made of it.
-__device__ __forceinline__ float pinned(float v) {
-    asm("" : "+v"(v));
-    return v;
-}
-
-// log(1 + e^v) = max(v, 0) + log(1 + t), t = e^-|v|; log(1 + t) as log(w) +
-// (t - (w - 1)) / w, w = 1 + t as rounded, which leaves 2^-48 of its rounding.
-__device__ __forceinline__ float softplus(float v, float* slope) {
-    const float t = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e), w = 1.0f + t, r = __builtin_amdgcn_rcpf(w);
-    *slope = (v >= 0.0f ? 1.0f : t) * r;
-    return fmaxf(v, 0.0f) + fmaf(__builtin_amdgcn_logf(w), kLn2, (t - (w - 1.0f)) * r);
-}
-__device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e)); }
 
 constexpr int kChans = 32;               // channels of a wave
 constexpr int kOwn = kSsmTile / 2;       // tokens of a tile that belong to a lane: 2 m + its parity
@@ -273,10 +256,12 @@ __device__ __forceinline__ float joined(const float* ex, int blocks, int m, int 
     return v;
 }
 
-template <typename T, int S, bool MULTI, int PASS>
-__global__ __launch_bounds__(MULTI ? 512 : 64) __attribute__((amdgpu_waves_per_eu(MULTI ? 2 : PASS == kSsmMarksBoth ? 3 : 4)))
+// BLOCKS: the most waves that share the states of a channel.
+template <typename T, int S, int BLOCKS, int PASS>
+__global__ __launch_bounds__(64 * BLOCKS) __attribute__((amdgpu_waves_per_eu(4)))
 void ssm_pass(pn_ssm_args a, SsmPlan p) {
-    constexpr int E = 4 * S, WAVES = MULTI ? 8 : 1;
+    constexpr int E = 4 * S, WAVES = BLOCKS;
+    constexpr bool MULTI = BLOCKS > 1;
     constexpr bool OUT = PASS == kSsmOutputs, MARKS = PASS == kSsmMarks || PASS == kSsmMarksBoth, BACK = PASS == kSsmMarksBoth;
     __shared__ __align__(16) float bc_lds[WAVES][kSsmTile * 2 * E];
     __shared__ __align__(16) float du_lds[WAVES][kSsmTile * kChans * 2], g_lds[BACK ? WAVES : 1][BACK ? kSsmTile * kChans : 2];
@@ -454,19 +439,17 @@ struct ChannelSum {
     }
 };
 
-constexpr int kTurn = 4;                 // tiles whose shares of db and dc wait in LDS
-
 // The waves of a workgroup: blocks of states (MULTI), or adjacent channel
-// blocks, whose shares of db and dc are added in LDS before they are written,
-// every kTurn tiles so that the waves need not keep step.
-template <typename T, int S, bool MULTI>
-__global__ __launch_bounds__(MULTI ? 512 : 256) __attribute__((amdgpu_waves_per_eu(2)))
+// blocks, whose shares of db and dc are added in LDS before they are written.
+template <typename T, int S, int BLOCKS>
+__global__ __launch_bounds__(BLOCKS > 1 ? 64 * BLOCKS : 256) __attribute__((amdgpu_waves_per_eu(2)))
 void ssm_gradients(pn_ssm_args a, SsmPlan p) {
-    constexpr int E = 4 * S, WAVES = MULTI ? 8 : 4;
+    constexpr int E = 4 * S, WAVES = BLOCKS > 1 ? BLOCKS : 4;
+    constexpr bool MULTI = BLOCKS > 1;
     __shared__ __align__(16) float bc_lds[WAVES][kSsmTile * 2 * E];
     __shared__ __align__(16) float du_lds[WAVES][kSsmTile * kChans * 2], g_lds[WAVES][kSsmTile * kChans];
     __shared__ float ex[3][MULTI ? WAVES * kOwn * 64 : 1];
-    __shared__ float shares[2][MULTI ? 1 : kTurn][MULTI ? 1 : WAVES][MULTI ? 1 : kSsmTile * 2 * E];
+    __shared__ float shares[2][MULTI ? 1 : WAVES][MULTI ? 1 : kSsmTile * 2 * E];
     __shared__ __align__(16) float in_lds[WAVES][128 * S];
     const SsmWave<T, S, !MULTI> w(a, p);
     if (w.seg >= p.n_seg) return;
@@ -508,9 +491,12 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
             ddp[o] = from_f32<T>(0.0f);
             if (gated) dzp[o] = from_f32<T>(0.0f);
         }
-    int turn = 0;                                        // tiles done
+    int turn = 0;
     T x[kOwn], dt[kOwn], z[kOwn], gy[kOwn], bv[w.M], cv[w.M];
+    float mark[2][S], since = 0.0f;
     auto load = [&](int64_t t0) {
+        w.get(w.at(ws + p.marks, t0 / kSsmTile), mark);
+        since = w.seg > 0 ? ws[p.since + w.own_at(t0 / kSsmTile)] : 0.0f;
         w.load_rows(a.x, t0, x);
         w.load_rows(a.dt, t0, dt);
         if (gated) w.load_rows(a.gate, t0, z);
@@ -522,10 +508,8 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
     if (w.begin < w.end) load(last);
     for (int64_t t0 = last; w.begin < w.end && t0 >= w.begin; t0 -= kSsmTile) {
         const int left = w.left(t0) - w.odd;             // the lane's token m exists if 2 m < left
-        float dl[kOwn], xs[kOwn], g[kOwn], slope[kOwn], dz[kOwn], e[kSsmTile][2][S], h[2][S], mark[2][S];
-        w.get(w.at(ws + p.marks, t0 / kSsmTile), mark);
+        float dl[kOwn], xs[kOwn], g[kOwn], slope[kOwn], dz[kOwn], e[kSsmTile][2][S], h[2][S];
         wave_sync();                                     // the last tile's have been read
-        const float since = w.seg > 0 ? ws[p.since + w.own_at(t0 / kSsmTile)] : 0.0f;
 #pragma unroll
         for (int m = 0; m < kOwn; ++m) {
             const bool on = 2 * m < left, mine = on && w.own;
@@ -558,7 +542,7 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
         const __amdgpu_buffer_rsrc_t dz_rows = w.rows_of(a.dgate, t0);
 #pragma unroll
         for (int m = 0; m < kOwn; ++m) {
-            __builtin_amdgcn_sched_barrier(0);               // a pair of tokens at a time: registers
+
             float part[4];
 #pragma unroll
             for (int par = 0; par < 2; ++par) {
@@ -587,7 +571,7 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
         }
 #pragma unroll
         for (int m = kOwn - 1; m >= 0; --m) {
-            __builtin_amdgcn_sched_barrier(0);
+
             float s1[4], s2[4];
 #pragma unroll
             for (int par = 1; par >= 0; --par) {
@@ -623,7 +607,7 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
                 if (MULTI) {
                     if (bc_on && t0 + i < w.end) bc_out[(t0 + i) * 2 * NP + bc_at] = sum;
                 } else if (bc_on) {
-                    shares[turn / kTurn & 1][turn % kTurn][wave][i * 2 * E + bc_at] = sum;
+                    shares[turn][wave][i * 2 * E + bc_at] = sum;
                 }
             }
             const float du = quad_sum(s1, w.j), dd = quad_sum(s2, w.j) * kLn2;
@@ -654,18 +638,13 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
                 }
             __syncthreads();
         } else {
-            if (turn % kTurn == kTurn - 1 || t0 == w.begin) {
-                __syncthreads();                         // the other half of shares is free since the last
-                const int tiles = turn % kTurn + 1;
-                for (int i = threadIdx.x; i < tiles * kSsmTile * 2 * E; i += 64 * p.wide) {
-                    const int n = i / (kSsmTile * 2 * E), at = i % (kSsmTile * 2 * E);
-                    float v = 0.0f;
-                    for (int q = 0; q < p.wide; ++q) v += shares[turn / kTurn & 1][n][q][at];
-                    const int64_t from = t0 + (tiles - 1 - n) * kSsmTile;
-                    if (at < (w.end - from) * 2 * E) bc_out[from * 2 * E + at] = v;
-                }
+            __syncthreads();                             // the other half of shares is free since the last
+            for (int i = threadIdx.x; i < kSsmTile * 2 * E; i += 64 * p.wide) {
+                float v = 0.0f;
+                for (int q = 0; q < p.wide; ++q) v += shares[turn][q][i];
+                if (i < (w.end - t0) * 2 * E) bc_out[t0 * 2 * E + i] = v;
             }
-            ++turn;
+            turn ^= 1;
         }
     }
     // the two parities of a channel
@@ -682,17 +661,18 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
         w.states([&](int k, int s, int64_t i) { a.d_initial_state[w.b * a.D * a.N + i] = r[k][s]; });
 }
 
-template <typename T, int S, bool MULTI>
+template <typename T, int S, int BLOCKS>
 hipError_t ssm_launch(const pn_ssm_args& a, const SsmPlan& p, SsmPass pass, hipStream_t st) {
-    const int threads = MULTI ? 64 * p.blocks : pass == kSsmGradients ? 64 * p.wide : 64;
+    const bool wide = BLOCKS == 1 && pass == kSsmGradients;
+    const int threads = 64 * (wide ? p.wide : p.blocks);
     const int64_t segs = pass == kSsmEnds ? p.n_seg - 1 : p.n_seg;
-    const dim3 grid = grid_of(segs * a.B * (pass == kSsmGradients && !MULTI ? p.chans / p.wide : p.chans), threads);
+    const dim3 grid = grid_of(segs * a.B * (wide ? p.chans / p.wide : p.chans), threads);
     switch (pass) {
-        case kSsmEnds: ssm_pass<T, S, MULTI, kSsmEnds><<<grid, threads, 0, st>>>(a, p); break;
-        case kSsmOutputs: ssm_pass<T, S, MULTI, kSsmOutputs><<<grid, threads, 0, st>>>(a, p); break;
-        case kSsmMarks: ssm_pass<T, S, MULTI, kSsmMarks><<<grid, threads, 0, st>>>(a, p); break;
-        case kSsmMarksBoth: ssm_pass<T, S, MULTI, kSsmMarksBoth><<<grid, threads, 0, st>>>(a, p); break;
-        default: ssm_gradients<T, S, MULTI><<<grid, threads, 0, st>>>(a, p); break;
+        case kSsmEnds: ssm_pass<T, S, BLOCKS, kSsmEnds><<<grid, threads, 0, st>>>(a, p); break;
+        case kSsmOutputs: ssm_pass<T, S, BLOCKS, kSsmOutputs><<<grid, threads, 0, st>>>(a, p); break;
+        case kSsmMarks: ssm_pass<T, S, BLOCKS, kSsmMarks><<<grid, threads, 0, st>>>(a, p); break;
+        case kSsmMarksBoth: ssm_pass<T, S, BLOCKS, kSsmMarksBoth><<<grid, threads, 0, st>>>(a, p); break;
+        default: ssm_gradients<T, S, BLOCKS><<<grid, threads, 0, st>>>(a, p); break;
     }
     return hipGetLastError();
 }
@@ -701,10 +681,12 @@ hipError_t ssm_launch(const pn_ssm_args& a, const SsmPlan& p, SsmPass pass, hipS
 
 template <typename T>
 hipError_t launch_ssm_pass(const pn_ssm_args& a, const SsmPlan& p, SsmPass pass, hipStream_t st) {
-    if (p.blocks > 1) return ssm_launch<T, 4, true>(a, p, pass, st);
-    if (p.states == 4) return ssm_launch<T, 1, false>(a, p, pass, st);
-    if (p.states == 8) return ssm_launch<T, 2, false>(a, p, pass, st);
-    return ssm_launch<T, 4, false>(a, p, pass, st);
+    if (p.blocks > 4) return ssm_launch<T, 4, 8>(a, p, pass, st);
+    if (p.blocks > 2) return ssm_launch<T, 4, 4>(a, p, pass, st);
+    if (p.blocks > 1) return ssm_launch<T, 4, 2>(a, p, pass, st);
+    if (p.states == 4) return ssm_launch<T, 1, 1>(a, p, pass, st);
+    if (p.states == 8) return ssm_launch<T, 2, 1>(a, p, pass, st);
+    return ssm_launch<T, 4, 1>(a, p, pass, st);
 }
 
 }  // namespace pn
