@@ -559,7 +559,7 @@ typedef struct pn_ssm_step_args {
 
 int pn_ssm_step(const pn_ssm_step_args* a);
 
-/* The norms around a block.  For each token of D (1 .. 16384) channels,
+/* The norms around a block.  For each token of D (1 .. 8192) channels,
  *     u = x * gate / (1 + e^-gate)                 (x without a gate),
  *     p = post_weight * u / sqrt(mean u^2 + eps)   (u without post_weight),
  *     s = residual + scale * p                     (scale NULL: 1; residual.p NULL: 0),

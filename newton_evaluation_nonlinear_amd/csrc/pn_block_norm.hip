@@ -139,7 +139,7 @@ __global__ __launch_bounds__(THREADS) void block_norm(pn_block_norm_args a) {
 // A workgroup takes `rows` rows one after the other; each lane keeps the sums
 // of its channels' weight gradients, which go to part[workgroup][3][D].
 template <typename T, typename R, int V, int NU, int THREADS>
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(4)))
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(THREADS > 256 ? 4 : 3)))
 void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float* part) {
     __shared__ float lds[2 * (THREADS / 64)];
     const int64_t wg = block_id();
@@ -256,18 +256,20 @@ int widest(const pn_block_norm_args& a, bool backward) {
 }
 
 // f(form) for rows of D channels, V at a time: the fewest waves that hold a
-// row in 8 values a lane (16 past 8192).  More values would take the registers
-// of the waves that hide each other's waits: 2050 channels in pairs, float32
-// residual, gradients of 8188 rows: 217 us with 16, see the head for 8.
+// row in 8 values a lane, or a few more in units of one or two channels, where
+// rows just past 2048 would leave half of twice the waves idle.  With 16
+// values the gradients take the registers of the waves that hide each other's
+// waits (2050 channels in pairs, float32 residual, 8188 rows: 217 us).
 template <int V, typename F>
 hipError_t with_threads(int64_t D, F f) {
     constexpr int NU = 8 / V;
     if (D <= 512) return f(Form<V, NU, 64>{});
     if (D <= 1024) return f(Form<V, NU, 128>{});
     if (D <= 2048) return f(Form<V, NU, 256>{});
+    if constexpr (V <= 2)
+        if (D <= 2560) return f(Form<V, 10 / V, 256>{});
     if (D <= 4096) return f(Form<V, NU, 512>{});
-    if (D <= 8192) return f(Form<V, NU, 1024>{});
-    return f(Form<V, 2 * NU, 1024>{});
+    return f(Form<V, NU, 1024>{});
 }
 
 template <typename T, typename R, typename F>
@@ -288,11 +290,13 @@ hipError_t forward_typed(const pn_block_norm_args& a, hipStream_t st) {
     });
 }
 
-// Rows of a workgroup of the gradients: four workgroups of four waves for
-// every unit, whose shares of the weights' gradients are then few.
+// Rows of a workgroup of the gradients: as many workgroups as run at once (12
+// waves a unit in workgroups of up to four waves, 16 in larger ones), so that
+// none is left for a second round.
 void backward_split(const pn_block_norm_args& a, int64_t* rows, int64_t* n_wg) {
     const int64_t n = a.B * a.T;
-    *rows = std::max<int64_t>(1, (n + 1023) / 1024);
+    const int64_t at_once = a.D <= 512 ? 3072 : a.D <= 1024 ? 1536 : a.D <= 2560 ? 768 : a.D <= 4096 ? 512 : 256;
+    *rows = std::max<int64_t>(1, (n + at_once - 1) / at_once);
     *n_wg = (n + *rows - 1) / *rows;
 }
 

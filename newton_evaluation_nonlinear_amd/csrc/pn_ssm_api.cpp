@@ -177,7 +177,7 @@ int check_norm_sizes(const pn_block_norm_args& a) {
     PN_TRY(check_types(a.dtype, a.B, a.T, a.D));
     if (a.residual_dtype != PN_F32 && a.residual_dtype != a.dtype)
         return fail(PN_EINVAL, "the residual has the storage type or float32");
-    if (a.D < 1 || a.D > 16384) return fail(PN_EUNSUPPORTED, "1 .. 16384 channels are supported");
+    if (a.D < 1 || a.D > 8192) return fail(PN_EUNSUPPORTED, "1 .. 8192 channels are supported");
     if (!(a.eps >= 0.0 && std::isfinite(a.eps))) return fail(PN_EINVAL, "eps must be finite and >= 0");
     return PN_OK;
 }

@@ -502,7 +502,7 @@ def test_norm_many_rows(dtype, rdtype, D):
 
 @pytest.mark.parametrize("dtype, rdtype", [("f32", "f32"), ("bf16", "f32")])
 def test_norm_widest(dtype, rdtype):
-    for D in (8200, 12345, 16384):
+    for D in (2049, 2560, 2561, 2562, 4097, 5000, 8191):
         check_norm(norm_inputs(dtype, rdtype, (1, 3), D), dtype, rdtype)
 
 

@@ -248,7 +248,7 @@ def _norm(dtype=1, rdtype=0, B=2, T=2, D=8, eps=1e-6, w=3 * GIB, pw=4 * GIB, sc=
 
 @pytest.mark.parametrize("kw, code", [
     (dict(dtype=3), pn.EINVAL), (dict(rdtype=2), pn.EINVAL), (dict(B=-1), pn.EINVAL), (dict(D=0), pn.EUNSUPPORTED),
-    (dict(D=16385), pn.EUNSUPPORTED), (dict(eps=-1.0), pn.EINVAL), (dict(eps=float("nan")), pn.EINVAL), (dict(w=3 * GIB + 2), pn.EINVAL),
+    (dict(D=8193), pn.EUNSUPPORTED), (dict(eps=-1.0), pn.EINVAL), (dict(eps=float("nan")), pn.EINVAL), (dict(w=3 * GIB + 2), pn.EINVAL),
     (dict(x=TOK(0)), pn.EINVAL), (dict(z=(7 * GIB + 1, 64, 32, 0)), pn.EINVAL), (dict(x=TOK(6, st=-8)), pn.EINVAL)])
 def test_norm_refusals(kw, code):
     need = pn.lib().pn_block_norm_workspace_bytes(_norm())
