@@ -3,8 +3,8 @@
 // ru = (mean u^2 + eps)^{-1/2} and rs likewise of s; and the gradients, with
 // n = u ru, m = s rs and t the gradient of s as a whole,
 //     e = w dy,  t = ds + rs (e - m mean(e m)),  dresidual = t,  dw = sum dy m,
-//     q = pw scale t,  du = ru (q - n mean(q n)),  dpw = sum scale t n,
-//     dscale = sum t p,  dx = du silu(gate),  dgate = du x silu'(gate).
+//     q = pw scale t,  du = ru (q - n mean(q n)),  dpw = scale sum t n,
+//     dscale = pw sum t n,  dx = du silu(gate),  dgate = du x silu'(gate).
 //
 // Bound: bytes.  A row stays in the registers of the lanes that hold it, NU
 // units of V channels each, so everything is read once and written once; sums
@@ -51,15 +51,24 @@ struct Row {
     int D;
     __device__ __forceinline__ int at(int u) const { return (static_cast<int>(threadIdx.x) + u * THREADS) * V; }
     __device__ __forceinline__ bool on(int u) const { return at(u) < D; }     // V divides D
+    // A row as it is stored, so that it can be on its way while another is worked on.
     template <typename T>
-    __device__ __forceinline__ void load(const T* row, float (*v)[V]) const {
+    __device__ __forceinline__ void fetch(const T* row, Pack<T, V>* q) const {
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            Pack<T, V> q{};
-            if (on(u)) q = *reinterpret_cast<const Pack<T, V>*>(row + at(u));
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[u][i] = to_f32(q.v[i]);
+            q[u] = Pack<T, V>{};
+            if (on(u)) q[u] = *reinterpret_cast<const Pack<T, V>*>(row + at(u));
         }
+    }
+    template <typename T>
+    __device__ __forceinline__ static void widen(const Pack<T, V>* q, float (*v)[V]) {
+        each([&](int u, int i) { v[u][i] = to_f32(q[u].v[i]); });
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(const T* row, float (*v)[V]) const {
+        Pack<T, V> q[NU];
+        fetch(row, q);
+        widen(q, v);
     }
     template <typename T>
     __device__ __forceinline__ void store(T* row, const float (*v)[V]) const {
@@ -137,81 +146,127 @@ __global__ __launch_bounds__(THREADS) void block_norm(pn_block_norm_args a) {
 }
 
 // A workgroup takes `rows` rows one after the other; each lane keeps the sums
-// of its channels' weight gradients, which go to part[workgroup][3][D].
+// of its channels' weight gradients, which go to part[workgroup][3][D].  The
+// weights wait in LDS, so that the next row can be on its way in registers
+// (not beside 16 values a lane).
 template <typename T, typename R, int V, int NU, int THREADS>
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(THREADS > 256 ? 4 : 3)))
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(THREADS > 256 || V * NU > 8 ? 2 : 3)))
 void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float* part) {
     __shared__ float lds[2 * (THREADS / 64)];
+    extern __shared__ __align__(32) float weights[];     // [3][D]: weight, post_weight, scale
     const int64_t wg = block_id();
     if (wg >= n_wg) return;
     const Row<V, NU, THREADS> r{static_cast<int>(a.D)};
     const float eps = static_cast<float>(a.eps), inv = 1.0f / static_cast<float>(a.D);
-    float w[NU][V], pw[NU][V], sc[NU][V], dw[NU][V], dpw[NU][V], dsc[NU][V];
-    r.each([&](int u, int i) {
-        dw[u][i] = dpw[u][i] = dsc[u][i] = 0.0f;
-        w[u][i] = pw[u][i] = sc[u][i] = 1.0f;
-    });
-    if (a.weight) r.load(a.weight, w);
-    if (a.post_weight) r.load(a.post_weight, pw);
-    if (a.scale) r.load(a.scale, sc);
-    const int64_t end = min((wg + 1) * rows, a.B * a.T);
-    for (int64_t row = wg * rows; row < end; ++row) {
+    float dw[NU][V], tn[NU][V];                          // sums of dy m and of t n (t u without post_weight)
+    {
+        float v[NU][V];                                  // a lane reads what it wrote itself
+        r.each([&](int u, int i) {
+            dw[u][i] = tn[u][i] = 0.0f;
+            v[u][i] = 1.0f;
+        });
+        if (a.weight) r.load(a.weight, v);
+        r.store(weights, v);
+        r.each([&](int u, int i) { v[u][i] = 1.0f; });
+        if (a.scale) r.load(a.scale, v);
+        r.store(weights + 2 * a.D, v);
+        if (a.post_weight) {
+            float w[NU][V];
+            r.load(a.post_weight, w);
+            r.store(weights + a.D, w);
+        }
+    }
+    const bool need = a.gate.p || a.post_weight || a.scale;
+    Pack<T, V> px[NU] = {}, pg[NU] = {}, pe[NU] = {};
+    Pack<R, V> ps[NU] = {}, pt[NU] = {};
+    auto fetch_first = [&](int64_t row) {
         const int64_t b = row / a.T, tok = row - b * a.T;
-        const bool need = a.gate.p || a.post_weight || a.scale;
-        float t[NU][V], x[NU][V], g[NU][V];
-        if (need) r.load(row_of<T>(a.x, b, tok), x);
-        if (a.gate.p) r.load(row_of<T>(a.gate, b, tok), g);
-        if (a.ds.p) {
-            r.load(row_of<R>(a.ds, b, tok), t);
+        if (a.weight) {
+            r.fetch(row_of<R>(a.s_in, b, tok), ps);
+            r.fetch(row_of<T>(a.dy, b, tok), pe);
+        }
+        if (a.ds.p) r.fetch(row_of<R>(a.ds, b, tok), pt);
+    };
+    auto fetch_last = [&](int64_t row) {
+        const int64_t b = row / a.T, tok = row - b * a.T;
+        if (need) r.fetch(row_of<T>(a.x, b, tok), px);
+        if (a.gate.p) r.fetch(row_of<T>(a.gate, b, tok), pg);
+    };
+    const int64_t end = min((wg + 1) * rows, a.B * a.T);
+    constexpr bool AHEAD = V * NU < 16;
+    if (AHEAD) {
+        fetch_first(wg * rows);
+        fetch_last(wg * rows);
+    }
+    for (int64_t row = wg * rows; row < end; ++row) {
+        float t[NU][V], x[NU][V], g[NU][V], s[NU][V], e[NU][V], w[NU][V];
+        if (!AHEAD) fetch_first(row);
+        r.widen(pt, t);
+        r.widen(ps, s);
+        r.widen(pe, e);
+        if (AHEAD) {
+            r.widen(px, x);
+            r.widen(pg, g);
+            if (row + 1 < end) {
+                fetch_first(row + 1);
+                fetch_last(row + 1);
+            }
         } else {
-            r.each([&](int u, int i) { t[u][i] = 0.0f; });
+            fetch_last(row);
         }
         if (a.weight) {
-            float s[NU][V], e[NU][V], ss = 0.0f, es = 0.0f;
-            r.load(row_of<R>(a.s_in, b, tok), s);
-            r.load(row_of<T>(a.dy, b, tok), e);
+            float ss = 0.0f, es = 0.0f;
+            r.load(weights, w);
             r.each([&](int u, int i) {
+                w[u][i] *= e[u][i];
                 ss = fmaf(s[u][i], s[u][i], ss);
-                es = fmaf(e[u][i] * w[u][i], s[u][i], es);
+                es = fmaf(w[u][i], s[u][i], es);
             });
             row_sums<THREADS>(ss, es, lds);
             const float rs = 1.0f / sqrtf(fmaf(ss, inv, eps)), mean = es * rs * inv;
             r.each([&](int u, int i) {
                 const float m = s[u][i] * rs;
                 dw[u][i] = fmaf(e[u][i], m, dw[u][i]);
-                t[u][i] = fmaf(rs, fmaf(-m, mean, e[u][i] * w[u][i]), t[u][i]);
+                t[u][i] = fmaf(rs, fmaf(-m, mean, w[u][i]), t[u][i]);
             });
         }
         if (a.dresidual) r.store(static_cast<R*>(a.dresidual) + row * a.D, t);
-        float act[NU][V];
-        r.each([&](int u, int i) { act[u][i] = a.gate.p ? logistic(g[u][i]) : 1.0f; });
-        auto silu = [&](int u, int i) { return a.gate.p ? g[u][i] * act[u][i] : 1.0f; };
+        if (!AHEAD) {
+            r.widen(px, x);
+            r.widen(pg, g);
+        }
+        // from here on e: the gate's sigmoid, s: u (x without a gate)
+        r.each([&](int u, int i) {
+            e[u][i] = a.gate.p ? logistic(g[u][i]) : 1.0f;
+            s[u][i] = a.gate.p ? x[u][i] * g[u][i] * e[u][i] : x[u][i];
+        });
         if (a.post_weight) {
-            float uu = 0.0f, qu = 0.0f;
+            float uu = 0.0f, qu = 0.0f, sc[NU][V];
+            r.load(weights + a.D, w);
+            r.load(weights + 2 * a.D, sc);
             r.each([&](int u, int i) {
-                const float v = x[u][i] * silu(u, i);
-                uu = fmaf(v, v, uu);
-                qu = fmaf(pw[u][i] * sc[u][i] * t[u][i], v, qu);
+                uu = fmaf(s[u][i], s[u][i], uu);
+                qu = fmaf(w[u][i] * sc[u][i] * t[u][i], s[u][i], qu);
             });
             row_sums<THREADS>(uu, qu, lds);
             const float ru = 1.0f / sqrtf(fmaf(uu, inv, eps)), mean = qu * ru * inv;
             r.each([&](int u, int i) {
-                const float n = x[u][i] * silu(u, i) * ru, tn = t[u][i] * n;
-                dpw[u][i] = fmaf(sc[u][i], tn, dpw[u][i]);
-                dsc[u][i] = fmaf(pw[u][i], tn, dsc[u][i]);
-                t[u][i] = ru * fmaf(-n, mean, pw[u][i] * sc[u][i] * t[u][i]);
+                const float n = s[u][i] * ru;
+                tn[u][i] = fmaf(t[u][i], n, tn[u][i]);
+                t[u][i] = ru * fmaf(-n, mean, w[u][i] * sc[u][i] * t[u][i]);
             });
         } else if (a.scale) {
+            r.load(weights + 2 * a.D, w);
             r.each([&](int u, int i) {
-                dsc[u][i] = fmaf(t[u][i], x[u][i] * silu(u, i), dsc[u][i]);
-                t[u][i] *= sc[u][i];
+                tn[u][i] = fmaf(t[u][i], s[u][i], tn[u][i]);
+                t[u][i] *= w[u][i];
             });
         }
         if (a.gate.p) {
             r.each([&](int u, int i) {                   // x: dgate, t: dx
-                const float du = t[u][i], s = act[u][i];
-                x[u][i] = du * x[u][i] * s * fmaf(g[u][i], 1.0f - s, 1.0f);
-                t[u][i] = du * g[u][i] * s;
+                const float du = t[u][i], p = e[u][i];
+                x[u][i] = du * x[u][i] * p * fmaf(g[u][i], 1.0f - p, 1.0f);
+                t[u][i] = du * g[u][i] * p;
             });
             r.store(static_cast<T*>(a.dgate) + row * a.D, x);
         }
@@ -219,8 +274,18 @@ void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float
     }
     float* q = part + wg * 3 * a.D;
     if (a.weight) r.store(q, dw);
-    if (a.post_weight) r.store(q + a.D, dpw);
-    if (a.scale) r.store(q + 2 * a.D, dsc);
+    float v[NU][V];
+    if (a.post_weight) {                                 // dpw = scale sum t n
+        r.load(weights + 2 * a.D, v);
+        r.each([&](int u, int i) { v[u][i] *= tn[u][i]; });
+        r.store(q + a.D, v);
+    }
+    if (a.scale) {                                       // dscale = pw sum t n
+        r.each([&](int u, int i) { v[u][i] = 1.0f; });
+        if (a.post_weight) r.load(weights + a.D, v);
+        r.each([&](int u, int i) { v[u][i] *= tn[u][i]; });
+        r.store(q + 2 * a.D, v);
+    }
 }
 
 // ---------------------------------------------------------------- choice of the form
@@ -256,10 +321,10 @@ int widest(const pn_block_norm_args& a, bool backward) {
 }
 
 // f(form) for rows of D channels, V at a time: the fewest waves that hold a
-// row in 8 values a lane, or a few more in units of one or two channels, where
-// rows just past 2048 would leave half of twice the waves idle.  With 16
-// values the gradients take the registers of the waves that hide each other's
-// waits (2050 channels in pairs, float32 residual, 8188 rows: 217 us).
+// row in 8 values a lane (16 past 4096 channels), or a few more in units of one
+// or two channels, where rows just past 2048 would leave half of twice the
+// waves idle.  With 16 values the gradients have no registers for the next row
+// (2050 channels in pairs, float32 residual, 8188 rows: 217 us).
 template <int V, typename F>
 hipError_t with_threads(int64_t D, F f) {
     constexpr int NU = 8 / V;
@@ -269,7 +334,7 @@ hipError_t with_threads(int64_t D, F f) {
     if constexpr (V <= 2)
         if (D <= 2560) return f(Form<V, 10 / V, 256>{});
     if (D <= 4096) return f(Form<V, NU, 512>{});
-    return f(Form<V, NU, 1024>{});
+    return f(Form<V, 2 * NU, 512>{});
 }
 
 template <typename T, typename R, typename F>
@@ -291,11 +356,11 @@ hipError_t forward_typed(const pn_block_norm_args& a, hipStream_t st) {
 }
 
 // Rows of a workgroup of the gradients: as many workgroups as run at once (12
-// waves a unit in workgroups of up to four waves, 16 in larger ones), so that
-// none is left for a second round.
+// waves a unit up to 2048 channels, 8 in the larger forms), so that none is
+// left for a second round.
 void backward_split(const pn_block_norm_args& a, int64_t* rows, int64_t* n_wg) {
     const int64_t n = a.B * a.T;
-    const int64_t at_once = a.D <= 512 ? 3072 : a.D <= 1024 ? 1536 : a.D <= 2560 ? 768 : a.D <= 4096 ? 512 : 256;
+    const int64_t at_once = a.D <= 512 ? 3072 : a.D <= 1024 ? 1536 : a.D <= 2048 ? 768 : a.D <= 2560 ? 512 : 256;
     *rows = std::max<int64_t>(1, (n + at_once - 1) / at_once);
     *n_wg = (n + *rows - 1) / *rows;
 }
@@ -307,7 +372,13 @@ hipError_t backward_typed(const pn_block_norm_args& a, hipStream_t st) {
     float* part = static_cast<float*>(a.workspace);
     const hipError_t e = with_form<T, R>(a, widest<T, R>(a, true), [&](auto form) {
         using Fm = decltype(form);
-        block_norm_backward<T, R, Fm::V, Fm::NU, Fm::THREADS><<<grid_of(n_wg, Fm::THREADS), Fm::THREADS, 0, st>>>(a, rows, n_wg, part);
+        const auto kernel = block_norm_backward<T, R, Fm::V, Fm::NU, Fm::THREADS>;
+        const int lds = static_cast<int>(12 * a.D);
+        if (lds > 48 * 1024) {
+            const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+            if (e != hipSuccess) return e;
+        }
+        kernel<<<grid_of(n_wg, Fm::THREADS), Fm::THREADS, lds, st>>>(a, rows, n_wg, part);
         return hipGetLastError();
     });
     float *dw = a.weight ? a.dweight : nullptr, *dpw = a.post_weight ? a.dpost_weight : nullptr, *dsc = a.scale ? a.dscale : nullptr;
