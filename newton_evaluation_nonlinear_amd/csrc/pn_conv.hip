@@ -181,17 +181,26 @@ __global__ __launch_bounds__(kBlock) void conv_backward(pn_conv_args a, ConvCut 
         if (taps.at(k)) token<T, V>(a, p.b, t0 - (K - 1) + k, n, p.d, x[k + 1]);
     const T* xrow = static_cast<const T*>(a.x.p) + p.b * a.x.sb + p.d;
     const T* grow = static_cast<const T*>(a.dy.p) + p.b * a.dy.sb + p.d;
-    constexpr int AHEAD = 4;                             // tokens loaded at a time
-    Pack<T, V> nx[AHEAD], ng[AHEAD];
+    constexpr int AHEAD = 4;                             // tokens loaded at a time, while those before are worked on
+    Pack<T, V> nx[AHEAD], ng[AHEAD], cx[AHEAD], cg[AHEAD];
+    auto fetch = [&](int64_t s) {                        // rows behind the last are the last again: not used
+        if (n <= 0) return;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int64_t t = min(s + j, n - 1);
+            nx[j] = *reinterpret_cast<const Pack<T, V>*>(xrow + t * a.x.st);
+            ng[j] = *reinterpret_cast<const Pack<T, V>*>(grow + t * a.dy.st);
+        }
+    };
+    fetch(t0);
     // x[k] and d[k]: of token t - (K - 1) + k
     for (int64_t s = t0; s < t1 + past; s += AHEAD) {
-        if (n > 0)
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {            // rows behind the last are the last again: not used
-                const int64_t t = min(s + j, n - 1);
-                nx[j] = *reinterpret_cast<const Pack<T, V>*>(xrow + t * a.x.st);
-                ng[j] = *reinterpret_cast<const Pack<T, V>*>(grow + t * a.dy.st);
-            }
+        for (int j = 0; j < AHEAD; ++j) {
+            cx[j] = nx[j];
+            cg[j] = ng[j];
+        }
+        if (s + AHEAD < t1 + past) fetch(s + AHEAD);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
             const int64_t t = s + j;
@@ -204,8 +213,8 @@ __global__ __launch_bounds__(kBlock) void conv_backward(pn_conv_args a, ConvCut 
                     d[k][i] = d[k + 1][i];
                     x[k][i] = x[k + 1][i];
                 }
-                x[K - 1][i] = on ? to_f32(nx[j].v[i]) : 0.0f;
-                float pre = bias[i], g = on ? to_f32(ng[j].v[i]) : 0.0f;
+                x[K - 1][i] = on ? to_f32(cx[j].v[i]) : 0.0f;
+                float pre = bias[i], g = on ? to_f32(cg[j].v[i]) : 0.0f;
 #pragma unroll
                 for (int k = 0; k < K; ++k)
                     if (taps.at(k)) pre = fmaf(w[k][i], x[k][i], pre);

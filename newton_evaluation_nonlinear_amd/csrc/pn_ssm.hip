@@ -158,7 +158,7 @@ SsmPlan plan_ssm(const pn_ssm_args& a, bool backward) {
     const int64_t rows = a.B * p.chans, waves = rows * p.blocks;
     p.tiles = (a.T + kSsmTile - 1) / kSsmTile;
     int64_t n = std::min<int64_t>((6144 + waves - 1) / waves, a.T / 32);
-    if (n < 3) n = 1;
+    if (waves >= 2048) n = 1;
     const int64_t per = std::max<int64_t>(1, (p.tiles + n - 1) / n);
     p.seg = per * kSsmTile;
     p.n_seg = static_cast<int32_t>(std::max<int64_t>(1, (p.tiles + per - 1) / per));

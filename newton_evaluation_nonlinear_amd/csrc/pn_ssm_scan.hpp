@@ -258,7 +258,7 @@ __device__ __forceinline__ float joined(const float* ex, int blocks, int m, int 
 
 // BLOCKS: the most waves that share the states of a channel.
 template <typename T, int S, int BLOCKS, int PASS>
-__global__ __launch_bounds__(64 * BLOCKS) __attribute__((amdgpu_waves_per_eu(4)))
+__global__ __launch_bounds__(64 * BLOCKS) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void ssm_pass(pn_ssm_args a, SsmPlan p) {
     constexpr int E = 4 * S, WAVES = BLOCKS;
     constexpr bool MULTI = BLOCKS > 1;
