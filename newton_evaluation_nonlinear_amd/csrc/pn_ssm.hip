@@ -144,9 +144,12 @@ hipError_t pass(const pn_ssm_args& a, const SsmPlan& p, SsmPass which, hipStream
 
 }  // namespace
 
-// Segments: as many waves as fill the device, no segment below 32 tokens.
-// Two sweeps of a segment then take the place of one of the sequence, so that
-// two segments gain nothing.
+// Segments, none below 32 tokens: 6144 waves, six for every SIMD, of which the
+// oldest run first and the others fill their waits (65536 tokens of 2048 channels in 2048, 4096, 6144 and 12288
+// waves: 1461, 1416, 1267 and 1334 us).  Two sweeps then take the place of one,
+// so two segments gain nothing, and from 2048 waves on one is enough (2048
+// tokens of 16 states, microseconds in one and in several: 1536 waves 673 and
+// 655, with gradients 3212 and 2735; 2048 waves 688 and 861, 3479 and 3624).
 SsmPlan plan_ssm(const pn_ssm_args& a, bool backward) {
     SsmPlan p{};
     p.states = a.N <= 4 ? 4 : a.N <= 8 ? 8 : 16;
@@ -158,7 +161,7 @@ SsmPlan plan_ssm(const pn_ssm_args& a, bool backward) {
     const int64_t rows = a.B * p.chans, waves = rows * p.blocks;
     p.tiles = (a.T + kSsmTile - 1) / kSsmTile;
     int64_t n = std::min<int64_t>((6144 + waves - 1) / waves, a.T / 32);
-    if (waves >= 2048) n = 1;
+    if (waves >= 2048 || n < 3) n = 1;
     const int64_t per = std::max<int64_t>(1, (p.tiles + n - 1) / n);
     p.seg = per * kSsmTile;
     p.n_seg = static_cast<int32_t>(std::max<int64_t>(1, (p.tiles + per - 1) / per));

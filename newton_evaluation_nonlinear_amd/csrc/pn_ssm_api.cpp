@@ -55,7 +55,7 @@ int check_types(int64_t dtype, int64_t B, int64_t T, int64_t D) {
     if (dtype < PN_F32 || dtype > PN_F16) return fail(PN_EINVAL, "unknown storage type %lld", (long long)dtype);
     if (B < 0 || T < 0 || D < 0) return fail(PN_EINVAL, "negative size");
     if (T > kMaxTokens || D > kMaxBlocks || !small_product({B, T}, kMaxBlocks) ||
-        !small_product({B, std::max<int64_t>(T, 1), D}, int64_t(1) << 40))
+        !small_product({B, std::max<int64_t>(T, 1), D}, int64_t(1) << 38))
         return fail(PN_EUNSUPPORTED, "size too large");
     return PN_OK;
 }
@@ -265,6 +265,7 @@ int pn_short_conv_step(const pn_conv_step_args* p) {
     const pn_conv_step_args& a = *p;
     PN_TRY(check_conv_sizes(a.dtype, a.B, 1, a.D, a.W, a.activation));
     if (a.n_slots < 0 || a.n_slots > kMaxSlots) return fail(PN_EINVAL, "n_slots out of range");
+    if (!small_product({std::max<int64_t>(a.n_slots, 1), a.D, a.W}, int64_t(1) << 45)) return fail(PN_EUNSUPPORTED, "size too large");
     if (a.B == 0 || a.D == 0) return PN_OK;
     const int64_t e = elem_bytes(a.dtype);
     PN_TRY(check_rows(a.x, "x", e));
@@ -320,7 +321,9 @@ int pn_ssm_step(const pn_ssm_step_args* p) {
     const pn_ssm_step_args& a = *p;
     PN_TRY(check_ssm_sizes(a.dtype, a.B, 1, a.D, a.N, a.G, a.softplus));
     if (a.n_slots < 0 || a.n_slots > kMaxSlots) return fail(PN_EINVAL, "n_slots out of range");
-    if (!small_product({std::max<int64_t>(a.n_slots, 1), std::max<int64_t>(a.D, 1), a.N}, int64_t(1) << 45)) return fail(PN_EUNSUPPORTED, "size too large");
+    if (!small_product({std::max<int64_t>(a.n_slots, 1), std::max<int64_t>(a.D, 1), a.N}, int64_t(1) << 45) ||
+        !small_product({a.B, a.D}, kMaxBlocks))
+        return fail(PN_EUNSUPPORTED, "size too large");
     if (a.B == 0 || a.D == 0) return PN_OK;
     const int64_t e = elem_bytes(a.dtype);
     PN_TRY(check_rows(a.x, "x", e));

@@ -393,6 +393,22 @@ def test_scan_segments(dtype):
     _close(h1, _np(final), 2.1 * fe, "state of two calls")
 
 
+@pytest.mark.parametrize("T", list(range(1, 34)) + [95, 96, 97, 127, 128, 129])
+def test_scan_lengths_of_one_call(T):
+    """Every length of the first tiles, and those at which segments begin."""
+    check_scan(scan_inputs("bf16", 1, T, 40, 16, 1, seed=T), "bf16")
+
+
+def test_one_token_with_any_token_stride():
+    """The stride of a single token is never used."""
+    for st in (1 << 20, 1 << 27, 1 << 33):
+        a, c, n = scan_inputs("bf16", 2, 1, 40, 16, 2), conv_inputs("bf16", 2, 1, 40, 4, True), norm_inputs("bf16", "f32", (2, 1), 40)
+        far = lambda t: t.as_strided(t.shape, (t.stride(0), st, *t.stride()[2:]))  # noqa: E731
+        check_scan({k: far(v) if k in ("x", "dt", "b", "c", "gate", "dy") else v for k, v in a.items()}, "bf16")
+        check_conv({k: far(v) if k in ("x", "dy") else v for k, v in c.items()}, "bf16")
+        check_norm({k: far(v) if v.dim() == 3 else v for k, v in n.items()}, "bf16", "f32")
+
+
 def test_scan_without_tokens():
     a = scan_inputs("bf16", 2, 0, 24, 16, 1)
     y, final = pn.ssm_scan(a["x"], a["dt"], a["A"], a["b"], a["c"], initial_state=a["initial_state"])
@@ -530,6 +546,21 @@ def test_norm_strides_and_single_tokens(dtype, rdtype):
     a["ds"] = a["ds"][:, :1].expand(3, 5, 48)
     check_norm(a, dtype, rdtype)
     check_norm({k: v[:, 0] if v.dim() == 3 else v for k, v in a.items()}, dtype, rdtype)
+
+
+def test_norm_of_wide_rows_is_captured():
+    """Rows whose weights take more LDS than a launch has by itself."""
+    a = norm_inputs("bf16", "bf16", (1, 5), 8192)
+    kw = {k: a[k] for k in ("gate", "post_weight", "scale")}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["residual"], a["weight"], **kw)
+    for i in range(3):
+        a["dy"].mul_(1.5)
+        graph.replay()
+        want = pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["residual"], a["weight"], **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want)), i
 
 
 def test_norm_without_tokens():

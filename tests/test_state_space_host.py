@@ -173,7 +173,8 @@ def _conv_step(dtype=0, B=2, D=8, W=4, act=1, w=3 * GIB, bias=0, x=TOK(4), state
 @pytest.mark.parametrize("kw, code", [
     (dict(dtype=-1), pn.EINVAL), (dict(B=-1), pn.EINVAL), (dict(W=9), pn.EUNSUPPORTED), (dict(w=0), pn.EINVAL), (dict(y=0), pn.EINVAL),
     (dict(state=0), pn.EINVAL), (dict(n_slots=1), pn.EINVAL), (dict(n_slots=-1), pn.EINVAL), (dict(slots=7 * GIB + 2), pn.EINVAL),
-    (dict(y=4 * GIB), pn.EINVAL), (dict(y=5 * GIB), pn.EINVAL), (dict(state=4 * GIB), pn.EINVAL), (dict(x=TOK(0)), pn.EINVAL)])
+    (dict(y=4 * GIB), pn.EINVAL), (dict(y=5 * GIB), pn.EINVAL), (dict(state=4 * GIB), pn.EINVAL), (dict(x=TOK(0)), pn.EINVAL),
+    (dict(n_slots=1 << 31, D=1 << 20), pn.EUNSUPPORTED)])
 def test_conv_step_refusals(kw, code):
     assert pn.lib().pn_short_conv_step(_conv_step(**kw)) == code
     assert pn.last_error() != ""
@@ -195,7 +196,8 @@ def _scan(dtype=0, B=2, T=2, D=8, N=16, G=1, soft=1, A=3 * GIB, skip=0, bias=0, 
     (dict(A=3 * GIB + 2), pn.EINVAL), (dict(x=TOK(0)), pn.EINVAL), (dict(dt=TOK(0)), pn.EINVAL), (dict(b=BC(0)), pn.EINVAL),
     (dict(c=(7 * GIB + 1, 64, 32, 16)), pn.EINVAL), (dict(z=(15 * GIB + 2, 64, 32, 0), dz=16 * GIB), pn.EINVAL),
     (dict(b=BC(6, sh=-1)), pn.EINVAL), (dict(n=17 * GIB + 2), pn.EINVAL), (dict(T=1 << 31), pn.EUNSUPPORTED),
-    (dict(B=1 << 20, T=1 << 10, D=1 << 12), pn.EUNSUPPORTED)])
+    (dict(B=1 << 20, T=1 << 10, D=1 << 12), pn.EUNSUPPORTED), (dict(D=1 << 25), pn.EUNSUPPORTED),
+    (dict(x=TOK(4, st=(1 << 26) + 1)), pn.EUNSUPPORTED), (dict(b=BC(6, st=1 << 27)), pn.EUNSUPPORTED)])
 def test_scan_refusals(kw, code):
     need = pn.lib().pn_ssm_scan_workspace_bytes(_scan(), 1)
     assert need > 256
@@ -225,6 +227,19 @@ def test_scan_outputs_and_workspace():
     assert size(_scan(B=0), 1) == 256
 
 
+@pytest.mark.parametrize("N", [1, 8, 16, 17, 128])
+def test_scan_workspace_at_every_small_length(N):
+    """A size for every length, that never shrinks with it, and none for a forward call of one segment."""
+    size = pn.lib().pn_ssm_scan_workspace_bytes
+    for B, D in ((1, 1), (1, 33), (3, 300), (64, 1100), (2000, 40)):
+        last = 0
+        for T in range(200):
+            n, back = size(_scan(B=B, T=T, D=D, N=N), 0), size(_scan(B=B, T=T, D=D, N=N), 1)
+            assert n >= 256 and back > 256 and (T >= 96 or n == 256), (B, D, T)
+            assert T >= 96 or back >= last
+            last = back
+
+
 def _scan_step(dtype=0, B=2, D=8, N=16, G=1, soft=1, A=3 * GIB, skip=0, bias=0, x=TOK(4), dt=TOK(5), z=TOK(0), b=BC(6), c=BC(7),
                state=8 * GIB, slots=0, n_slots=2, y=9 * GIB):
     return ss._SSM_STEP(dtype, B, D, N, G, soft, A, skip, bias, *x, *dt, *z, *b, *c, state, slots, n_slots, y, 0)
@@ -234,7 +249,8 @@ def _scan_step(dtype=0, B=2, D=8, N=16, G=1, soft=1, A=3 * GIB, skip=0, bias=0, 
     (dict(dtype=9), pn.EINVAL), (dict(B=-1), pn.EINVAL), (dict(N=200), pn.EUNSUPPORTED), (dict(G=5), pn.EINVAL), (dict(A=0), pn.EINVAL),
     (dict(y=0), pn.EINVAL), (dict(state=0), pn.EINVAL), (dict(n_slots=1), pn.EINVAL), (dict(n_slots=-1), pn.EINVAL),
     (dict(slots=10 * GIB + 2), pn.EINVAL), (dict(y=8 * GIB), pn.EINVAL), (dict(y=4 * GIB), pn.EINVAL), (dict(state=7 * GIB), pn.EINVAL),
-    (dict(dt=TOK(0)), pn.EINVAL), (dict(b=BC(6, sb=-3)), pn.EINVAL)])
+    (dict(dt=TOK(0)), pn.EINVAL), (dict(b=BC(6, sb=-3)), pn.EINVAL),
+    (dict(n_slots=1 << 31, D=1 << 20), pn.EUNSUPPORTED), (dict(B=1 << 20, D=1 << 16), pn.EUNSUPPORTED)])
 def test_scan_step_refusals(kw, code):
     assert pn.lib().pn_ssm_step(_scan_step(**kw)) == code
     assert pn.last_error() != ""
