@@ -63,19 +63,17 @@ class BlockNorm(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, residual, weight, post_weight, scale):
-        y, s = pn.block_norm(x, weight, residual=residual, post_weight=post_weight, scale=scale)
-        ctx.save_for_backward(x, s, weight, post_weight, scale)
-        ctx.had_residual = residual is not None
+        ctx.save_for_backward(x, residual, weight, post_weight, scale)
         ctx.set_materialize_grads(False)
-        return y, s
+        return pn.block_norm(x, weight, residual=residual, post_weight=post_weight, scale=scale)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, ds):
-        x, s, weight, post_weight, scale = ctx.saved_tensors
-        dx, dw, dr, _, dpw, dsc = pn.block_norm_backward(_dense(dy, x), None if ds is None else ds.contiguous(), x, s, weight,
-                                                         post_weight=post_weight, scale=scale)
-        return dx, dr if ctx.had_residual else None, dw, dpw, dsc
+        x, residual, weight, post_weight, scale = ctx.saved_tensors
+        dx, dw, dr, _, dpw, dsc = pn.block_norm_backward(_dense(dy, x), None if ds is None else ds.contiguous(), x, weight,
+                                                         residual=residual, post_weight=post_weight, scale=scale)
+        return dx, dr, dw, dpw, dsc
 
 
 class StateSpaceBlock(torch.nn.Module):

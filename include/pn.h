@@ -569,7 +569,7 @@ int pn_ssm_step(const pn_ssm_step_args* a);
  * block takes.  x, gate, y and their gradients have the storage type, the
  * residual, s and theirs residual_dtype: the storage type or PN_F32.  Means
  * are float32 sums of squares: rows of elements past 1e18 come out as 0.
- * The backward reads s as it was stored. */
+ * The backward takes what the forward took, and forms s again. */
 typedef struct pn_block_norm_args {
     int64_t dtype, residual_dtype, B, T, D;
     double eps;
@@ -578,7 +578,6 @@ typedef struct pn_block_norm_args {
     void *y, *s;                /* forward: contiguous [B, T, D]; y where weight is given */
     pn_tokens dy, ds;           /* backward: gradients of y (where weight is given) and of
                                    s (p NULL: 0)                                 */
-    pn_tokens s_in;             /* backward: the forward's s                     */
     void *dx, *dgate, *dresidual;   /* backward: [B, T, D]; dgate where the gate is given,
                                    dresidual or NULL                             */
     float *dweight, *dpost_weight, *dscale;      /* backward, where the input is given */

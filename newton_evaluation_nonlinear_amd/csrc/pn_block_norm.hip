@@ -6,6 +6,9 @@
 //     q = pw scale t,  du = ru (q - n mean(q n)),  dpw = scale sum t n,
 //     dscale = pw sum t n,  dx = du silu(gate),  dgate = du x silu'(gate).
 //
+// The gradients form s again from what the forward took, in float32: from s
+// as it was stored in 16 bits, dw would keep its rounding.
+//
 // Bound: bytes.  A row stays in the registers of the lanes that hold it, NU
 // units of V channels each, so everything is read once and written once; sums
 // over a row go through the lanes and, in workgroups of several waves, LDS.
@@ -170,27 +173,22 @@ void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float
         r.each([&](int u, int i) { v[u][i] = 1.0f; });
         if (a.scale) r.load(a.scale, v);
         r.store(weights + 2 * a.D, v);
-        if (a.post_weight) {
-            float w[NU][V];
-            r.load(a.post_weight, w);
-            r.store(weights + a.D, w);
-        }
+        r.each([&](int u, int i) { v[u][i] = 1.0f; });
+        if (a.post_weight) r.load(a.post_weight, v);
+        r.store(weights + a.D, v);
     }
-    const bool need = a.gate.p || a.post_weight || a.scale;
     Pack<T, V> px[NU] = {}, pg[NU] = {}, pe[NU] = {};
     Pack<R, V> ps[NU] = {}, pt[NU] = {};
     auto fetch_first = [&](int64_t row) {
         const int64_t b = row / a.T, tok = row - b * a.T;
-        if (a.weight) {
-            r.fetch(row_of<R>(a.s_in, b, tok), ps);
-            r.fetch(row_of<T>(a.dy, b, tok), pe);
-        }
-        if (a.ds.p) r.fetch(row_of<R>(a.ds, b, tok), pt);
+        r.fetch(row_of<T>(a.x, b, tok), px);
+        if (a.gate.p) r.fetch(row_of<T>(a.gate, b, tok), pg);
+        if (a.residual.p) r.fetch(row_of<R>(a.residual, b, tok), ps);
     };
     auto fetch_last = [&](int64_t row) {
         const int64_t b = row / a.T, tok = row - b * a.T;
-        if (need) r.fetch(row_of<T>(a.x, b, tok), px);
-        if (a.gate.p) r.fetch(row_of<T>(a.gate, b, tok), pg);
+        if (a.weight) r.fetch(row_of<T>(a.dy, b, tok), pe);
+        if (a.ds.p) r.fetch(row_of<R>(a.ds, b, tok), pt);
     };
     const int64_t end = min((wg + 1) * rows, a.B * a.T);
     constexpr bool AHEAD = V * NU < 16;
@@ -199,14 +197,14 @@ void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float
         fetch_last(wg * rows);
     }
     for (int64_t row = wg * rows; row < end; ++row) {
-        float t[NU][V], x[NU][V], g[NU][V], s[NU][V], e[NU][V], w[NU][V];
+        float t[NU][V], x[NU][V], g[NU][V], s[NU][V], e[NU][V], act[NU][V], w[NU][V], sc[NU][V];
         if (!AHEAD) fetch_first(row);
-        r.widen(pt, t);
+        r.widen(px, x);
+        r.widen(pg, g);
         r.widen(ps, s);
-        r.widen(pe, e);
         if (AHEAD) {
-            r.widen(px, x);
-            r.widen(pg, g);
+            r.widen(pt, t);
+            r.widen(pe, e);
             if (row + 1 < end) {
                 fetch_first(row + 1);
                 fetch_last(row + 1);
@@ -214,8 +212,24 @@ void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float
         } else {
             fetch_last(row);
         }
+        // the forward: act is the gate's sigmoid
+        r.each([&](int u, int i) { act[u][i] = a.gate.p ? logistic(g[u][i]) : 1.0f; });
+        auto block = [&](int u, int i) { return a.gate.p ? x[u][i] * g[u][i] * act[u][i] : x[u][i]; };
+        float ru = 1.0f, uu = 0.0f, unused = 0.0f;
+        if (a.post_weight) {
+            r.each([&](int u, int i) { uu = fmaf(block(u, i), block(u, i), uu); });
+            row_sums<THREADS>(uu, unused, lds);
+            ru = 1.0f / sqrtf(fmaf(uu, inv, eps));
+        }
+        if (!AHEAD) {
+            r.widen(pt, t);
+            r.widen(pe, e);
+        }
         if (a.weight) {
             float ss = 0.0f, es = 0.0f;
+            r.load(weights + a.D, w);
+            r.load(weights + 2 * a.D, sc);
+            r.each([&](int u, int i) { s[u][i] = fmaf(sc[u][i], block(u, i) * ru * w[u][i], s[u][i]); });
             r.load(weights, w);
             r.each([&](int u, int i) {
                 w[u][i] *= e[u][i];
@@ -231,40 +245,31 @@ void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float
             });
         }
         if (a.dresidual) r.store(static_cast<R*>(a.dresidual) + row * a.D, t);
-        if (!AHEAD) {
-            r.widen(px, x);
-            r.widen(pg, g);
-        }
-        // from here on e: the gate's sigmoid, s: u (x without a gate)
-        r.each([&](int u, int i) {
-            e[u][i] = a.gate.p ? logistic(g[u][i]) : 1.0f;
-            s[u][i] = a.gate.p ? x[u][i] * g[u][i] * e[u][i] : x[u][i];
-        });
         if (a.post_weight) {
-            float uu = 0.0f, qu = 0.0f, sc[NU][V];
+            float qu = 0.0f;
             r.load(weights + a.D, w);
             r.load(weights + 2 * a.D, sc);
             r.each([&](int u, int i) {
-                uu = fmaf(s[u][i], s[u][i], uu);
-                qu = fmaf(w[u][i] * sc[u][i] * t[u][i], s[u][i], qu);
+                w[u][i] *= sc[u][i] * t[u][i];
+                qu = fmaf(w[u][i], block(u, i), qu);
             });
-            row_sums<THREADS>(uu, qu, lds);
-            const float ru = 1.0f / sqrtf(fmaf(uu, inv, eps)), mean = qu * ru * inv;
+            row_sums<THREADS>(qu, unused, lds);
+            const float mean = qu * ru * inv;
             r.each([&](int u, int i) {
-                const float n = s[u][i] * ru;
+                const float n = block(u, i) * ru;
                 tn[u][i] = fmaf(t[u][i], n, tn[u][i]);
-                t[u][i] = ru * fmaf(-n, mean, w[u][i] * sc[u][i] * t[u][i]);
+                t[u][i] = ru * fmaf(-n, mean, w[u][i]);
             });
         } else if (a.scale) {
-            r.load(weights + 2 * a.D, w);
+            r.load(weights + 2 * a.D, sc);
             r.each([&](int u, int i) {
-                tn[u][i] = fmaf(t[u][i], s[u][i], tn[u][i]);
-                t[u][i] *= w[u][i];
+                tn[u][i] = fmaf(t[u][i], block(u, i), tn[u][i]);
+                t[u][i] *= sc[u][i];
             });
         }
         if (a.gate.p) {
             r.each([&](int u, int i) {                   // x: dgate, t: dx
-                const float du = t[u][i], p = e[u][i];
+                const float du = t[u][i], p = act[u][i];
                 x[u][i] = du * x[u][i] * p * fmaf(g[u][i], 1.0f - p, 1.0f);
                 t[u][i] = du * g[u][i] * p;
             });
@@ -305,7 +310,7 @@ int widest(const pn_block_norm_args& a, bool backward) {
     int64_t t = bits(a.x, sizeof(T)) | bits(a.gate, sizeof(T)), r = 0;
     if (backward) {
         t |= (a.weight ? bits(a.dy, sizeof(T)) : 0) | ptr(a.dx) | (a.gate.p ? ptr(a.dgate) : 0);
-        r |= bits(a.ds, sizeof(R)) | (a.weight ? bits(a.s_in, sizeof(R)) : 0) | ptr(a.dresidual);
+        r |= bits(a.ds, sizeof(R)) | bits(a.residual, sizeof(R)) | ptr(a.dresidual);
     } else {
         t |= a.weight ? ptr(a.y) : 0;
         r |= bits(a.residual, sizeof(R)) | ptr(a.s);

@@ -154,8 +154,11 @@ SsmPlan plan_ssm(const pn_ssm_args& a, bool backward) {
     SsmPlan p{};
     p.states = a.N <= 4 ? 4 : a.N <= 8 ? 8 : 16;
     p.blocks = static_cast<int32_t>((a.N + 15) / 16);
+    // channel blocks of a workgroup of the gradients: 4, or fewer where that
+    // many leave more than an eighth of them empty
     const int64_t per_group = (a.D / a.G + 31) / 32;
-    p.wide = p.blocks > 1 || per_group == 1 ? 1 : per_group == 2 ? 2 : 4;
+    p.wide = backward && p.blocks == 1 ? 4 : 1;
+    while (p.wide > 1 && ((per_group + p.wide - 1) / p.wide * p.wide - per_group) * 8 > per_group) p.wide /= 2;
     p.per_group = static_cast<int32_t>((per_group + p.wide - 1) / p.wide * p.wide);
     p.chans = static_cast<int32_t>(a.G) * p.per_group;
     const int64_t rows = a.B * p.chans, waves = rows * p.blocks;

@@ -195,14 +195,11 @@ int check_norm(const pn_block_norm_args* p, bool backward) {
     if (n > 0) {
         PN_TRY(check_rows(a.x, "x", e));
         if (a.gate.p) PN_TRY(check_rows(a.gate, "gate", e));
+        if (a.residual.p) PN_TRY(check_rows(a.residual, "residual", er));
         if (!backward) {
-            if (a.residual.p) PN_TRY(check_rows(a.residual, "residual", er));
             if (!a.s || (a.weight && !a.y)) return fail(PN_EINVAL, "an output is NULL");
         } else {
-            if (a.weight) {
-                PN_TRY(check_rows(a.dy, "dy", e));
-                PN_TRY(check_rows(a.s_in, "s", er));
-            }
+            if (a.weight) PN_TRY(check_rows(a.dy, "dy", e));
             if (a.ds.p) PN_TRY(check_rows(a.ds, "ds", er));
             if (!a.dx || (a.gate.p && !a.dgate)) return fail(PN_EINVAL, "an output is NULL");
         }
@@ -211,16 +208,17 @@ int check_norm(const pn_block_norm_args* p, bool backward) {
     }
     const Range x = range3(a.x, a.B, a.T, a.D, e), z = range3(a.gate, a.B, a.T, a.D, e);
     const Range w = range(a.weight, 4 * a.D), pw = range(a.post_weight, 4 * a.D), sc = range(a.scale, 4 * a.D);
+    const Range res = range3(a.residual, a.B, a.T, a.D, er);
     if (!backward)
         return check_overlaps({range(a.weight ? a.y : nullptr, e * n), range(a.s, er * n)},
-                              {x, z, w, pw, sc, range3(a.residual, a.B, a.T, a.D, er)});
+                              {x, z, w, pw, sc, res});
     const size_t need = n > 0 ? padded(block_norm_workspace(a)) : 0;
     PN_TRY(check_workspace(a.workspace, a.workspace_bytes, need));
     return check_overlaps({range(a.dx, e * n), range(a.gate.p ? a.dgate : nullptr, e * n), range(a.dresidual, er * n),
                            range(a.weight ? a.dweight : nullptr, 4 * a.D), range(a.post_weight ? a.dpost_weight : nullptr, 4 * a.D),
                            range(a.scale ? a.dscale : nullptr, 4 * a.D), need ? range(a.workspace, static_cast<int64_t>(need)) : Range{0, 0}},
-                          {x, z, w, pw, sc, a.weight ? range3(a.dy, a.B, a.T, a.D, e) : Range{0, 0},
-                           a.weight ? range3(a.s_in, a.B, a.T, a.D, er) : Range{0, 0}, range3(a.ds, a.B, a.T, a.D, er)});
+                          {x, z, w, pw, sc, res, a.weight ? range3(a.dy, a.B, a.T, a.D, e) : Range{0, 0},
+                           range3(a.ds, a.B, a.T, a.D, er)});
 }
 
 int zeros(float* p, int64_t n, hipStream_t st) { return p ? launched(launch_fill(p, n, st)) : PN_OK; }

@@ -14,6 +14,12 @@ __device__ __forceinline__ float pinned(float v) {
     return v;
 }
 
+// v if on, otherwise 0, by a select and not a branch around what v takes.
+__device__ __forceinline__ float kept(bool on, float v) {
+    v = pinned(v);
+    return on ? v : 0.0f;
+}
+
 // log(1 + e^v) = max(v, 0) + log(1 + t), t = e^-|v|; log(1 + t) as log(w) +
 // (t - (w - 1)) / w, w = 1 + t as rounded, which leaves 2^-48 of its rounding.
 __device__ __forceinline__ float softplus(float v, float* slope) {

@@ -201,9 +201,16 @@ struct SsmWave {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), static_cast<short>(0),
                                                  static_cast<int>(((rows - 1) * static_cast<uint32_t>(st) + width) * sizeof(T)), 0x00020000);
     }
-    __device__ __forceinline__ static T read(__amdgpu_buffer_rsrc_t r, uint32_t at) {
-        if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
-        else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+    // An element as it is stored, in a register of its own (kept as 16-bit
+    // values the compiler packs them in pairs, which costs more than it saves).
+    __device__ __forceinline__ static uint32_t read(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+        if constexpr (sizeof(T) == 4) return __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+        else return __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
+    }
+    __device__ __forceinline__ static float widen(uint32_t v) {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(v);
+        else if constexpr (__is_same(T, bf16)) return __uint_as_float(v << 16);
+        else return to_f32(__builtin_bit_cast(T, static_cast<uint16_t>(v)));
     }
     __device__ __forceinline__ static void write(__amdgpu_buffer_rsrc_t r, uint32_t at, float v) {
         if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, at, 0, 0);
@@ -211,7 +218,7 @@ struct SsmWave {
     }
     static constexpr uint32_t kNowhere = 0x80000000u;    // behind every tile
     // The lane's tokens and channel of x.
-    __device__ __forceinline__ void load_rows(const pn_tokens& x, int64_t t0, T* v) const {
+    __device__ __forceinline__ void load_rows(const pn_tokens& x, int64_t t0, uint32_t* v) const {
         const __amdgpu_buffer_rsrc_t r = rows_at(static_cast<const T*>(x.p) + b * x.sb + t0 * x.st, x.st, left(t0), static_cast<int>(a.D));
         const uint32_t st = static_cast<uint32_t>(x.st) * sizeof(T), at = odd * st + ch * sizeof(T);
 #pragma unroll
@@ -222,12 +229,16 @@ struct SsmWave {
         return rows_at(static_cast<const T*>(out) + (b * a.T + t0) * a.D, a.D,
                        static_cast<int>(min(a.T - t0, static_cast<int64_t>(kSsmTile))), static_cast<int>(a.D));
     }
+    // An output that is not wanted: nothing is written.
+    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t no_rows() {
+        return __builtin_amdgcn_make_buffer_rsrc(nullptr, static_cast<short>(0), 0, 0x00020000);
+    }
     __device__ __forceinline__ uint32_t row_at(int m) const {
         const uint32_t st = static_cast<uint32_t>(a.D) * sizeof(T);
         return (own ? odd * st + ch * sizeof(T) : kNowhere) + 2 * m * st;
     }
     // The b and c of a tile, to LDS as [token][b | c][E]; 0 for states and tokens that do not exist.
-    __device__ __forceinline__ void load_bc(const T* src, int64_t st, int64_t t0, T* v) const {
+    __device__ __forceinline__ void load_bc(const T* src, int64_t st, int64_t t0, uint32_t* v) const {
         const __amdgpu_buffer_rsrc_t r = rows_at(src + t0 * st, st, left(t0), static_cast<int>(a.N));
 #pragma unroll
         for (int m = 0; m < M; ++m) {
@@ -235,11 +246,11 @@ struct SsmWave {
             v[m] = read(r, n < a.N && i < kSsmTile * E ? (i / E * static_cast<uint32_t>(st) + n) * sizeof(T) : kNowhere);
         }
     }
-    __device__ __forceinline__ void store_bc(float* lds, int which, const T* v) const {
+    __device__ __forceinline__ void store_bc(float* lds, int which, const uint32_t* v) const {
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             const int i = lane + 64 * m;
-            if (i < kSsmTile * E) lds[(i / E * 2 + which) * E + i % E] = to_f32(v[m]);
+            if (i < kSsmTile * E) lds[(i / E * 2 + which) * E + i % E] = widen(v[m]);
         }
     }
     __device__ __forceinline__ void read_bc(const float* lds, int i, int which, float* v) const {
@@ -296,8 +307,7 @@ void ssm_pass(pn_ssm_args a, SsmPlan p) {
     }
     float since = 0.0f;                                  // sum of the channel's steps
     constexpr bool C = OUT || BACK;
-    T x[kOwn], dt[kOwn], z[kOwn], gy[kOwn];
-    T bv[w.M], cv[w.M];
+    uint32_t x[kOwn], dt[kOwn], z[kOwn], gy[kOwn], bv[w.M], cv[w.M];
     auto load = [&](int64_t t0) {
         w.load_rows(a.x, t0, x);
         w.load_rows(a.dt, t0, dt);
@@ -313,16 +323,16 @@ void ssm_pass(pn_ssm_args a, SsmPlan p) {
 #pragma unroll
         for (int m = 0; m < kOwn; ++m) {
             const bool on = 2 * m < left;
-            const float raw = to_f32(dt[m]) + bias;
+            const float raw = w.widen(dt[m]) + bias;
             float slope;
             const float soft = pinned(softplus(raw, &slope));
             dl[m] = on ? (a.softplus ? soft : raw) : 0.0f;
-            xs[m] = on ? to_f32(x[m]) : 0.0f;
+            xs[m] = on ? w.widen(x[m]) : 0.0f;
             steps += dl[m];
             if (C) {
-                const float zf = gated ? to_f32(z[m]) : 0.0f, act = pinned(zf * logistic(zf));
+                const float zf = gated ? w.widen(z[m]) : 0.0f, act = pinned(zf * logistic(zf));
                 g[m] = gated ? act : 1.0f;
-                if (BACK) g[m] = on ? g[m] * to_f32(gy[m]) : 0.0f;
+                if (BACK) g[m] = on ? g[m] * w.widen(gy[m]) : 0.0f;
             }
         }
         wave_sync();
@@ -370,7 +380,7 @@ void ssm_pass(pn_ssm_args a, SsmPlan p) {
             if (OUT) {
                 const float y = quad_sum(part, w.j);
                 if (MULTI) ex[(w.blk * kOwn + m) * 64 + w.lane] = y;
-                else w.write(y_rows, w.row_at(m), 2 * m < left ? pinned(fmaf(skip, xs[m], y) * g[m]) : 0.0f);
+                else w.write(y_rows, w.row_at(m), kept(2 * m < left, fmaf(skip, xs[m], y) * g[m]));
             }
         }
         if (OUT && MULTI) {
@@ -492,7 +502,7 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
             if (gated) dzp[o] = from_f32<T>(0.0f);
         }
     int turn = 0;
-    T x[kOwn], dt[kOwn], z[kOwn], gy[kOwn], bv[w.M], cv[w.M];
+    uint32_t x[kOwn], dt[kOwn], z[kOwn], gy[kOwn], bv[w.M], cv[w.M];
     float mark[2][S], since = 0.0f;
     auto load = [&](int64_t t0) {
         w.get(w.at(ws + p.marks, t0 / kSsmTile), mark);
@@ -513,15 +523,16 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
 #pragma unroll
         for (int m = 0; m < kOwn; ++m) {
             const bool on = 2 * m < left, mine = on && w.own;
-            const float raw = to_f32(dt[m]) + bias, dy = to_f32(gy[m]);
+            const float raw = w.widen(dt[m]) + bias, dy = w.widen(gy[m]);
             float sl = 1.0f;
             const float soft = pinned(softplus(raw, &sl));
             dl[m] = on ? (a.softplus ? soft : raw) : 0.0f;
-            slope[m] = a.softplus ? pinned(sl) : 1.0f;
-            xs[m] = mine ? to_f32(x[m]) : 0.0f;
-            const float zf = gated ? to_f32(z[m]) : 0.0f, sg = logistic(zf), act = pinned(zf * sg);
-            g[m] = mine ? (gated ? dy * act : dy) : 0.0f;
-            dz[m] = dy * sg * fmaf(zf, 1.0f - sg, 1.0f);
+            const float rise = pinned(sl);
+            slope[m] = a.softplus ? rise : 1.0f;
+            xs[m] = mine ? w.widen(x[m]) : 0.0f;
+            const float zf = gated ? w.widen(z[m]) : 0.0f, sg = logistic(zf), act = pinned(zf * sg);
+            g[m] = kept(mine, dy * (gated ? act : 1.0f));
+            dz[m] = pinned(dy * sg * fmaf(zf, 1.0f - sg, 1.0f));
             w.store_du(du_of, m, dl[m], dl[m] * xs[m]);
             w.store_g(g_of, m, g[m]);
         }
@@ -539,7 +550,7 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
         wave_sync();
         if (t0 > w.begin) load(t0 - kSsmTile);
         const __amdgpu_buffer_rsrc_t dx_rows = w.rows_of(a.dx, t0), dd_rows = w.rows_of(a.ddt, t0);
-        const __amdgpu_buffer_rsrc_t dz_rows = w.rows_of(a.dgate, t0);
+        const __amdgpu_buffer_rsrc_t dz_rows = gated ? w.rows_of(a.dgate, t0) : w.no_rows();
 #pragma unroll
         for (int m = 0; m < kOwn; ++m) {
 
@@ -563,10 +574,10 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
                     part[2 * par + k] = y;
                 }
             }
-            if (gated) {
+            {
                 const float y = quad_sum(part, w.j);
                 if (MULTI) ex[0][(w.blk * kOwn + m) * 64 + w.lane] = y;
-                else w.write(dz_rows, w.row_at(m), 2 * m < left ? pinned(dz[m] * fmaf(skip, xs[m], y)) : 0.0f);
+                else w.write(dz_rows, w.row_at(m), kept(2 * m < left, dz[m] * fmaf(skip, xs[m], y)));
             }
         }
 #pragma unroll
@@ -615,8 +626,8 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
                 ex[1][(w.blk * kOwn + m) * 64 + w.lane] = du;
                 ex[2][(w.blk * kOwn + m) * 64 + w.lane] = dd;
             } else {
-                const float ddt = 2 * m < left ? pinned(fmaf(xs[m], du, dd) * slope[m]) : 0.0f;
-                w.write(dx_rows, w.row_at(m), 2 * m < left ? pinned(fmaf(dl[m], du, skip * g[m])) : 0.0f);
+                const float ddt = kept(2 * m < left, fmaf(xs[m], du, dd) * slope[m]);
+                w.write(dx_rows, w.row_at(m), kept(2 * m < left, fmaf(dl[m], du, skip * g[m])));
                 w.write(dd_rows, w.row_at(m), ddt);
                 dskip = fmaf(g[m], xs[m], dskip);
                 dbias += ddt;
@@ -628,8 +639,8 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
             for (int m = 0; m < kOwn; ++m)
                 if (m % p.blocks == w.blk) {
                     const float du = joined(ex[1], p.blocks, m, w.lane), dd = joined(ex[2], p.blocks, m, w.lane);
-                    const float ddt = 2 * m < left ? pinned(fmaf(xs[m], du, dd) * slope[m]) : 0.0f;
-                    w.write(dx_rows, w.row_at(m), 2 * m < left ? pinned(fmaf(dl[m], du, skip * g[m])) : 0.0f);
+                    const float ddt = kept(2 * m < left, fmaf(xs[m], du, dd) * slope[m]);
+                    w.write(dx_rows, w.row_at(m), kept(2 * m < left, fmaf(dl[m], du, skip * g[m])));
                     w.write(dd_rows, w.row_at(m), ddt);
                     if (gated)
                         w.write(dz_rows, w.row_at(m), 2 * m < left ? dz[m] * fmaf(skip, xs[m], joined(ex[0], p.blocks, m, w.lane)) : 0.0f);

@@ -19,7 +19,7 @@ _CONV = struct.Struct("=6q3q4qq2q4qqq2qq3q").pack
 _CONV_STEP = struct.Struct("=5q2q4q2qq2q").pack
 _SSM = struct.Struct("=7q3qq20qqqq4qq5q3qq3q").pack
 _SSM_STEP = struct.Struct("=6q3q20q3q2q").pack
-_NORM = struct.Struct("=5qd3q12q2q12q3q3q3q").pack
+_NORM = struct.Struct("=5qd3q12q2q8q3q3q3q").pack
 _NONE = (0, 0, 0, 0)
 
 EXPORTED = ("pn_short_conv", "pn_short_conv_backward", "pn_short_conv_workspace_bytes", "pn_short_conv_step", "pn_ssm_scan",
@@ -252,26 +252,25 @@ def block_norm(x, weight=None, residual=None, gate=None, post_weight=None, scale
     y = x.new_empty(shape) if weight is not None else None
     s = torch.empty(shape, dtype=rt, device=x.device)
     _run(dev, "pn_block_norm", _NORM(code, _DTYPES[rt], *sizes, float(eps), *w, *tok, *res, _at(y), s.data_ptr(), *_NONE, *_NONE,
-                                     *_NONE, 0, 0, 0, 0, 0, 0, 0, 0, _raw_stream(dev)))
+                                     0, 0, 0, 0, 0, 0, 0, 0, _raw_stream(dev)))
     return y, s
 
 
-def block_norm_backward(dy, ds, x, s, weight=None, gate=None, post_weight=None, scale=None, eps=1e-6):
-    """Gradients of ``block_norm`` from those of y (None without ``weight``) and s (None: 0), with the s that it returned:
-    (dx, dweight, dresidual, dgate, dpost_weight, dscale), None where the input is; dresidual is the residual's where there
-    was one, in s's type."""
+def block_norm_backward(dy, ds, x, weight=None, residual=None, gate=None, post_weight=None, scale=None, eps=1e-6):
+    """Gradients of ``block_norm`` from those of y (None without ``weight``) and s (None: 0): (dx, dweight, dresidual, dgate,
+    dpost_weight, dscale), None where the input is."""
     shape, sizes, dt, code, dev, tok, w = _norm_inputs(x, weight, gate, post_weight, scale)
-    rt = _residual_type(s, "s", dt)
-    stream = _rows(s, "s", rt, shape, dev)
+    rt = dt if residual is None else _residual_type(residual, "residual", dt)
+    res = _rows(residual, "residual", rt, shape, dev)
     gy = _rows(_given(dy, "dy"), "dy", dt, shape, dev) if weight is not None else _NONE
     gs = _rows(ds, "ds", rt, shape, dev)
-    dx, dr = x.new_empty(shape), torch.empty(shape, dtype=rt, device=x.device)
+    dx, dr = x.new_empty(shape), torch.empty(shape, dtype=rt, device=x.device) if residual is not None else None
     dz = x.new_empty(shape) if gate is not None else None
     dw, dpw, dsc = (torch.empty_like(t) if t is not None else None for t in (weight, post_weight, scale))
 
     def block(ws, nbytes):
-        return _NORM(code, _DTYPES[rt], *sizes, float(eps), *w, *tok, *_NONE, 0, 0, *gy, *gs, *stream, dx.data_ptr(), _at(dz),
-                     dr.data_ptr(), _at(dw), _at(dpw), _at(dsc), ws, nbytes, _raw_stream(dev))
+        return _NORM(code, _DTYPES[rt], *sizes, float(eps), *w, *tok, *res, 0, 0, *gy, *gs, dx.data_ptr(), _at(dz), _at(dr),
+                     _at(dw), _at(dpw), _at(dsc), ws, nbytes, _raw_stream(dev))
 
     key = ("norm", code, *sizes, weight is None, post_weight is None, scale is None)
     ws, at, size = _workspace(x, "pn_block_norm_workspace_bytes", key, block(0, 0))

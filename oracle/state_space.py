@@ -161,9 +161,9 @@ def block_norm(x, weight=None, residual=None, gate=None, post_weight=None, scale
     return None if weight is None else s / np.sqrt((s * s).mean(-1, keepdims=True) + eps) * _f(weight), s
 
 
-def block_norm_backward(dy, ds, x, s, weight=None, gate=None, post_weight=None, scale=None, eps=1e-6):
-    """((dx, dweight, dresidual, dgate, dpost_weight, dscale), the same sums over absolute values), s as it is given."""
-    x, s = _f(x), _f(s)
+def block_norm_backward(dy, ds, x, weight=None, residual=None, gate=None, post_weight=None, scale=None, eps=1e-6):
+    """((dx, dweight, dresidual, dgate, dpost_weight, dscale), the same sums over absolute values)."""
+    x = _f(x)
     act, slope = 1.0, None
     if gate is not None:
         z = _f(gate)
@@ -171,6 +171,9 @@ def block_norm_backward(dy, ds, x, s, weight=None, gate=None, post_weight=None, 
         act, slope = z * l, l * (1.0 + z * (1.0 - l))
     u = x * act
     sc = 1.0 if scale is None else _f(scale)
+    ru = 1.0 if post_weight is None else 1.0 / np.sqrt((u * u).mean(-1, keepdims=True) + eps)
+    res = 0.0 if residual is None else _f(residual)
+    p = sc * u * ru * (1.0 if post_weight is None else _f(post_weight))
     lead = tuple(range(x.ndim - 1))
     both = []
     for f in (lambda v: v, np.abs):
@@ -178,13 +181,13 @@ def block_norm_backward(dy, ds, x, s, weight=None, gate=None, post_weight=None, 
         t = np.zeros_like(x) if ds is None else f(_f(ds))
         dw = dpw = dsc = dz = None
         if weight is not None:
+            s = res + p
             rs = 1.0 / np.sqrt((s * s).mean(-1, keepdims=True) + eps)
-            m, e = s * rs, _f(dy) * _f(weight)
-            t = t + rs * (f(e) + sign * f(m) * f(e * m).mean(-1, keepdims=True))
-            dw = f(_f(dy) * m).sum(lead)
+            m, e = (f(res) + f(p)) * rs, f(_f(dy) * _f(weight))
+            t = t + rs * (e + sign * m * (e * m).mean(-1, keepdims=True))
+            dw = (f(_f(dy)) * m).sum(lead)
         dr, du = t, f(np.broadcast_to(sc, t.shape)) * t
         if post_weight is not None:
-            ru = 1.0 / np.sqrt((u * u).mean(-1, keepdims=True) + eps)
             n, pw = u * ru, _f(post_weight)
             dpw = (du * f(n)).sum(lead)
             dsc = (t * f(pw * n)).sum(lead)
@@ -194,5 +197,6 @@ def block_norm_backward(dy, ds, x, s, weight=None, gate=None, post_weight=None, 
             dsc = (t * f(u)).sum(lead)
         if gate is not None:
             dz = du * f(x * slope)
-        both.append((du * f(np.broadcast_to(act, du.shape)), dw, dr, dz, dpw, dsc if scale is not None else None))
+        both.append((du * f(np.broadcast_to(act, du.shape)), dw, dr if residual is not None else None, dz, dpw,
+                     dsc if scale is not None else None))
     return tuple(both)

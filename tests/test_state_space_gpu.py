@@ -482,9 +482,13 @@ def check_norm(a, dtype, rdtype, eps=1e-5, backward=True):
         _close(y, wy, _bound(dtype, wy, np.abs(h["weight"]) * rs * se + np.abs(wy) * (far + 40 * U)), "y")
     if not backward:
         return
-    got = pn.block_norm_backward(a["dy"] if a["weight"] is not None else None, a["ds"], a["x"], s, a["weight"], eps=eps, **kw)
-    want, mag = ref.block_norm_backward(h["dy"], h["ds"], h["x"], _np(s), h["weight"], eps=eps, **hk)
-    n = (8 * zmax + 160) * U
+    got = pn.block_norm_backward(a["dy"] if a["weight"] is not None else None, a["ds"], a["x"], a["weight"],
+                                 residual=a["residual"], eps=eps, **kw)
+    want, mag = ref.block_norm_backward(h["dy"], h["ds"], h["x"], h["weight"], h["residual"], eps=eps, **hk)
+    # the roundings of s are relative to its terms, |residual| + |p|, and so is what they do to its norm
+    terms = np.abs(p) + (0.0 if h["residual"] is None else np.abs(h["residual"]))
+    far = np.sqrt((terms ** 2).sum(-1) / np.maximum((ws ** 2).sum(-1), 1e-300)).max()
+    n = (8 * zmax + 160) * (1.0 + far) * U
     for x, w, m, name in zip(got, want, mag, ("dx", "dweight", "dresidual", "dgate", "dpost_weight", "dscale")):
         if w is None:
             assert x is None, name
@@ -554,11 +558,11 @@ def test_norm_of_wide_rows_is_captured():
     kw = {k: a[k] for k in ("gate", "post_weight", "scale")}
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        out = pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["residual"], a["weight"], **kw)
+        out = pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["weight"], residual=a["residual"], **kw)
     for i in range(3):
         a["dy"].mul_(1.5)
         graph.replay()
-        want = pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["residual"], a["weight"], **kw)
+        want = pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["weight"], residual=a["residual"], **kw)
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(out, want)), i
 
@@ -568,7 +572,7 @@ def test_norm_without_tokens():
     kw = {k: a[k] for k in ("gate", "post_weight", "scale")}
     y, s = pn.block_norm(a["x"], a["weight"], residual=a["residual"], **kw)
     assert y.shape == (2, 0, 64) and s.dtype is torch.float32
-    back = pn.block_norm_backward(a["dy"], a["ds"], a["x"], s, a["weight"], **kw)
+    back = pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["weight"], residual=a["residual"], **kw)
     assert not any(back[i].any() for i in (1, 4, 5))
 
 
@@ -606,7 +610,8 @@ def _calls():
         ("scan step", one, lambda a: (pn.ssm_step(*(a[k] for k in ("x", "dt", "A", "b", "c")), a["initial_state"], **pick(a, ks[:3])),
                                       a["initial_state"])),
         ("norm", n, lambda a: pn.block_norm(a["x"], a["weight"], residual=a["residual"], **pick(a, kn))),
-        ("norm gradients", n, lambda a: pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["residual"], a["weight"], **pick(a, kn))),
+        ("norm gradients", n, lambda a: pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["weight"], residual=a["residual"],
+                                                                **pick(a, kn))),
     ]
 
 

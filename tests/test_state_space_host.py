@@ -106,7 +106,8 @@ def test_scan_gradient_against_differences(softplus):
     assert all((m >= np.abs(v) - 1e-12).all() for v, m in zip(grads, bounds))
 
 
-@pytest.mark.parametrize("drop", [(), ("gate",), ("post_weight",), ("scale",), ("weight",), ("gate", "post_weight", "scale")])
+@pytest.mark.parametrize("drop", [(), ("gate",), ("post_weight",), ("scale",), ("weight",), ("gate", "post_weight", "scale"),
+                                  ("residual",), ("residual", "post_weight")])
 def test_norm_gradient_against_differences(drop):
     g = _rng(5)
     a = dict(x=g.standard_normal((2, 3, 5)), residual=g.standard_normal((2, 3, 5)), gate=g.standard_normal((2, 3, 5)),
@@ -118,8 +119,7 @@ def test_norm_gradient_against_differences(drop):
         y, s = ref.block_norm(**a, eps=eps)
         return float((0.0 if y is None else (y * dy).sum()) + (s * ds).sum())
 
-    kw = {k: v for k, v in a.items() if k != "residual"}
-    grads, mags = ref.block_norm_backward(dy, ds, s=ref.block_norm(**a, eps=eps)[1], **kw, eps=eps)
+    grads, mags = ref.block_norm_backward(dy, ds, **a, eps=eps)
     named = dict(zip(("x", "weight", "residual", "gate", "post_weight", "scale"), grads))
     assert all((v is None) == (k not in a) for k, v in named.items())
     _differences(loss, a, {k: v for k, v in named.items() if v is not None})
@@ -257,9 +257,9 @@ def test_scan_step_refusals(kw, code):
 
 
 def _norm(dtype=1, rdtype=0, B=2, T=2, D=8, eps=1e-6, w=3 * GIB, pw=4 * GIB, sc=5 * GIB, x=TOK(6), z=TOK(7), r=TOK(8), y=9 * GIB,
-          s=10 * GIB, dy=TOK(11), ds=TOK(12), s_in=TOK(13), dx=14 * GIB, dz=15 * GIB, dr=16 * GIB, dw=17 * GIB, dpw=18 * GIB,
+          s=10 * GIB, dy=TOK(11), ds=TOK(12), dx=14 * GIB, dz=15 * GIB, dr=16 * GIB, dw=17 * GIB, dpw=18 * GIB,
           dsc=19 * GIB, ws=0, wsn=0):
-    return ss._NORM(dtype, rdtype, B, T, D, eps, w, pw, sc, *x, *z, *r, y, s, *dy, *ds, *s_in, dx, dz, dr, dw, dpw, dsc, ws, wsn, 0)
+    return ss._NORM(dtype, rdtype, B, T, D, eps, w, pw, sc, *x, *z, *r, y, s, *dy, *ds, dx, dz, dr, dw, dpw, dsc, ws, wsn, 0)
 
 
 @pytest.mark.parametrize("kw, code", [
@@ -281,8 +281,8 @@ def test_norm_outputs_and_workspace():
     n = pn.lib().pn_block_norm_workspace_bytes(_norm())
     assert b(_norm()) == b(_norm(ws=40 * GIB, wsn=n - 1)) == b(_norm(ws=40 * GIB + 8, wsn=n)) == pn.EWORKSPACE
     ok = dict(ws=40 * GIB, wsn=n)
-    for kw in (dict(dx=0), dict(dz=0), dict(dw=0), dict(dpw=0), dict(dsc=0), dict(dy=TOK(0)), dict(s_in=TOK(0)), dict(dx=6 * GIB),
-               dict(dr=12 * GIB), dict(dz=14 * GIB), dict(dr=16 * GIB + 2)):
+    for kw in (dict(dx=0), dict(dz=0), dict(dw=0), dict(dpw=0), dict(dsc=0), dict(dy=TOK(0)), dict(dx=6 * GIB),
+               dict(dr=8 * GIB), dict(dr=12 * GIB), dict(dz=14 * GIB), dict(dr=16 * GIB + 2)):
         assert b(_norm(**{**ok, **kw})) == pn.EINVAL, kw
     assert pn.lib().pn_block_norm_workspace_bytes(_norm(w=0, pw=0, sc=0)) == 256
     assert pn.lib().pn_block_norm_workspace_bytes(_norm(D=0)) == 0 and pn.last_error() != ""
