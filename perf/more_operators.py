@@ -213,7 +213,7 @@ def _run_own(s):
         y, r = pn.block_norm(s["x"], s["w"], residual=s["r"], **kw)
         if not s["train"]:
             return y, r
-        back = pn.block_norm_backward(s["dy"], s["ds"], s["x"], r, s["w"], **kw)
+        back = pn.block_norm_backward(s["dy"], s["ds"], s["x"], s["w"], residual=s["r"], **kw)
         return (y, r) + tuple(t for t in back if t is not None)
     kw = dict(skip=s["skip"], gate=s["gate"], dt_bias=s["dt_bias"])
     if op == "scan_step":
