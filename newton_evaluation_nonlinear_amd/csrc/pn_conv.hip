@@ -4,14 +4,21 @@
 //     dx_t = sum_k w_k d_{t+W-1-k},   dw_k = sum_t d_t x_{t-W+1+k},   dbias = sum_t d_t,
 // and its single-token form.
 //
-// Bound: bytes.  A thread takes V adjacent channels (8 bytes where sizes,
-// strides and alignment allow, one channel otherwise) and walks `run` tokens
-// with the last W - 1 in registers, so that a token is read once and, at the
-// ends of runs, W - 1 times more.  (16 bytes at a time take twice the
-// registers and leave too few waves: 62 us where 8 take 50, 8 x 4096 tokens of
-// 2048 channels in bfloat16.)
+// Bound: bytes.  A thread takes V adjacent channels (8 bytes in the forward, two
+// channels in the gradients, where sizes, strides and alignment allow, one
+// channel otherwise) and walks `run` tokens with the last W - 1 in registers, so
+// that a token is read once and, at the ends of runs, W - 1 times more.  Wider
+// vectors leave too few waves: 16 bytes take 62 us where 8 take 50 (8 x 4096
+// tokens of 2048 channels, 4 taps, bfloat16), the gradients of four channels 123
+// where two take 104.  The number of taps is known to the compiler: with a
+// branch a tap the gradients of 3 and 8 taps take 209 and 419 us, not 94 and 168.
+//
+// Measured at that size: 50 us, 5.4 TB/s (part of it from the cache); gradients
+// 104, 3.9 TB/s, and 7 for the sums; in float32 105 and 186, 5.1 and 4.3 TB/s.
+// Single tokens of 256 x 4096 channels 6.6 us.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pn_ssm.hpp"
 #include "pn_ssm_device.hpp"
@@ -55,13 +62,13 @@ __device__ __forceinline__ void token(const pn_conv_args& a, int64_t b, int64_t 
     }
 }
 
-// The taps of V channels in their places (P: see Taps below), 0 in the others.
-template <int V, typename P>
-__device__ __forceinline__ void weights(const pn_conv_args& a, const P& taps, int d, float (*w)[V]) {
+// The taps of V channels.
+template <int V, int W>
+__device__ __forceinline__ void weights(const float* weight, int d, float (*w)[V]) {
 #pragma unroll
-    for (int k = 0; k < P::K; ++k)
+    for (int k = 0; k < W; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) w[k][i] = taps.at(k) ? a.weight[(d + i) * a.W + k - taps.first] : 0.0f;
+        for (int i = 0; i < V; ++i) w[k][i] = weight[static_cast<int64_t>(d + i) * W + k];
 }
 
 struct Place {
@@ -84,25 +91,11 @@ __device__ __forceinline__ int64_t length(const pn_conv_args& a, int64_t b) {
     return a.lengths ? max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.lengths[b]), a.T)) : a.T;
 }
 
-// Places for taps: K of them hold W, or exactly W taps (known then, without a
-// branch a tap).  Four tokens at a time; the next four are loaded before the
-// products of these.
-template <int K_, bool EXACT_>
-struct Taps {
-    static constexpr int K = K_;
-    static constexpr bool EXACT = EXACT_;
-    int first;               // place of the first tap
-    __host__ __device__ __forceinline__ explicit Taps(int64_t W) : first(EXACT ? 0 : K - static_cast<int>(W)) {}
-    __device__ __forceinline__ bool at(int k) const { return EXACT || k >= first; }
-};
-
-template <typename T, int V, typename P>
+// Four tokens at a time; the next four are loaded before the products of these.
+template <typename T, int V, int W>
 __global__ __launch_bounds__(kBlock) void conv(pn_conv_args a, ConvCut c) {
-    constexpr int K = P::K;
     const Place p = place<V>(a, c);
     if (!p.on) return;
-    const P taps(a.W);
-    const int W = P::EXACT ? K : static_cast<int>(a.W);
     const int64_t n = length(a, p.b), t0 = p.run * c.run, t1 = min(t0 + c.run, a.T), end = min(t1, n);
     T* y = static_cast<T*>(a.y) + p.b * a.T * a.D + p.d;
     if (p.run == 0 && a.final_state)
@@ -112,13 +105,12 @@ __global__ __launch_bounds__(kBlock) void conv(pn_conv_args a, ConvCut c) {
             store<T, V>(static_cast<T*>(a.final_state) + (p.b * (W - 1) + r) * a.D + p.d, v);
         }
     if (t0 < end) {
-        float w[K][V], bias[V], x[K - 1 + 4][V];
-        weights<V>(a, taps, p.d, w);
+        float w[W][V], bias[V], x[W - 1 + 4][V];
+        weights<V, W>(a.weight, p.d, w);
 #pragma unroll
         for (int i = 0; i < V; ++i) bias[i] = a.bias ? a.bias[p.d + i] : 0.0f;
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k)
-            if (taps.at(k)) token<T, V>(a, p.b, t0 - (K - 1) + k, n, p.d, x[k]);
+        for (int k = 0; k < W - 1; ++k) token<T, V>(a, p.b, t0 - (W - 1) + k, n, p.d, x[k]);
         const T* row = static_cast<const T*>(a.x.p) + p.b * a.x.sb + p.d;
         Pack<T, V> next[4];
         auto fetch = [&](int64_t t) {                    // rows behind the last are the last again: not stored
@@ -130,7 +122,7 @@ __global__ __launch_bounds__(kBlock) void conv(pn_conv_args a, ConvCut c) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < V; ++i) x[K - 1 + j][i] = to_f32(next[j].v[i]);
+                for (int i = 0; i < V; ++i) x[W - 1 + j][i] = to_f32(next[j].v[i]);
             if (t + 4 < end) fetch(t + 4);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -138,17 +130,16 @@ __global__ __launch_bounds__(kBlock) void conv(pn_conv_args a, ConvCut c) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[i] = bias[i];
 #pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (taps.at(k))                      // taps that are not there touch no token
+                for (int k = 0; k < W; ++k)
 #pragma unroll
-                        for (int i = 0; i < V; ++i) v[i] = fmaf(w[k][i], x[j + k][i], v[i]);
+                    for (int i = 0; i < V; ++i) v[i] = fmaf(w[k][i], x[j + k][i], v[i]);
                 if (a.activation)
 #pragma unroll
                     for (int i = 0; i < V; ++i) v[i] *= logistic(v[i]);
                 if (t + j < end) store<T, V>(y + (t + j) * a.D, v);
             }
 #pragma unroll
-            for (int k = 0; k < K - 1; ++k)
+            for (int k = 0; k < W - 1; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i) x[k][i] = x[k + 4][i];
         }
@@ -159,26 +150,23 @@ __global__ __launch_bounds__(kBlock) void conv(pn_conv_args a, ConvCut c) {
 
 // Gradients.  The walk goes over tokens t0 .. t1 + W - 2: each gives d_t from
 // its W tokens, and with it dx of the token W - 1 before.
-template <typename T, int V, typename P>
+template <typename T, int V, int W>
 __global__ __launch_bounds__(kBlock) void conv_backward(pn_conv_args a, ConvCut c, float* part) {
-    constexpr int K = P::K;
+    constexpr int past = W - 1;
     const Place p = place<V>(a, c);
     if (!p.on) return;
-    const P taps(a.W);
-    const int W = P::EXACT ? K : static_cast<int>(a.W), past = W - 1;
     const int64_t n = length(a, p.b), t0 = p.run * c.run, t1 = min(t0 + c.run, a.T);
-    float w[K][V], bias[V], x[K][V], d[K][V], dw[K][V], db[V];
-    weights<V>(a, taps, p.d, w);
+    float w[W][V], bias[V], x[W][V], d[W][V], dw[W][V], db[V];
+    weights<V, W>(a.weight, p.d, w);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         bias[i] = a.bias ? a.bias[p.d + i] : 0.0f;
         db[i] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) dw[k][i] = d[k][i] = x[k][i] = 0.0f;
+        for (int k = 0; k < W; ++k) dw[k][i] = d[k][i] = x[k][i] = 0.0f;
     }
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k)
-        if (taps.at(k)) token<T, V>(a, p.b, t0 - (K - 1) + k, n, p.d, x[k + 1]);
+    for (int k = 0; k < W - 1; ++k) token<T, V>(a, p.b, t0 - (W - 1) + k, n, p.d, x[k + 1]);
     const T* xrow = static_cast<const T*>(a.x.p) + p.b * a.x.sb + p.d;
     const T* grow = static_cast<const T*>(a.dy.p) + p.b * a.dy.sb + p.d;
     constexpr int AHEAD = 4;                             // tokens loaded at a time, while those before are worked on
@@ -192,8 +180,61 @@ __global__ __launch_bounds__(kBlock) void conv_backward(pn_conv_args a, ConvCut 
             ng[j] = *reinterpret_cast<const Pack<T, V>*>(grow + t * a.dy.st);
         }
     };
+    // x[k] and d[k]: of token t - (W - 1) + k.  Whole: all tokens up to the tile's
+    // end are the run's and the sequence's and dx is the run's, so that nothing
+    // is looked up.
+    auto tile = [&](int64_t s, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int64_t t = s + j;
+            if (!WHOLE && t >= t1 + past) break;
+            const bool on = WHOLE || t < n;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) {
+                    d[k][i] = d[k + 1][i];
+                    x[k][i] = x[k + 1][i];
+                }
+                x[W - 1][i] = on ? to_f32(cx[j].v[i]) : 0.0f;
+                float pre = bias[i];
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    pre = fmaf(w[k][i], x[k][i], pre);
+                const float g = to_f32(cg[j].v[i]), q = logistic(pre), by = a.activation ? q * fmaf(pre, 1.0f - q, 1.0f) : 1.0f;
+                d[W - 1][i] = on ? g * by : 0.0f;
+            }
+            if (WHOLE || t < t1)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    db[i] += d[W - 1][i];
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+                        dw[k][i] = fmaf(d[W - 1][i], x[k][i], dw[k][i]);
+                }
+            const int64_t at = t - past;                 // W - 1 tokens back: d[W - W + q] is that of token at + q
+            if (!WHOLE && at < t0 && !(p.run == 0 && a.d_initial_state)) continue;
+            float v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[i] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    v[i] = fmaf(w[k][i], d[W - 1 - k][i], v[i]);
+                if (!WHOLE && at >= n) v[i] = 0.0f;
+            }
+            if (!WHOLE && a.d_final_state && at < n && at >= n - past) {
+                float f[V];
+                load<T, V>(static_cast<const T*>(a.d_final_state) + (p.b * past + at - (n - past)) * a.D + p.d, f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] += f[i];
+            }
+            if (WHOLE || at >= 0) store<T, V>(static_cast<T*>(a.dx) + (p.b * a.T + at) * a.D + p.d, v);
+            else store<T, V>(static_cast<T*>(a.d_initial_state) + (p.b * past + past + at) * a.D + p.d, v);
+        }
+    };
     fetch(t0);
-    // x[k] and d[k]: of token t - (K - 1) + k
     for (int64_t s = t0; s < t1 + past; s += AHEAD) {
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
@@ -201,64 +242,15 @@ __global__ __launch_bounds__(kBlock) void conv_backward(pn_conv_args a, ConvCut 
             cg[j] = ng[j];
         }
         if (s + AHEAD < t1 + past) fetch(s + AHEAD);
-#pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-            const int64_t t = s + j;
-            if (t >= t1 + past) break;
-            const bool on = t < n;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-#pragma unroll
-                for (int k = 0; k < K - 1; ++k) {
-                    d[k][i] = d[k + 1][i];
-                    x[k][i] = x[k + 1][i];
-                }
-                x[K - 1][i] = on ? to_f32(cx[j].v[i]) : 0.0f;
-                float pre = bias[i], g = on ? to_f32(cg[j].v[i]) : 0.0f;
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (taps.at(k)) pre = fmaf(w[k][i], x[k][i], pre);
-                if (a.activation) {
-                    const float q = logistic(pre);
-                    g = on ? g * q * fmaf(pre, 1.0f - q, 1.0f) : 0.0f;
-                }
-                d[K - 1][i] = g;
-            }
-            if (t < t1)
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    db[i] += d[K - 1][i];
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        if (taps.at(k)) dw[k][i] = fmaf(d[K - 1][i], x[k][i], dw[k][i]);
-                }
-            const int64_t at = t - past;                 // W - 1 tokens back: d[K - W + q] is that of token at + q
-            if (at < t0 && !(p.run == 0 && a.d_initial_state)) continue;
-            float v[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                v[i] = 0.0f;
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (taps.at(k)) v[i] = fmaf(w[k][i], d[K - 1 - (k - taps.first)][i], v[i]);
-                if (at >= n) v[i] = 0.0f;
-            }
-            if (a.d_final_state && at < n && at >= n - past) {
-                float f[V];
-                load<T, V>(static_cast<const T*>(a.d_final_state) + (p.b * past + at - (n - past)) * a.D + p.d, f);
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[i] += f[i];
-            }
-            if (at >= 0) store<T, V>(static_cast<T*>(a.dx) + (p.b * a.T + at) * a.D + p.d, v);
-            else store<T, V>(static_cast<T*>(a.d_initial_state) + (p.b * past + past + at) * a.D + p.d, v);
-        }
+        if (s - past >= t0 && s + AHEAD <= min(t1, n)) tile(s, std::true_type());
+        else tile(s, std::false_type());
     }
     float* q = part + (p.b * c.runs + p.run) * (W + 1) * a.D;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (taps.at(k)) q[(p.d + i) * a.W + k - taps.first] = dw[k][i];
+        for (int k = 0; k < W; ++k)
+            q[(p.d + i) * a.W + k] = dw[k][i];
         q[a.W * a.D + p.d + i] = db[i];
     }
 }
@@ -270,11 +262,13 @@ __global__ __launch_bounds__(kBlock) void conv_state_gradient(const T* d_final, 
     if (i < n) d_initial[i] = d_final ? d_final[i] : from_f32<T>(0.0f);
 }
 
-template <typename T, int V>
+// A channel's taps are read together: one by one, a line of memory a lane, they
+// take longer than the states (14.6 us where the call above takes 6.6).
+template <typename T, int V, int W>
 __global__ __launch_bounds__(kBlock) void conv_step(pn_conv_step_args a, int vecs) {
     const int64_t id = static_cast<int64_t>(block_id()) * kBlock + threadIdx.x, b = id / vecs;
     if (b >= a.B) return;
-    const int d = static_cast<int>(id - b * vecs) * V, W = static_cast<int>(a.W);
+    const int d = static_cast<int>(id - b * vecs) * V;
     const int64_t slot = a.slots ? a.slots[b] : b;
     T* y = static_cast<T*>(a.y) + b * a.D + d;
     float v[V];
@@ -285,20 +279,19 @@ __global__ __launch_bounds__(kBlock) void conv_step(pn_conv_step_args a, int vec
         return;
     }
     T* s = static_cast<T*>(a.state) + slot * (W - 1) * a.D + d;
-    Pack<T, V> row[8];
+    Pack<T, V> row[W];
 #pragma unroll
-    for (int k = 0; k < 7; ++k)
-        if (k < W - 1) row[k] = *reinterpret_cast<const Pack<T, V>*>(s + k * a.D);
-    const Pack<T, V> x = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(a.x.p) + b * a.x.sb + d);
+    for (int k = 0; k < W - 1; ++k) row[k] = *reinterpret_cast<const Pack<T, V>*>(s + k * a.D);
+    row[W - 1] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(a.x.p) + b * a.x.sb + d);
+    float w[W][V];
+    weights<V, W>(a.weight, d, w);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = a.bias ? a.bias[d + i] : 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        if (k > W - 1) continue;
-        const Pack<T, V> t = k == W - 1 ? x : row[k];
-        if (k > 0) *reinterpret_cast<Pack<T, V>*>(s + (k - 1) * a.D) = t;
+    for (int k = 0; k < W; ++k) {
+        if (k > 0) *reinterpret_cast<Pack<T, V>*>(s + (k - 1) * a.D) = row[k];
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = fmaf(a.weight[static_cast<int64_t>(d + i) * W + k], to_f32(t.v[i]), v[i]);
+        for (int i = 0; i < V; ++i) v[i] = fmaf(w[k][i], to_f32(row[k].v[i]), v[i]);
     }
     if (a.activation)
 #pragma unroll
@@ -324,12 +317,19 @@ ConvCut cut(const pn_conv_args& a, int V, int least) {
     return c;
 }
 
-// f(places for W taps): exact for 4, the usual number.
+// f(the number of taps, known to the compiler: no branch a tap).
 template <typename F>
 hipError_t with_taps(int64_t W, F f) {
-    if (W == 4) return f(Taps<4, true>(W));
-    if (W < 4) return f(Taps<4, false>(W));
-    return f(Taps<8, false>(W));
+    switch (W) {
+        case 1: return f(std::integral_constant<int, 1>());
+        case 2: return f(std::integral_constant<int, 2>());
+        case 3: return f(std::integral_constant<int, 3>());
+        case 4: return f(std::integral_constant<int, 4>());
+        case 5: return f(std::integral_constant<int, 5>());
+        case 6: return f(std::integral_constant<int, 6>());
+        case 7: return f(std::integral_constant<int, 7>());
+        default: return f(std::integral_constant<int, 8>());
+    }
 }
 
 template <typename T>
@@ -339,9 +339,9 @@ hipError_t conv_typed(const pn_conv_args& a, hipStream_t st) {
     const ConvCut c = cut(a, wide ? V : 1, 8);
     const dim3 grid = grid_of((a.B * c.runs * c.vecs + kBlock - 1) / kBlock, kBlock);
     return with_taps(a.W, [&](auto taps) {
-        using P = decltype(taps);
-        if (wide) conv<T, V, P><<<grid, kBlock, 0, st>>>(a, c);
-        else conv<T, 1, P><<<grid, kBlock, 0, st>>>(a, c);
+        constexpr int W = decltype(taps)::value;
+        if (wide) conv<T, V, W><<<grid, kBlock, 0, st>>>(a, c);
+        else conv<T, 1, W><<<grid, kBlock, 0, st>>>(a, c);
         return hipGetLastError();
     });
 }
@@ -350,7 +350,7 @@ hipError_t conv_typed(const pn_conv_args& a, hipStream_t st) {
 // does not depend on alignment.
 template <typename T>
 hipError_t backward_typed(const pn_conv_args& a, hipStream_t st) {
-    constexpr int V = 8 / sizeof(T);
+    constexpr int V = 2;
     const bool wide = aligned(a.D, sizeof(T), V, strides(a.x, a.B, a.T) | strides(a.dy, a.B, a.T), a.x.p, a.dy.p,
                               a.initial_state, a.d_final_state, a.dx, a.d_initial_state);
     ConvCut c = cut(a, 1, 16);
@@ -358,9 +358,9 @@ hipError_t backward_typed(const pn_conv_args& a, hipStream_t st) {
     const dim3 grid = grid_of((a.B * c.runs * c.vecs + kBlock - 1) / kBlock, kBlock);
     float* part = static_cast<float*>(a.workspace);
     const hipError_t e = with_taps(a.W, [&](auto taps) {
-        using P = decltype(taps);
-        if (wide) conv_backward<T, V, P><<<grid, kBlock, 0, st>>>(a, c, part);
-        else conv_backward<T, 1, P><<<grid, kBlock, 0, st>>>(a, c, part);
+        constexpr int W = decltype(taps)::value;
+        if (wide) conv_backward<T, V, W><<<grid, kBlock, 0, st>>>(a, c, part);
+        else conv_backward<T, 1, W><<<grid, kBlock, 0, st>>>(a, c, part);
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -373,9 +373,12 @@ hipError_t step_typed(const pn_conv_step_args& a, hipStream_t st) {
     const bool wide = aligned(a.D, sizeof(T), V, a.B > 1 ? a.x.sb : 0, a.x.p, a.state, a.y);
     const int vecs = static_cast<int>(wide ? a.D / V : a.D);
     const dim3 grid = grid_of((a.B * vecs + kBlock - 1) / kBlock, kBlock);
-    if (wide) conv_step<T, V><<<grid, kBlock, 0, st>>>(a, vecs);
-    else conv_step<T, 1><<<grid, kBlock, 0, st>>>(a, vecs);
-    return hipGetLastError();
+    return with_taps(a.W, [&](auto taps) {
+        constexpr int W = decltype(taps)::value;
+        if (wide) conv_step<T, V, W><<<grid, kBlock, 0, st>>>(a, vecs);
+        else conv_step<T, 1, W><<<grid, kBlock, 0, st>>>(a, vecs);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace
