@@ -513,10 +513,10 @@ int pn_short_conv_step(const pn_conv_step_args* a);
  * D a multiple of G: channel d reads group d / (D / G).  A is finite, < 0 in
  * use; growth is allowed as far as exp(A[d] sum delta) over the tokens is
  * finite in float32.  The token strides of x, dt, gate, b, c and dy go up to
- * 2^26 elements, D up to 2^24.  Steps and decays are float32: exp(delta A) to (2 |delta A| + 2) 2^-24 of itself,
- * 0 below 2^-126.  A NaN or infinity in a token reaches that token's outputs
- * and those after it (in the gradients also those before it), as NaN or
- * infinity. */
+ * 2^26 elements, D up to 2^24.  Steps and decays are float32: exp(delta A) to
+ * (2 |delta A| + 2) 2^-24 of itself, 0 below 2^-126.  A NaN or infinity in a
+ * token reaches that token's outputs and those after it (in the gradients also
+ * those before it), as NaN or infinity. */
 typedef struct pn_ssm_args {
     int64_t dtype, B, T, D, N, G, softplus;
     const float *A, *skip, *dt_bias;    /* [D, N]; [D] or NULL; [D] or NULL       */

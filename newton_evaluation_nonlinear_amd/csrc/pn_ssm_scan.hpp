@@ -15,11 +15,25 @@
 // belong to.  More than 16 states are blocks of 16 in as many waves, which add
 // their shares of such sums through LDS.
 //
-// Bound: instructions.  A state and token take an exponential (9 cycles of a
-// SIMD, which does nothing else meanwhile) and 3 to 4 products and sums (2.5
-// each, from two waves on).  So waves are kept small: four channels a quad
-// need a fourth fewer instructions for the sums over channels, but twice the
-// registers, and then the SIMD waits.
+// Bound: instructions, of which a state and token take an exponential, three
+// products and sums to move it, one for y, and nine and a second exponential
+// for its gradients.  On one SIMD an exponential takes 3.5 ns, a product or sum
+// of vector registers 1.1 where two waves issue them together and 2.1 alone, a
+// DPP move or a product with a scalar register 1.8; eight states moved by a
+// token (8 exponentials, 24 others) 64 ns, in whatever order and from one wave
+// on to eight.  So a tile is kept free of branches (rows past the end and
+// channels that do not exist are left to range-checked buffer accesses, values
+// that are not wanted to selects), and waves are kept small: with four channels
+// a quad the gradients spilled and took 2490 us where they now take 1000.  The
+// vector units are busy more than 90 % of the time in kSsmEnds, kSsmOutputs
+// (where channels fill the device) and kSsmMarksBoth, and 80 % in the
+// gradients, which hold 238 registers and run two waves on a SIMD.
+//
+// Measured, bfloat16, 16 states (us, medians of traced calls): 65536 tokens of
+// 2048 channels: ends 431, outputs 668 (1.0 TB/s in all); 8 x 4096 tokens of
+// 2048 channels: ends 195, outputs 301, marks 359, gradients 1005, the sums of db
+// and dc 23.  4 x 4096 tokens of 512 channels with 128 states, as many states in
+// all as the second: ends 183, outputs 296, gradients 1025, sums 81.
 //
 // Time.  Where channels do not fill the device the tokens are cut into
 // segments: a first pass takes the state that a segment leaves alone
