@@ -40,11 +40,14 @@ __device__ __forceinline__ void load(const T* p, float* v) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = to_f32(q.v[i]);
 }
+// Binary16 is rounded from the float32 value everywhere: a product and sum that
+// round to 16 bits at once, where the compiler finds them, would make a token's
+// last bit depend on its place in a run.
 template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const float* v) {
     Pack<T, V> q;
 #pragma unroll
-    for (int i = 0; i < V; ++i) q.v[i] = from_f32<T>(v[i]);
+    for (int i = 0; i < V; ++i) q.v[i] = from_f32<T>(std::is_same<T, f16>::value ? pinned(v[i]) : v[i]);
     *reinterpret_cast<Pack<T, V>*>(p) = q;
 }
 

@@ -567,7 +567,6 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
         const __amdgpu_buffer_rsrc_t dz_rows = gated ? w.rows_of(a.dgate, t0) : w.no_rows();
 #pragma unroll
         for (int m = 0; m < kOwn; ++m) {
-
             float part[4];
 #pragma unroll
             for (int par = 0; par < 2; ++par) {
@@ -596,7 +595,6 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
         }
 #pragma unroll
         for (int m = kOwn - 1; m >= 0; --m) {
-
             float s1[4], s2[4];
 #pragma unroll
             for (int par = 1; par >= 0; --par) {

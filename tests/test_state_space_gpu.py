@@ -164,6 +164,38 @@ def test_conv_without_tokens():
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("W", [1, 3, 4, 5, 8])
+def test_conv_many_sequences_are_the_few(dtype, W):
+    """Where there are many sequences a thread takes longer runs of tokens: outputs and token gradients are those of a few
+    sequences at a time, bit for bit.  The weights' gradients add at most 64 products in a run here, 16 there, then in 64 bits,
+    and are rounded once: 82 roundings of the sum of magnitudes (which is off by 65 itself) and some to spare."""
+    n = torch.randint(0, 262, (64,), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    n[:4] = torch.tensor([0, 1, 64, 261])
+    a = conv_inputs(dtype, 64, 261, 1024, W, True)
+    a["lengths"] = n.to(DEV)
+
+    def both(a, at):
+        c = {k: v if k in ("weight", "bias") else v[at] for k, v in a.items()}
+        kw = dict(bias=c["bias"], initial_state=c["initial_state"], lengths=c["lengths"])
+        y = pn.short_conv(c["x"], c["weight"], **kw)
+        return y, [pn.short_conv_backward(c["dy"], c["x"], c["weight"], d_final_state=c["d_final_state"], activation=act, **kw)
+                   for act in (True, False)]
+
+    y, grads = both(a, slice(None))
+    mags = both({k: v if k == "lengths" else v.abs() for k, v in a.items()}, slice(None))[1][1]
+    sums = [0.0, 0.0]
+    for i in range(0, 64, 4):
+        at = slice(i, i + 4)
+        few, few_grads = both(a, at)
+        assert torch.equal(y[0][at], few[0]) and torch.equal(y[1][at], few[1])
+        for g, f in zip(grads, few_grads):
+            assert torch.equal(g[0][at], f[0]) and torch.equal(g[3][at], f[3])
+        sums = [s + t.double() for s, t in zip(sums, few_grads[1][1:3])]
+    for got, want, mag in zip(grads[1][1:3], sums, mags[1:3]):
+        assert bool(((got.double() - want).abs() <= 100 * 2.0 ** -24 * mag.double()).all())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("W", [1, 2, 4, 8])
 @pytest.mark.parametrize("D", [24, 33])
 def test_conv_steps_are_the_prompt(dtype, W, D):
