@@ -176,14 +176,30 @@ struct SsmWave {
     __device__ __forceinline__ int64_t own_at(int64_t n) const {
         return (n * a.B * p.chans + row) * kChans + (lane >> 2) * 2 + (j & 1);
     }
+    // h faded over the segments first, first + step, .. (count of them), each
+    // of which adds its own end; their loads wait for one another in eights
+    // only (one by one they take 25 us more
+    // where there are 95).
+    __device__ __forceinline__ void over_segments(float* ws, int64_t ends, int first_seg, int step, int count, const float (*A2)[S],
+                                                  float (*h)[S]) const {
+        constexpr int TOGETHER = 8;
+        for (int i = 0; i < count; i += TOGETHER) {
+            float more[TOGETHER][2][S], steps[TOGETHER];
+#pragma unroll
+            for (int u = 0; u < TOGETHER; ++u) {         // behind the last one: the last one again, not used
+                const int at_seg = first_seg + min(i + u, count - 1) * step;
+                get(at(ws + ends, at_seg), more[u]);
+                steps[u] = ws[p.decay + own_at(at_seg)];
+            }
+#pragma unroll
+            for (int u = 0; u < TOGETHER; ++u)
+                if (i + u < count) fade(h, steps[u], A2, more[u]);
+        }
+    }
     // The state before segment seg > 0 from the ends of those before it.
     __device__ __forceinline__ void carried(float* ws, const float (*A2)[S], float (*h)[S]) const {
         get(at(ws + p.ends, 0), h);
-        for (int i = 1; i < seg; ++i) {
-            float more[2][S];
-            get(at(ws + p.ends, i), more);
-            fade(h, ws[p.decay + own_at(i)], A2, more);
-        }
+        over_segments(ws, p.ends, 1, 1, seg - 1, A2, h);
     }
 
     // Step and u of the lane's tokens, to LDS as [token][channel][2], and those of the quad's two channels from there.
@@ -497,11 +513,7 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
     }
     if (a.d_final_state)
         w.states([&](int k, int s, int64_t i) { r[k][s] = a.d_final_state[w.b * a.D * a.N + i]; });
-    for (int i = p.n_seg - 1; i > w.seg; --i) {          // what the segments behind give
-        float more[2][S];
-        w.get(w.at(ws + p.rends, i), more);
-        w.fade(r, ws[p.decay + w.own_at(i)], A2, more);
-    }
+    w.over_segments(ws, p.rends, p.n_seg - 1, -1, p.n_seg - 1 - w.seg, A2, r);   // what the segments behind give
     float dskip = 0.0f, dbias = 0.0f;
     const int NP = p.blocks * E;
     float* bc_out = ws + p.part_bc + (static_cast<int64_t>(MULTI ? w.cb : w.cb / p.wide) * a.B + w.b) * a.T * 2 * NP;
