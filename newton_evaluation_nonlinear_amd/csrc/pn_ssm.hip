@@ -5,6 +5,7 @@
 // 16 states (143 MB) in 32 us, 4.5 TB/s, nearly the rate of a large copy.
 
 #include <algorithm>
+#include <cmath>
 
 #include "pn_ssm.hpp"
 #include "pn_ssm_device.hpp"
@@ -145,12 +146,22 @@ hipError_t pass(const pn_ssm_args& a, const SsmPlan& p, SsmPass which, hipStream
 
 }  // namespace
 
-// Segments, none below 32 tokens: 6144 waves, six for every SIMD, of which the
-// oldest run first and the others fill their waits (65536 tokens of 2048 channels in 2048, 4096, 6144 and 12288
-// waves: 1461, 1416, 1267 and 1334 us).  Two sweeps then take the place of one,
-// so two segments gain nothing, and from 2048 waves on one is enough (2048
-// tokens of 16 states, microseconds in one and in several: 1536 waves 673 and
-// 655, with gradients 3212 and 2735; 2048 waves 688 and 861, 3479 and 3624).
+// Segments of 32 tokens or more: 6144 waves, six for every SIMD, of which the
+// oldest run first and the others fill their waits (65536 tokens of 2048
+// channels in 2048, 4096, 6144 and 12288 waves: 1461, 1416, 1267 and 1334 us).
+// Two sweeps then take the place of one, so two segments gain nothing, and from
+// 2048 waves on one is enough (2048 tokens of 16 states, microseconds in one and
+// in several: 1536 waves 673 and 655, with gradients 3212 and 2735; 2048 waves
+// 688 and 861, 3479 and 3624).  Up to a wave for every SIMD a call takes as long
+// as one wave's tokens, and segments may be shorter, 16 tokens and in the
+// gradients 8 (2048 channels of 16 states, 32 and less: 64 tokens 16.4 and
+// 15.1 us, with gradients 84.5 and 46.1; 256 tokens 19.1 and 15.3, 76.6 and
+// 65.1).  With 2048 such waves in place of 1024 nothing is gained (512 tokens:
+// 21.5 and 24.1, 84.1 and 86.1), and below 64 tokens one sweep is as fast.  A
+// segment goes over the ends of those before it, so there are at most 64 or
+// the root of the tokens (256 channels, 65536 tokens in 768 and 256: 351 and
+// 182 us, with gradients 1174 and 638; 1024 channels, 4096 tokens in 128 and 64:
+// 74 and 55, 237 and 178; half and three halves as many are slower).
 SsmPlan plan_ssm(const pn_ssm_args& a, bool backward) {
     SsmPlan p{};
     p.states = a.N <= 4 ? 4 : a.N <= 8 ? 8 : 16;
@@ -165,6 +176,8 @@ SsmPlan plan_ssm(const pn_ssm_args& a, bool backward) {
     const int64_t rows = a.B * p.chans, waves = rows * p.blocks;
     p.tiles = (a.T + kSsmTile - 1) / kSsmTile;
     int64_t n = std::min<int64_t>((6144 + waves - 1) / waves, a.T / 32);
+    if (a.T >= (backward ? 24 : 64)) n = std::max(n, std::min<int64_t>(1024 / waves, a.T / (backward ? 8 : 16)));
+    n = std::min(n, std::max<int64_t>(64, static_cast<int64_t>(std::sqrt(static_cast<double>(a.T)))));
     if (waves >= 2048 || n < 3) n = 1;
     const int64_t per = std::max<int64_t>(1, (p.tiles + n - 1) / n);
     p.seg = per * kSsmTile;

@@ -24,14 +24,14 @@
 // on to eight.  So a tile is kept free of branches (rows past the end and
 // channels that do not exist are left to range-checked buffer accesses, values
 // that are not wanted to selects), and waves are kept small: with four channels
-// a quad the gradients spilled and took 2490 us where they now take 1000.  The
+// a quad the gradients spilled and took 2490 us where they now take 990.  The
 // vector units are busy more than 90 % of the time in kSsmEnds, kSsmOutputs
 // (where channels fill the device) and kSsmMarksBoth, and 80 % in the
 // gradients, which hold 238 registers and run two waves on a SIMD.
 //
 // Measured, bfloat16, 16 states (us, medians of traced calls): 65536 tokens of
-// 2048 channels: ends 431, outputs 668 (1.0 TB/s in all); 8 x 4096 tokens of
-// 2048 channels: ends 195, outputs 301, marks 359, gradients 1005, the sums of db
+// 2048 channels: ends 419, outputs 643 (1.0 TB/s in all); 8 x 4096 tokens of
+// 2048 channels: ends 195, outputs 297, marks 353, gradients 990, the sums of db
 // and dc 23.  4 x 4096 tokens of 512 channels with 128 states, as many states in
 // all as the second: ends 183, outputs 296, gradients 1025, sums 81.
 //
@@ -176,10 +176,9 @@ struct SsmWave {
     __device__ __forceinline__ int64_t own_at(int64_t n) const {
         return (n * a.B * p.chans + row) * kChans + (lane >> 2) * 2 + (j & 1);
     }
-    // h faded over the segments first, first + step, .. (count of them), each
-    // of which adds its own end; their loads wait for one another in eights
-    // only (one by one they take 25 us more
-    // where there are 95).
+    // h faded over `count` segments from first_seg on, each of which adds its
+    // own end.  The loads of eight go out together: one by one, 95 segments take
+    // 25 us more.
     __device__ __forceinline__ void over_segments(float* ws, int64_t ends, int first_seg, int step, int count, const float (*A2)[S],
                                                   float (*h)[S]) const {
         constexpr int TOGETHER = 8;

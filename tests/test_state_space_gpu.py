@@ -425,7 +425,7 @@ def test_scan_segments(dtype):
     _close(h1, _np(final), 2.1 * fe, "state of two calls")
 
 
-@pytest.mark.parametrize("T", list(range(1, 34)) + [95, 96, 97, 127, 128, 129])
+@pytest.mark.parametrize("T", list(range(1, 34)) + [63, 64, 65, 81, 95, 96, 97, 127, 128, 129, 143, 161, 257, 513, 1100])
 def test_scan_lengths_of_one_call(T):
     """Every length of the first tiles, and those at which segments begin."""
     check_scan(scan_inputs("bf16", 1, T, 40, 16, 1, seed=T), "bf16")
