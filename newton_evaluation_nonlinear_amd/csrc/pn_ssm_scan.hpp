@@ -24,14 +24,14 @@
 // on to eight.  So a tile is kept free of branches (rows past the end and
 // channels that do not exist are left to range-checked buffer accesses, values
 // that are not wanted to selects), and waves are kept small: with four channels
-// a quad the gradients spilled and took 2490 us where they now take 990.  The
+// a quad the gradients spilled and took 2490 us where they now take 995.  The
 // vector units are busy more than 90 % of the time in kSsmEnds, kSsmOutputs
 // (where channels fill the device) and kSsmMarksBoth, and 80 % in the
 // gradients, which hold 238 registers and run two waves on a SIMD.
 //
 // Measured, bfloat16, 16 states (us, medians of traced calls): 65536 tokens of
-// 2048 channels: ends 419, outputs 643 (1.0 TB/s in all); 8 x 4096 tokens of
-// 2048 channels: ends 195, outputs 297, marks 353, gradients 990, the sums of db
+// 2048 channels: ends 424, outputs 641 (1.0 TB/s in all); 8 x 4096 tokens of
+// 2048 channels: ends 195, outputs 297, marks 355, gradients 995, the sums of db
 // and dc 23.  4 x 4096 tokens of 512 channels with 128 states, as many states in
 // all as the second: ends 183, outputs 296, gradients 1025, sums 81.
 //
