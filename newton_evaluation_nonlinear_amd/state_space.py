@@ -134,7 +134,7 @@ def short_conv_backward(dy, x, weight, bias=None, initial_state=None, d_final_st
 def short_conv_step(x, weight, state, bias=None, slots=None, activation=True):
     """One token x [B, D] of each sequence: returns y [B, D] and moves ``state`` [n_slots, W - 1, D] (x's type) on by it,
     sequence b at slots[b] (int32) or at b.  A slot outside the pool (by custom -1) marks an idle row: its y is 0 and
-    nothing is updated."""
+    nothing is updated.  Two rows must not name the same slot."""
     (B, D), dt, code, dev, tok, W, w, b = _conv_inputs(x, weight, bias, 2)
     n = _array(slots, "slots", torch.int32, (B,), dev)
     pool = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 3 else 0
@@ -215,7 +215,8 @@ def ssm_step(x, dt, A, b, c, state, skip=None, gate=None, dt_bias=None, softplus
     """One token of each sequence: updates ``state`` float32 [n_slots, D, N] in place and returns y [B, D].
 
     x, dt and gate [B, D], b and c [B, G, N]; sequence b at slots[b] (int32) or at b.  A slot outside the pool (by custom
-    -1) marks an idle row: its y is 0 and nothing is updated."""
+    -1) marks an idle row: its y is 0 and nothing is updated.  Two rows must not name the
+    same slot."""
     (B, D), ty, code, dev, N, G, w, tok = _ssm_inputs(x, dt, A, b, c, skip, gate, dt_bias, 2)
     n = _array(slots, "slots", torch.int32, (B,), dev)
     pool = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 3 else 0
