@@ -1,0 +1,81 @@
+"""State-space operators on the GPU where sizes, splits and values are extreme.
+
+Tolerances are those of test_state_space_gpu.py unless a test derives its own.
+"""
+
+import pytest
+import torch
+
+import newton_evaluation_nonlinear_amd as pn
+from test_sequence_gpu import DEV, TINY, TYPES
+from test_state_space_gpu import PAIRS, check_norm, conv_inputs, norm_inputs, scan_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- masked values
+
+
+def _same(got, want):
+    for x, y in zip(got, want):
+        assert (x is None) == (y is None)
+        if x is not None:
+            assert bool(torch.isfinite(y).all()) and torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype, rdtype", PAIRS)
+@pytest.mark.parametrize("D", [7, 64, 2050, 4104, 8192])
+@pytest.mark.parametrize("post", [True, False])
+def test_norm_gates_of_the_lowest_value(dtype, rdtype, D, post, monkeypatch):
+    """A gate of the type's lowest value lets through what one of -200 does: v sigmoid(v) and its slope are 0 in float32
+    there (200 e^-200 is 1e-85), so outputs and gradients are the same bits, and those of -200 are the oracle's.  To the
+    tolerance comes half the smallest subnormal of float32 and bfloat16, below which a result is rounded to 0."""
+    a = norm_inputs(dtype, rdtype, (2, 4), D)
+    a["x"], a["dy"] = a["x"] * 4, a["dy"] * 4
+    if not post:
+        a["post_weight"] = None
+    off = torch.zeros(2, 4, D, dtype=torch.bool, device=DEV)
+    off[0, 1], off[1, 2, ::3] = True, True
+    results = []
+    for value in (torch.finfo(TYPES[dtype]).min, -200.0):
+        a["gate"] = torch.where(off, value, a["gate"].float()).to(TYPES[dtype])
+        kw = {k: a[k] for k in ("residual", "gate", "post_weight", "scale")}
+        results.append(pn.block_norm(a["x"], a["weight"], **kw) + pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["weight"], **kw))
+    _same(*results)
+    for t, bits in (("f32", 150), ("bf16", 134)):
+        monkeypatch.setitem(TINY, t, 2.0 ** -bits)
+    check_norm(a, dtype, rdtype)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("N", [8, 16, 40])
+def test_scan_gates_of_the_lowest_value(dtype, N):
+    a = scan_inputs(dtype, 2, 70, 40, N, 1)
+    off = torch.zeros(2, 70, 40, dtype=torch.bool, device=DEV)
+    off[0, 9], off[1, :, ::3] = True, True
+    results = []
+    for value in (torch.finfo(TYPES[dtype]).min, -200.0):
+        z = torch.where(off, value, a["gate"].float()).to(TYPES[dtype])
+        kw = dict(skip=a["skip"], dt_bias=a["dt_bias"])
+        args = (a["x"], a["dt"], a["A"], a["b"], a["c"])
+        pool = a["initial_state"].clone()
+        step = pn.ssm_step(a["x"][:, 9], a["dt"][:, 9], a["A"], a["b"][:, 9], a["c"][:, 9], pool, gate=z[:, 9], **kw)
+        kw.update(gate=z, initial_state=a["initial_state"])
+        results.append(pn.ssm_scan(*args, **kw) + pn.ssm_scan_backward(a["dy"], *args, d_final_state=a["d_final_state"], **kw) + (step, pool))
+    _same(*results)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_conv_biases_of_the_lowest_value(dtype):
+    """Channels that their bias closes, as one of -1000 does."""
+    a = conv_inputs(dtype, 2, 70, 40, 4, True)
+    results = []
+    for value in (torch.finfo(torch.float32).min, -1000.0):
+        bias = a["bias"].clone()
+        bias[::3] = value
+        kw = dict(bias=bias, initial_state=a["initial_state"])
+        pool = a["initial_state"].clone()
+        results.append(pn.short_conv(a["x"], a["weight"], **kw)
+                       + pn.short_conv_backward(a["dy"], a["x"], a["weight"], d_final_state=a["d_final_state"], **kw)
+                       + (pn.short_conv_step(a["x"][:, 0], a["weight"], pool, bias=bias), pool))
+    _same(*results)
