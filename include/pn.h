@@ -512,7 +512,8 @@ int pn_short_conv_step(const pn_conv_step_args* a);
  * out, a NULL gate.p the gate.  x, dt, gate [B, T, D]; b and c [B, T, G, N],
  * D a multiple of G: channel d reads group d / (D / G).  A is finite, < 0 in
  * use; growth is allowed as far as exp(A[d] sum delta) over the tokens is
- * finite in float32.  The token strides of x, dt, gate, b, c and dy go up to
+ * finite in float32, and the gradient of delta_t as far as it is.  The token
+ * strides of x, dt, gate, b, c and dy go up to
  * 2^26 elements, D up to 2^24.  Steps and decays are float32: exp(delta A) to
  * (2 |delta A| + 2) 2^-24 of itself, 0 below 2^-126.  A NaN or infinity in a
  * token reaches that token's outputs and those after it (in the gradients also

@@ -45,6 +45,8 @@
 // each once forward from its mark with e kept in registers, once back.
 #pragma once
 
+#include <cfloat>
+
 #include "pn_ssm.hpp"
 #include "pn_ssm_device.hpp"
 
@@ -136,12 +138,16 @@ struct SsmWave {
             for (int s = 0; s < S; ++s)
                 if (has(k) && n0 + s < a.N) f(k, s, static_cast<int64_t>(chan(k)) * a.N + n0 + s);
     }
+    // A log2(e), finite for every finite A: tokens without a step (those behind the last) multiply it with 0.
     __device__ __forceinline__ void decays(float (*A2)[S]) const {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int s = 0; s < S; ++s) A2[k][s] = 0.0f;
-        states([&](int k, int s, int64_t i) { A2[k][s] = a.A[i] * kLog2e; });
+        states([&](int k, int s, int64_t i) {
+            const float v = a.A[i] * kLog2e;
+            A2[k][s] = fabsf(v) > FLT_MAX ? copysignf(FLT_MAX, v) : v;
+        });
     }
     // A state array of the workspace: [.., row, block, k, lane, s].
     __device__ __forceinline__ float* at(float* base, int64_t n) const {

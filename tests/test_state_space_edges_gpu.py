@@ -8,7 +8,7 @@ import torch
 
 import newton_evaluation_nonlinear_amd as pn
 from test_sequence_gpu import DEV, TINY, TYPES
-from test_state_space_gpu import PAIRS, check_norm, conv_inputs, norm_inputs, scan_inputs
+from test_state_space_gpu import PAIRS, check_norm, check_scan, conv_inputs, norm_inputs, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,26 @@ def test_conv_biases_of_the_lowest_value(dtype):
                        + pn.short_conv_backward(a["dy"], a["x"], a["weight"], d_final_state=a["d_final_state"], **kw)
                        + (pn.short_conv_step(a["x"][:, 0], a["weight"], pool, bias=bias), pool))
     _same(*results)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("N", [3, 8, 16, 40])
+@pytest.mark.parametrize("T", [13, 200])
+def test_scan_decays_of_the_lowest_value(dtype, N, T):
+    """A of float32's lowest value forgets everything at every step above 1e-28, as -1e30 does: the same bits, those of -1e30
+    the oracle's, in sequences that end inside a tile too.  A step of 0 (softplus of -200) keeps the state."""
+    a = scan_inputs(dtype, 3, T, 40, N, 1)
+    a["A"] = a["A"].clone()
+    lengths = [T, T - 3, 1]
+    n = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    closed = a["dt"].clone()
+    closed[0, 5:9] = -200.0
+    results = []
+    for value in (torch.finfo(torch.float32).min, -1e30):
+        a["A"][:, ::2] = value
+        kw = dict(skip=a["skip"], gate=a["gate"], dt_bias=a["dt_bias"], initial_state=a["initial_state"], lengths=n)
+        rest = (a["A"], a["b"], a["c"])
+        results.append(pn.ssm_scan(a["x"], closed, *rest, **kw) + pn.ssm_scan(a["x"], a["dt"], *rest, **kw)
+                       + pn.ssm_scan_backward(a["dy"], a["x"], a["dt"], *rest, d_final_state=a["d_final_state"], **kw))
+    _same(*results)
+    check_scan(a, dtype, lengths=lengths)
