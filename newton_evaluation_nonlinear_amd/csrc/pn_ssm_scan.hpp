@@ -484,6 +484,14 @@ struct ChannelSum {
     }
 };
 
+// Tiles whose shares of dA, dskip and ddt_bias are added in float32; such sums
+// are joined in float64, here in LDS and at last in column_sum.
+constexpr int kJoin = 8;
+// Bytes of LDS that a wave of the gradients keeps for itself: those sums and
+// the segment's first state.
+template <int S>
+constexpr int kept_lds_bytes() { return 64 * ((2 * S + 2) * 8 + 2 * S * 4); }
+
 // The waves of a workgroup: blocks of states (MULTI), or adjacent channel
 // blocks, whose shares of db and dc are added in LDS before they are written.
 template <typename T, int S, int BLOCKS>
@@ -495,7 +503,7 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
     __shared__ __align__(16) float du_lds[WAVES][kSsmTile * kChans * 2], g_lds[WAVES][kSsmTile * kChans];
     __shared__ float ex[3][MULTI ? WAVES * kOwn * 64 : 1];
     __shared__ float shares[2][MULTI ? 1 : WAVES][MULTI ? 1 : kSsmTile * 2 * E];
-    __shared__ __align__(16) float in_lds[WAVES][128 * S];
+    extern __shared__ __align__(16) char kept_lds[];
     const SsmWave<T, S, !MULTI> w(a, p);
     if (w.seg >= p.n_seg) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -506,7 +514,11 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
     T *dxp = static_cast<T*>(a.dx), *ddp = static_cast<T*>(a.ddt), *dzp = static_cast<T*>(a.dgate);
     float A2[2][S], r[2][S], dA[2][S];
     w.decays(A2);
-    float* in = in_lds[wave] + w.lane * S;               // the segment's first state: the lane's own, in put()'s order
+    // the lane's own: sums (those of dA, dskip, ddt_bias) and the segment's first state in put()'s order
+    double* sums = reinterpret_cast<double*>(kept_lds + wave * kept_lds_bytes<S>()) + w.lane;
+    float* in = reinterpret_cast<float*>(kept_lds + wave * kept_lds_bytes<S>() + 64 * (2 * S + 2) * 8) + w.lane * S;
+#pragma unroll
+    for (int i = 0; i < 2 * S + 2; ++i) sums[64 * i] = 0.0;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -532,7 +544,19 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
             ddp[o] = from_f32<T>(0.0f);
             if (gated) dzp[o] = from_f32<T>(0.0f);
         }
-    int turn = 0;
+    auto join = [&]() {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                sums[64 * (k * S + s)] += dA[k][s];
+                dA[k][s] = 0.0f;
+            }
+        sums[64 * 2 * S] += dskip;
+        sums[64 * (2 * S + 1)] += dbias;
+        dskip = dbias = 0.0f;
+    };
+    int turn = 0, since_join = 0;
     uint32_t x[kOwn], dt[kOwn], z[kOwn], gy[kOwn], bv[w.M], cv[w.M];
     float mark[2][S], since = 0.0f;
     auto load = [&](int64_t t0) {
@@ -686,12 +710,21 @@ void ssm_gradients(pn_ssm_args a, SsmPlan p) {
             }
             turn ^= 1;
         }
+        if (++since_join == kJoin) {
+            join();
+            since_join = 0;
+        }
     }
+    join();
     // the two parities of a channel
+    dskip = static_cast<float>(sums[64 * 2 * S]);
+    dbias = static_cast<float>(sums[64 * (2 * S + 1)]);
     dskip += dpp<0x4E>(dskip);
     dbias += dpp<0x4E>(dbias);
     const int64_t part = w.b * p.n_seg + w.seg;
-    w.states([&](int k, int s, int64_t i) { ws[p.part_A + part * a.D * a.N + i] = dA[k][s]; });
+    w.states([&](int k, int s, int64_t i) {
+        ws[p.part_A + part * a.D * a.N + i] = static_cast<float>(sums[64 * (k * S + s)]);
+    });
     if (w.own && w.odd == 0) {
         float* v = ws + p.part_vec + (part * p.blocks + w.blk) * 2 * a.D + w.ch;
         v[0] = dskip;
@@ -712,7 +745,15 @@ hipError_t ssm_launch(const pn_ssm_args& a, const SsmPlan& p, SsmPass pass, hipS
         case kSsmOutputs: ssm_pass<T, S, BLOCKS, kSsmOutputs><<<grid, threads, 0, st>>>(a, p); break;
         case kSsmMarks: ssm_pass<T, S, BLOCKS, kSsmMarks><<<grid, threads, 0, st>>>(a, p); break;
         case kSsmMarksBoth: ssm_pass<T, S, BLOCKS, kSsmMarksBoth><<<grid, threads, 0, st>>>(a, p); break;
-        default: ssm_gradients<T, S, BLOCKS><<<grid, threads, 0, st>>>(a, p); break;
+        default: {
+            const auto kernel = ssm_gradients<T, S, BLOCKS>;
+            const int lds = threads / 64 * kept_lds_bytes<S>();
+            if (lds > 48 * 1024) {
+                const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+                if (e != hipSuccess) return e;
+            }
+            kernel<<<grid, threads, lds, st>>>(a, p);
+        }
     }
     return hipGetLastError();
 }

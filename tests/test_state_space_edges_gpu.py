@@ -3,14 +3,39 @@
 Tolerances are those of test_state_space_gpu.py unless a test derives its own.
 """
 
+import numpy as np
 import pytest
 import torch
 
 import newton_evaluation_nonlinear_amd as pn
-from test_sequence_gpu import DEV, TINY, TYPES
-from test_state_space_gpu import PAIRS, check_norm, check_scan, conv_inputs, norm_inputs, scan_inputs
+from newton_evaluation_nonlinear_amd import state_space as ss
+from oracle import state_space as ref
+from test_sequence_gpu import DEV, TINY, TYPES, _np
+from test_state_space_gpu import PAIRS, U, check_norm, check_scan, conv_inputs, norm_inputs, scan_inputs
 
 pytestmark = pytest.mark.gpu
+
+CODE = {"f32": 0, "bf16": 1, "f16": 2}
+
+
+def scan_bytes(B, T, D, N, G, wide, segments):
+    """Workspace of the scan's gradients with `wide` channel blocks a workgroup and `segments` of the time axis."""
+    states, blocks = (4 if N <= 4 else 8 if N <= 8 else 16), -(-N // 16)
+    per_group = -(-(-(-(D // G) // 32)) // wide) * wide
+    tiles, chans = -(-T // 8), G * per_group
+    rows = B * chans
+    state = rows * blocks * states * 32
+    parts = [tiles * state, tiles * rows * 32, chans // wide * B * T * 2 * blocks * states, B * segments * D * N,
+             B * segments * blocks * 2 * D]
+    if segments > 1:
+        parts += [segments * state, segments * rows * 32, segments * state]
+    return 4 * sum(-(-n // 64) * 64 for n in parts)
+
+
+def scan_splits(dtype, B, T, D, N, G):
+    """(channel blocks of a workgroup, segments) of the scan's gradients: those that its workspace has room for."""
+    n = pn.lib().pn_ssm_scan_workspace_bytes(ss._SSM(CODE[dtype], B, T, D, N, G, 1, *[0] * 44), 1)
+    return [(wide, k) for wide in (1, 2, 4) for k in range(1, min(T, 300) // 8 + 2) if n == scan_bytes(B, T, D, N, G, wide, k)]
 
 
 # ---------------------------------------------------------------- masked values
@@ -102,3 +127,28 @@ def test_scan_decays_of_the_lowest_value(dtype, N, T):
                        + pn.ssm_scan_backward(a["dy"], a["x"], a["dt"], *rest, d_final_state=a["d_final_state"], **kw))
     _same(*results)
     check_scan(a, dtype, lengths=lengths)
+
+
+# ---------------------------------------------------------------- long sums
+
+
+@pytest.mark.parametrize("B, N", [(2048, 1), (1024, 20), (256, 128)])
+def test_scan_sums_over_a_long_segment(B, N):
+    """Sums over 16384 tokens of one segment, of terms of one sign and (after the first few) one size, which a single float32
+    sum would leave by 2e-5 and more of itself.
+
+    Every sequence is the same, so the sums are B times the oracle's of one.  With A = -1 and steps of about 2 a decay,
+    e^-2 = 0.13, is off by at most 9 U of itself (the step's rounding and two of the exponent, times 2, and two more), a state
+    and its gradient by (0.13 * 10 + 0.87 * 3 + 1) U / 0.87 < 6 U, a kept state by 16, the terms of dA by 25 and those of
+    dskip by 1.  The terms of ddt_bias are sums over N states: 30 + 2 N, for what each term and the sums in lanes and
+    waves take.  64 terms are added in float32, which is 64 U at most; the rest of the sum is float64, rounded twice."""
+    T, v = 16384, 0.7234
+    same = lambda *s: torch.full(s, v, device=DEV).expand(B, *s[1:])  # noqa: E731
+    x, b, dt = same(1, T, 1), same(1, T, 1, N), same(1, T, 1) + 0.6
+    A, skip, bias = -torch.ones(1, N, device=DEV), torch.full((1,), v, device=DEV), torch.full((1,), v, device=DEV)
+    assert scan_splits("f32", B, T, 1, N, 1) == [(1, 1)]
+    got = pn.ssm_scan_backward(x, x, dt, A, b, b, skip=skip, dt_bias=bias, softplus=False)
+    one = [_np(t[:1]) for t in (x, x, dt)] + [_np(A), _np(b[:1]), _np(b[:1]), _np(skip), None, _np(bias)]
+    want, mag = (ref.ssm_scan_backward(*one, softplus=False, bound=bound) for bound in (False, True))
+    for i, n in ((2, 25), (5, 1), (7, 30 + 2 * N)):
+        assert (np.abs(_np(got[i]) / B - want[i]) <= (n + 66) * U * mag[i]).all(), (i, _np(got[i]) / B, want[i])
