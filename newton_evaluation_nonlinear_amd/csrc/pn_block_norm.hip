@@ -369,12 +369,14 @@ hipError_t forward_typed(const pn_block_norm_args& a, hipStream_t st) {
 }
 
 // Rows of a workgroup of the gradients: as many workgroups as run at once (12
-// waves a unit up to 2048 channels, 8 in the larger forms), so that none is
-// left for a second round.
+// waves a unit up to 2048 channels, 8 in the larger forms), or a multiple of
+// them: a lane adds the weights' gradients of at most 128 rows in float32, the
+// rest of the sum is column_sum's in float64.
 void backward_split(const pn_block_norm_args& a, int64_t* rows, int64_t* n_wg) {
     const int64_t n = a.B * a.T;
     const int64_t at_once = 256 * (a.D <= 512 ? 12 : a.D <= 1024 ? 6 : a.D <= 2048 ? 3 : a.D <= 2560 ? 2 : 1);
-    *rows = std::max<int64_t>(1, (n + at_once - 1) / at_once);
+    const int64_t wgs = at_once * std::max<int64_t>(1, (n + 128 * at_once - 1) / (128 * at_once));
+    *rows = std::max<int64_t>(1, (n + wgs - 1) / wgs);
     *n_wg = (n + *rows - 1) / *rows;
 }
 

@@ -152,3 +152,23 @@ def test_scan_sums_over_a_long_segment(B, N):
     want, mag = (ref.ssm_scan_backward(*one, softplus=False, bound=bound) for bound in (False, True))
     for i, n in ((2, 25), (5, 1), (7, 30 + 2 * N)):
         assert (np.abs(_np(got[i]) / B - want[i]) <= (n + 66) * U * mag[i]).all(), (i, _np(got[i]) / B, want[i])
+
+
+@pytest.mark.parametrize("D, rows", [(4, (1 << 23) + 5), (600, 2000000)])
+def test_norm_sums_over_many_rows(D, rows):
+    """Sums over many equal rows, which a single float32 sum of a workgroup's (2731 of 4 channels, 1303 of 600) would leave by
+    more than the bound.
+
+    A term is off by less than 40 U of itself (the mean of D squares in lanes and waves: 12 roundings of its terms, so 6 of
+    its root, twice; root, reciprocal, products, and the mean in t, of the size of its terms).  At most 128 terms are added
+    in float32, the rest in float64, rounded twice; the sums are `rows` times the oracle's of one row."""
+    g = torch.Generator().manual_seed(3)
+    row = (torch.rand(1, 1, D, generator=g) + 0.5).to(DEV)
+    x = row.expand(1, rows, D)
+    w = torch.ones(D, device=DEV)
+    got = pn.block_norm_backward(x, None, x, w, post_weight=w, scale=w)
+    want, mag = ref.block_norm_backward(_np(row), None, _np(row), _np(w), None, None, _np(w), _np(w))
+    for i in (1, 4, 5):
+        assert (np.abs(_np(got[i]) / rows - want[i]) <= (40 + 130) * U * mag[i]).all(), i
+    block = ss._NORM(0, 0, 1, rows, D, 1e-6, 1, 1, 1, *[0] * 31)
+    assert pn.lib().pn_block_norm_workspace_bytes(block) >= 12 * D * (rows // 128)
