@@ -569,7 +569,11 @@ int pn_ssm_step(const pn_ssm_step_args* a);
  * x is what a block gives, s the residual stream after it and y what the next
  * block takes.  x, gate, y and their gradients have the storage type, the
  * residual, s and theirs residual_dtype: the storage type or PN_F32.  Means
- * are float32 sums of squares: rows of elements past 1e18 come out as 0.
+ * are float32 sums of squares: a row whose squares sum past 3.4e38 (elements
+ * of u, or of s, past sqrt(3.4e38 / D): 4e17 with 2048 channels) comes out of
+ * that norm as 0, and passes it no gradient.  eps is taken in float32, and
+ * squares below 1e-38 are lost beside it: with an eps of 0, rows of elements
+ * under 1e-19 come out too large, infinite or NaN.
  * The backward takes what the forward took, and forms s again. */
 typedef struct pn_block_norm_args {
     int64_t dtype, residual_dtype, B, T, D;

@@ -6,6 +6,10 @@
 //     q = pw scale t,  du = ru (q - n mean(q n)),  dpw = scale sum t n,
 //     dscale = pw sum t n,  dx = du silu(gate),  dgate = du x silu'(gate).
 //
+// A row whose squares pass float32 has ru or rs of 0: nothing goes through that
+// norm, and neither does a gradient, also where the sums of its products are
+// past float32.
+//
 // The gradients form s again from what the forward took, in float32: from s
 // as it was stored in 16 bits, dw would keep its rounding.
 //
@@ -245,7 +249,7 @@ void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float
                 es = fmaf(w[u][i], s[u][i], es);
             });
             row_sums<THREADS>(ss, es, lds);
-            const float rs = 1.0f / sqrtf(fmaf(ss, inv, eps)), mean = es * rs * inv;
+            const float rs = 1.0f / sqrtf(fmaf(ss, inv, eps)), mean = rs > 0.0f ? es * rs * inv : 0.0f;
             r.each([&](int u, int i) {
                 const float m = s[u][i] * rs;
                 dw[u][i] = fmaf(e[u][i], m, dw[u][i]);
@@ -262,7 +266,7 @@ void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float
                 qu = fmaf(w[u][i], block(u, i), qu);
             });
             row_sums<THREADS>(qu, unused, lds);
-            const float mean = qu * ru * inv;
+            const float mean = ru > 0.0f ? qu * ru * inv : 0.0f;
             r.each([&](int u, int i) {
                 const float n = block(u, i) * ru;
                 tn[u][i] = fmaf(t[u][i], n, tn[u][i]);

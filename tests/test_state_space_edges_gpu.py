@@ -172,3 +172,40 @@ def test_norm_sums_over_many_rows(D, rows):
         assert (np.abs(_np(got[i]) / rows - want[i]) <= (40 + 130) * U * mag[i]).all(), i
     block = ss._NORM(0, 0, 1, rows, D, 1e-6, 1, 1, 1, *[0] * 31)
     assert pn.lib().pn_block_norm_workspace_bytes(block) >= 12 * D * (rows // 128)
+
+
+# ---------------------------------------------------------------- far rows
+
+
+def _far(dtype, D, by, g):
+    """[1, 3, D] of elements of `by` times the size at which their squares sum to float32's largest value."""
+    size = by * float(np.sqrt(np.finfo(np.float32).max / D))
+    return (torch.where(torch.rand(1, 3, D, generator=g) < 0.5, -size, size)).to(DEV).to(TYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype, rdtype", [p for p in PAIRS if p[0] != "f16"])
+@pytest.mark.parametrize("D", [1, 7, 64, 2048, 2050, 8192])
+def test_norm_rows_on_both_sides_of_float32(dtype, rdtype, D):
+    """Rows whose squares just fit float32 are normed like others; past it they come out as 0 and pass no gradient, also
+    where the sums of the gradient's products do not fit either.  (bfloat16 is within 2^-8 of the sizes given.)"""
+    g = torch.Generator().manual_seed(D)
+    a = norm_inputs(dtype, rdtype, (1, 3), D)
+    a["gate"] = None
+    plain = dict(a, post_weight=None)
+    check_norm(dict(plain, residual=_far(rdtype, D, 0.99, g)), dtype, rdtype)
+    check_norm(dict(a, x=_far(dtype, D, 0.99, g)), dtype, rdtype)
+    for dy in (a["dy"], torch.full_like(a["dy"], 1e25)):
+        far = dict(plain, residual=_far(rdtype, D, 1.01, g))         # past it in s
+        y, s = pn.block_norm(far["x"], far["weight"], residual=far["residual"], scale=far["scale"])
+        dx, dw, dr, _, _, dsc = pn.block_norm_backward(dy, far["ds"], far["x"], far["weight"], residual=far["residual"], scale=far["scale"])
+        assert not y.any() and not dw.any() and bool(torch.isfinite(s).all()) and torch.equal(dr, far["ds"])
+        assert torch.equal(dx, (far["ds"].float() * far["scale"]).to(dx.dtype))
+        want = (far["ds"].double() * far["x"].double()).sum((0, 1))
+        assert bool(((dsc.double() - want).abs() <= 8 * U * (far["ds"].double() * far["x"].double()).abs().sum((0, 1))).all())
+    x = _far(dtype, D, 1.01, g)                                      # past it in u: with a large gradient of s
+    ds = torch.full_like(a["ds"], 1e25)
+    kw = dict(residual=a["residual"], post_weight=a["post_weight"], scale=a["scale"])
+    y, s = pn.block_norm(x, a["weight"], **kw)
+    assert torch.equal(s, a["residual"]) and bool(torch.isfinite(y).all())
+    dx, dw, dr, _, dpw, dsc = pn.block_norm_backward(a["dy"], ds, x, a["weight"], **kw)
+    assert not dx.any() and not dpw.any() and not dsc.any() and torch.equal(dr, ds)
