@@ -15,8 +15,6 @@ from test_state_space_gpu import PAIRS, U, check_norm, check_scan, conv_inputs, 
 
 pytestmark = pytest.mark.gpu
 
-CODE = {"f32": 0, "bf16": 1, "f16": 2}
-
 
 def scan_bytes(B, T, D, N, G, wide, segments):
     """Workspace of the scan's gradients with `wide` channel blocks a workgroup and `segments` of the time axis."""
@@ -32,10 +30,52 @@ def scan_bytes(B, T, D, N, G, wide, segments):
     return 4 * sum(-(-n // 64) * 64 for n in parts)
 
 
-def scan_splits(dtype, B, T, D, N, G):
+def scan_splits(B, T, D, N, G):
     """(channel blocks of a workgroup, segments) of the scan's gradients: those that its workspace has room for."""
-    n = pn.lib().pn_ssm_scan_workspace_bytes(ss._SSM(CODE[dtype], B, T, D, N, G, 1, *[0] * 44), 1)
+    n = pn.lib().pn_ssm_scan_workspace_bytes(ss._SSM(0, B, T, D, N, G, 1, *[0] * 44), 1)
     return [(wide, k) for wide in (1, 2, 4) for k in range(1, min(T, 300) // 8 + 2) if n == scan_bytes(B, T, D, N, G, wide, k)]
+
+
+def norm_groups(rows, D):
+    """Workgroups of the norm's gradients, from the workspace that holds three rows of each."""
+    return pn.lib().pn_block_norm_workspace_bytes(ss._NORM(0, 0, 1, rows, D, 1e-5, 1, 1, 1, *[0] * 31)) / (12 * D)
+
+
+# ---------------------------------------------------------------- splits
+
+
+# B, T, D, N, G, channel blocks of a workgroup of the gradients, segments, lengths
+WIDE = [(1, 20, 128, 16, 1, 4, 1, None),                 # one share of db and dc
+        (3, 23, 256, 12, 1, 4, 1, [23, 0, 9]),           # two
+        (2, 96, 128, 3, 1, 4, 12, [96, 37]),             # in segments
+        (1, 40, 512, 8, 1, 4, 5, [33]),
+        (2, 22, 256, 16, 2, 4, 1, [22, 17]),             # two groups
+        (2, 50, 480, 16, 1, 4, 4, [50, 8]),              # 15 blocks and one without a channel
+        (1, 17, 257, 16, 1, 2, 1, None),                 # 9 blocks, the last of one channel, and one without
+        (2, 29, 288, 5, 1, 2, 2, [29, 24]),
+        (1, 21, 1026, 4, 2, 2, 1, None),                 # 17 and one without, twice
+        (1, 18, 64, 16, 1, 2, 1, None),
+        (8, 90, 2048, 3, 1, 4, 1, [90, 89, 65, 64, 63, 8, 1, 0]),   # sums over more than 64 tokens of a segment
+        (64, 75, 6, 128, 1, 1, 1, None)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("case", WIDE, ids=["x".join(map(str, c[:5])) for c in WIDE])
+def test_scan_gradients_of_wide_groups(dtype, case):
+    """Workgroups of several channel blocks, that add their shares of db and dc in LDS; and long single segments."""
+    *sizes, _, _, lengths = case
+    check_scan(scan_inputs(dtype, *sizes), dtype, lengths=lengths)
+
+
+ROWS = [(40, 6200), (512, 6200), (514, 3100), (2048, 1550), (2050, 1100), (2559, 1100), (2560, 1100), (4096, 601), (4097, 601),
+        (4104, 601), (8191, 601), (8192, 601)]
+
+
+@pytest.mark.parametrize("dtype, rdtype", [("f32", "f32"), ("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("D, rows", ROWS)
+def test_norm_gradients_of_several_rows_a_workgroup(dtype, rdtype, D, rows):
+    """Three rows for each workgroup of the gradients, and fewer for the last."""
+    check_norm(norm_inputs(dtype, rdtype, (1, rows), D), dtype, rdtype)
 
 
 # ---------------------------------------------------------------- masked values
@@ -146,7 +186,7 @@ def test_scan_sums_over_a_long_segment(B, N):
     same = lambda *s: torch.full(s, v, device=DEV).expand(B, *s[1:])  # noqa: E731
     x, b, dt = same(1, T, 1), same(1, T, 1, N), same(1, T, 1) + 0.6
     A, skip, bias = -torch.ones(1, N, device=DEV), torch.full((1,), v, device=DEV), torch.full((1,), v, device=DEV)
-    assert scan_splits("f32", B, T, 1, N, 1) == [(1, 1)]
+    assert scan_splits(B, T, 1, N, 1) == [(1, 1)]
     got = pn.ssm_scan_backward(x, x, dt, A, b, b, skip=skip, dt_bias=bias, softplus=False)
     one = [_np(t[:1]) for t in (x, x, dt)] + [_np(A), _np(b[:1]), _np(b[:1]), _np(skip), None, _np(bias)]
     want, mag = (ref.ssm_scan_backward(*one, softplus=False, bound=bound) for bound in (False, True))
@@ -170,8 +210,7 @@ def test_norm_sums_over_many_rows(D, rows):
     want, mag = ref.block_norm_backward(_np(row), None, _np(row), _np(w), None, None, _np(w), _np(w))
     for i in (1, 4, 5):
         assert (np.abs(_np(got[i]) / rows - want[i]) <= (40 + 130) * U * mag[i]).all(), i
-    block = ss._NORM(0, 0, 1, rows, D, 1e-6, 1, 1, 1, *[0] * 31)
-    assert pn.lib().pn_block_norm_workspace_bytes(block) >= 12 * D * (rows // 128)
+    assert norm_groups(rows, D) >= rows // 128
 
 
 # ---------------------------------------------------------------- far rows
@@ -209,3 +248,92 @@ def test_norm_rows_on_both_sides_of_float32(dtype, rdtype, D):
     assert torch.equal(s, a["residual"]) and bool(torch.isfinite(y).all())
     dx, dw, dr, _, dpw, dsc = pn.block_norm_backward(a["dy"], ds, x, a["weight"], **kw)
     assert not dx.any() and not dpw.any() and not dsc.any() and torch.equal(dr, ds)
+
+
+# ---------------------------------------------------------------- past 2^32 elements
+
+
+def test_steps_on_pools_past_32_bits():
+    """Slots whose states lie past 2^31 and 2^32 elements of their pool give what the same states give in a small one."""
+    B, D, N, W = 5, 4096, 16, 4
+    slots = [69999, 0, 65536, 32768, -1]
+    s, c = scan_inputs("bf16", B, 1, D, N, 1), conv_inputs("bf16", B, 1, D, W, True)
+    for pool_of, per, step in (
+            (lambda n: torch.empty(n, D, N, device=DEV), s["initial_state"],
+             lambda pool, n: pn.ssm_step(s["x"][:, 0], s["dt"][:, 0], s["A"], s["b"][:, 0], s["c"][:, 0], pool, gate=s["gate"][:, 0], slots=n)),
+            (lambda n: torch.empty(n * 6, W - 1, D, device=DEV, dtype=torch.bfloat16), c["initial_state"],
+             lambda pool, n: pn.short_conv_step(c["x"][:, 0], c["weight"], pool, bias=c["bias"], slots=n))):
+        few = per.clone()
+        want = step(few, torch.tensor([0, 1, 2, 3, -1], dtype=torch.int32, device=DEV))
+        pool = pool_of(70000)
+        at = [i * (pool.shape[0] // 70000) for i in slots[:4]]
+        for i, b in zip(at, range(4)):
+            pool[i] = per[b]
+        got = step(pool, torch.tensor(at + [-1], dtype=torch.int32, device=DEV))
+        assert pool.numel() > 1 << 32 and torch.equal(got, want)
+        assert all(torch.equal(pool[i], few[b]) for i, b in zip(at, range(4)))
+        del pool
+
+
+def test_sequences_more_than_32_bits_apart():
+    """Sequences 2^32 elements apart in memory are as good as their copies."""
+    B, T, D, N = 2, 20, 40, 16
+    far = torch.empty((1 << 32) + 4096, dtype=torch.bfloat16, device=DEV)
+
+    def apart(t):
+        v = far.as_strided(t.shape, (1 << 32, *t.stride()[1:]))
+        return v.copy_(t)
+
+    s, c, n = scan_inputs("bf16", B, T, D, N, 1), conv_inputs("bf16", B, T, D, 4, True), norm_inputs("bf16", "bf16", (B, T), D)
+    kw = dict(skip=s["skip"], dt_bias=s["dt_bias"], gate=s["gate"])
+    calls = [("x", c, lambda a: pn.short_conv(a["x"], a["weight"], bias=a["bias"])),
+             ("dy", c, lambda a: pn.short_conv_backward(a["dy"], a["x"], a["weight"], bias=a["bias"])),
+             ("x", n, lambda a: pn.block_norm(a["x"], a["weight"], residual=a["residual"])),
+             ("residual", n, lambda a: pn.block_norm(a["x"], a["weight"], residual=a["residual"])),
+             ("dy", n, lambda a: pn.block_norm_backward(a["dy"], a["ds"], a["x"], a["weight"], residual=a["residual"]))]
+    for k in ("x", "dt", "b", "c"):
+        calls.append((k, s, lambda a: pn.ssm_scan(a["x"], a["dt"], a["A"], a["b"], a["c"], **kw)))
+    for k in ("dy", "x", "b"):
+        calls.append((k, s, lambda a: pn.ssm_scan_backward(a["dy"], a["x"], a["dt"], a["A"], a["b"], a["c"], **kw)))
+    for k, a, f in calls:
+        _same(f(dict(a, **{k: apart(a[k])})), f(a))
+
+
+def test_tokens_past_32_bits():
+    """One sequence of 2^32 and some elements: its last tokens are those of a call that starts shortly before them, whose state
+    is forgotten by then (e^-2 a token and less; 100 tokens are 1e-86).  The scan rounds its segments apart: twice the
+    rounding of bfloat16, and of the float32 sums 100 U of their magnitude, which a tenth of a rounding covers where the
+    result is not a small difference: 2^-12 of the largest value is added."""
+    D, T, tail = 4096, (1 << 20) + 40, 200
+    x = torch.empty(1, T, D, dtype=torch.bfloat16, device=DEV).uniform_(-1.0, 1.0)
+    end = x[:, -tail:].contiguous()
+    w, bias = torch.rand(D, 4, device=DEV), torch.rand(D, device=DEV)
+    y, last = pn.short_conv(x, w, bias=bias)
+    few, few_last = pn.short_conv(end, w, bias=bias)
+    assert torch.equal(y[:, -100:], few[:, -100:]) and torch.equal(last, few_last)
+    del y
+    dx = pn.short_conv_backward(x, x, w, bias=bias)[0]
+    assert torch.equal(dx[:, -100:], pn.short_conv_backward(end, end, w, bias=bias)[0][:, -100:])
+    del dx
+    y, s = pn.block_norm(x, bias, post_weight=bias)
+    few, few_s = pn.block_norm(end, bias, post_weight=bias)
+    assert torch.equal(y[:, -tail:], few) and torch.equal(s[:, -tail:], few_s)
+    del y, s
+    dx = pn.block_norm_backward(x, None, x, bias, post_weight=bias)[0]
+    assert torch.equal(dx[:, -tail:], pn.block_norm_backward(end, None, end, bias, post_weight=bias)[0])
+    del dx
+
+    def close(got, want):
+        got, want = got[:, -100:].float(), want[:, -100:].float()
+        assert bool(((got - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -12 * want.abs().max()).all())
+
+    A = -1.0 - torch.rand(D, 1, device=DEV)
+    b = torch.rand(1, T, 1, 1, device=DEV).to(torch.bfloat16)
+    args = lambda x, b: (x, x, A, b, b)  # noqa: E731
+    dt_bias = torch.full((D,), 3.0, device=DEV)               # steps of 2.1 to 4.02
+    end_b = b[:, -tail:].contiguous()
+    close(pn.ssm_scan(*args(x, b), dt_bias=dt_bias)[0], pn.ssm_scan(*args(end, end_b), dt_bias=dt_bias)[0])
+    got = pn.ssm_scan_backward(x, *args(x, b), dt_bias=dt_bias)
+    want = pn.ssm_scan_backward(end, *args(end, end_b), dt_bias=dt_bias)
+    close(got[0], want[0])
+    close(got[1], want[1])
