@@ -2,7 +2,8 @@
 and the norms around a block, each with its gradients.
 
 Tokens are [B, T, D], the scan's b and c [B, T, G, N], its states [B, D, N], the convolution's state the last W - 1 tokens
-[B, W - 1, D].  Functions named *_bound give the sum of the absolute values of the terms of each element instead.
+[B, W - 1, D].  The gradients also come as the sums of the absolute values of their terms, which error bounds are made of:
+second results of short_conv_backward and block_norm_backward, ssm_scan_backward with ``bound``.
 """
 
 import numpy as np
@@ -82,25 +83,24 @@ def _steps(dt, dt_bias, use):
     return (softplus(v), logistic(v)) if use else (v, np.ones_like(v))
 
 
-def ssm_scan(x, dt, A, b, c, skip=None, gate=None, dt_bias=None, softplus=True, initial_state=None, lengths=None, bound=False):
-    """(y, final state), or with ``bound`` the sums of absolute terms of both."""
+def ssm_scan(x, dt, A, b, c, skip=None, gate=None, dt_bias=None, softplus=True, initial_state=None, lengths=None):
+    """(y, final state)."""
     x, A, b, c = _f(x), _f(A), _f(b), _f(c)
     B, T, D = x.shape
     G, N = b.shape[2:]
     delta, _ = _steps(dt, dt_bias, softplus)
-    f = np.abs if bound else (lambda v: v)
     b, c = np.repeat(b, D // G, 2), np.repeat(c, D // G, 2)
-    h = np.zeros((B, D, N)) if initial_state is None else f(_f(initial_state).copy())
+    h = np.zeros((B, D, N)) if initial_state is None else _f(initial_state).copy()
     y = np.zeros((B, T, D))
     for i, n in enumerate(_lengths(lengths, B, T)):
         for t in range(n):
-            h[i] = np.exp(delta[i, t][:, None] * A) * h[i] + f((delta[i, t] * x[i, t])[:, None] * b[i, t])
-            y[i, t] = (f(c[i, t]) * h[i]).sum(-1)
+            h[i] = np.exp(delta[i, t][:, None] * A) * h[i] + (delta[i, t] * x[i, t])[:, None] * b[i, t]
+            y[i, t] = (c[i, t] * h[i]).sum(-1)
             if skip is not None:
-                y[i, t] += f(_f(skip) * x[i, t])
+                y[i, t] += _f(skip) * x[i, t]
             if gate is not None:
                 z = _f(gate)[i, t]
-                y[i, t] *= f(z * logistic(z))
+                y[i, t] *= z * logistic(z)
     return y, h
 
 
