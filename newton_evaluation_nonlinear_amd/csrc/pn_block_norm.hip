@@ -223,10 +223,10 @@ void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float
         } else {
             fetch_last(row);
         }
-        // the forward: act is the gate's sigmoid, which goes to the gate first: 0 times a gate of the type's lowest
-        // value is 0, where the gate times x or its gradient is past float32
+        // the forward: act is the gate's sigmoid, which is multiplied with before the gate: 0 for a gate of the
+        // type's lowest value, whose product with x or a gradient may be past float32
         r.each([&](int u, int i) { act[u][i] = a.gate.p ? logistic(g[u][i]) : 1.0f; });
-        auto block = [&](int u, int i) { return a.gate.p ? x[u][i] * (g[u][i] * act[u][i]) : x[u][i]; };
+        auto block = [&](int u, int i) { return a.gate.p ? x[u][i] * act[u][i] * g[u][i] : x[u][i]; };
         float ru = 1.0f, uu = 0.0f, unused = 0.0f;
         if (a.post_weight) {
             r.each([&](int u, int i) { uu = fmaf(block(u, i), block(u, i), uu); });
@@ -281,9 +281,9 @@ void block_norm_backward(pn_block_norm_args a, int64_t rows, int64_t n_wg, float
         }
         if (a.gate.p) {
             r.each([&](int u, int i) {                   // x: dgate, t: dx
-                const float du = t[u][i], p = act[u][i];
-                x[u][i] = du * x[u][i] * (p * fmaf(g[u][i], 1.0f - p, 1.0f));
-                t[u][i] = du * (g[u][i] * p);
+                const float p = act[u][i], du = t[u][i] * p;
+                x[u][i] = du * x[u][i] * fmaf(g[u][i], 1.0f - p, 1.0f);
+                t[u][i] = du * g[u][i];
             });
             r.store(static_cast<T*>(a.dgate) + row * a.D, x);
         }
