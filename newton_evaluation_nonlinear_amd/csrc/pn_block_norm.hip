@@ -22,10 +22,10 @@
 // Measured: 8 x 4096 rows of 2048 channels, bfloat16, gate, norms, scale and
 // residual: 130 to 140 us, 4.8 to 5.1 TB/s; half as many with gradients 76 and
 // 120, 4.4 and 4.5 TB/s, and 8 for the weights' sums; 8192 channels, 4 x 4096
-// rows: 272 and 686, 4.9 and 3.1 TB/s (the gradients hold 16 channels a lane
+// rows: 272 and 674, 4.9 and 3.1 TB/s (the gradients hold 16 channels a lane
 // and run 8 waves a unit).  4 x 2047 rows of 2050 channels on a float32 residual,
 // two channels at a time: 66 and 89, 6 for the sums.  Odd widths go channel by
-// channel: 2049 channels, 4 x 4096 rows, 173 and 172.
+// channel: 2049 channels, 4 x 4096 rows, 164 to 173 and 172 to 177.
 
 #include <algorithm>
 
@@ -338,10 +338,15 @@ int widest(const pn_block_norm_args& a, bool backward) {
 }
 
 // f(form) for rows of D channels, V at a time: the fewest waves that hold a
-// row in 8 values a lane (16 past 4096 channels), or a few more in units of one
-// or two channels, where rows just past 2048 would leave half of twice the
-// waves idle.  With 16 values the gradients have no registers for the next row
-// (2050 channels in pairs, float32 residual, 8188 rows: 217 us).
+// row in 8 values a lane (16 past 4096 channels), or ten in units of one or two
+// channels, where rows of 2049 to 2560 would leave half of twice the waves idle
+// (32768 rows in bfloat16 in 256 and in 512 threads, forward and gradients:
+// 2050 channels in pairs 233 and 281, 283 and 499 us; 2304 in pairs 245 and 300,
+// 289 and 498; 2559 one by one 383 and 421, 360 and 591; 2560 in pairs 255 and
+// 310, 298 and 500).  In units of 16 bytes, 512 threads: 2304 channels 186 and
+// 462, 2560 191 and 463; ten values are no whole number of such units.  With 16
+// values the gradients have no registers for the next row (2050 channels in
+// pairs, float32 residual, 8188 rows: 217 us).
 template <int V, typename F>
 hipError_t with_threads(int64_t D, F f) {
     constexpr int NU = 8 / V;
@@ -374,7 +379,9 @@ hipError_t forward_typed(const pn_block_norm_args& a, hipStream_t st) {
 
 // Rows of a workgroup of the gradients: as many workgroups as run at once (12
 // waves a unit up to 2048 channels, 8 in the larger forms), or a multiple of
-// them: a lane adds the weights' gradients of at most 128 rows in float32, the
+// them (of 2049 to 2560 channels in units of 16 bytes, whose workgroup has 8
+// waves and not 4, always: the split is one of sizes alone; that form takes 462
+// us where half as many workgroups take 458, 32768 rows of 2304).  A lane adds the weights' gradients of at most 128 rows in float32, the
 // rest of the sum is column_sum's in float64.
 void backward_split(const pn_block_norm_args& a, int64_t* rows, int64_t* n_wg) {
     const int64_t n = a.B * a.T;
