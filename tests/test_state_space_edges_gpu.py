@@ -131,6 +131,27 @@ def test_scan_gates_of_the_lowest_value(dtype, N):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("N", [8, 16, 40])
+@pytest.mark.parametrize("closed", ["lowest", "infinite"])
+def test_scan_steps_closed_by_a_mask(dtype, N, closed):
+    """dt of the type's lowest value or minus infinity is a step of 0, as is that of -200: the state is kept."""
+    a = scan_inputs(dtype, 2, 70, 40, N, 1)
+    off = torch.zeros(2, 70, 40, dtype=torch.bool, device=DEV)
+    off[0, 9], off[1, :, ::3], off[1, 30:50] = True, True, True
+    results = []
+    for value in (torch.finfo(TYPES[dtype]).min if closed == "lowest" else -float("inf"), -200.0):
+        dt = torch.where(off, value, a["dt"].float()).to(TYPES[dtype])
+        kw = dict(skip=a["skip"], dt_bias=a["dt_bias"])
+        pool = a["initial_state"].clone()
+        step = pn.ssm_step(a["x"][:, 9], dt[:, 9], a["A"], a["b"][:, 9], a["c"][:, 9], pool, gate=a["gate"][:, 9], **kw)
+        assert torch.equal(pool[0], a["initial_state"][0])
+        args = (a["x"], dt, a["A"], a["b"], a["c"])
+        kw.update(gate=a["gate"], initial_state=a["initial_state"])
+        results.append(pn.ssm_scan(*args, **kw) + pn.ssm_scan_backward(a["dy"], *args, d_final_state=a["d_final_state"], **kw) + (step, pool))
+    _same(*results)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 def test_conv_biases_of_the_lowest_value(dtype):
     """Channels that their bias closes, as one of -1000 does."""
     a = conv_inputs(dtype, 2, 70, 40, 4, True)
@@ -337,3 +358,52 @@ def test_tokens_past_32_bits():
     want = pn.ssm_scan_backward(end, *args(end, end_b), dt_bias=dt_bias)
     close(got[0], want[0])
     close(got[1], want[1])
+
+
+# ---------------------------------------------------------------- captured, and where a NaN goes
+
+
+@pytest.mark.parametrize("N", [64, 128])
+def test_scan_gradients_of_many_states_are_captured(N):
+    """Workgroups of four and eight waves, whose LDS is more than a launch has by itself."""
+    a = scan_inputs("bf16", 2, 90, 40, N, 1)
+
+    def call():
+        return pn.ssm_scan_backward(a["dy"], a["x"], a["dt"], a["A"], a["b"], a["c"], skip=a["skip"], gate=a["gate"],
+                                    dt_bias=a["dt_bias"], initial_state=a["initial_state"], d_final_state=a["d_final_state"])
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for i in range(4):
+        a["dy"].mul_(-0.75)
+        graph.replay()
+        want = call()
+        torch.cuda.synchronize()
+        _same(out, want)
+
+
+@pytest.mark.parametrize("N", [4, 16, 40])
+@pytest.mark.parametrize("T", [30, 300])
+@pytest.mark.parametrize("what", ["x", "dt", "gate", "b", "c"])
+def test_scan_nans_stay_where_they_belong(N, T, what):
+    """A NaN in a token of a channel (of a group, for b and c) reaches no earlier output, no other channel and no other
+    sequence."""
+    B, D, G, at = 2, 70, 2, T // 2
+    a = scan_inputs("f32", B, T, D, N, G)
+    kw = dict(skip=a["skip"], dt_bias=a["dt_bias"])
+
+    def call():
+        return pn.ssm_scan(a["x"], a["dt"], a["A"], a["b"], a["c"], gate=a["gate"], **kw)
+
+    y, h = call()
+    a[what][1, at, 1] = float("nan")
+    bad = slice(1, 2) if what in ("x", "dt", "gate") else slice(D // G, D)
+    got, state = call()
+    reached = torch.zeros(B, T, D, dtype=torch.bool, device=DEV)
+    reached[1, at:at + 1 if what in ("gate", "c") else T, bad] = True
+    assert torch.equal(torch.isnan(got), reached) and torch.equal(torch.where(reached, 0, got), torch.where(reached, 0, y))
+    left = torch.zeros(B, D, N, dtype=torch.bool, device=DEV)
+    left[1, bad] = what not in ("gate", "c")
+    assert torch.equal(torch.isnan(state), left) and torch.equal(torch.where(left, 0, state), torch.where(left, 0, h))
